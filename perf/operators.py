@@ -1,0 +1,573 @@
+"""Cases of the operators around the routed layer: the balance loss, the norms with gate and
+residual, the gradient norm and the AdamW step, each in plain torch operations and as the
+library's calls (``own``)."""
+import math
+
+import torch
+
+own = False
+device = "cuda" if torch.cuda.is_available() else "cpu"
+
+BF16, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+TYPES = {"bf16": BF16, "f32": F32}
+BLOCK = 256          # values for each scale of an 8-bit state
+MASK32 = 0xFFFFFFFF
+
+
+# ------------------------------------------------------------------ cases
+def listed():
+    return [
+        # a few tokens of a small layer, as in a debugging run or at the end of a ragged batch: latency
+        {"name": "balance_64x8", "op": "balance", "T": 64, "E": 8, "k": 2, "S": 1, "mask": False, "add": False},
+        # the gate of a 128-expert layer over one micro-batch, added to the layer's own d_logits
+        {"name": "balance_16384x128", "op": "balance", "T": 16384, "E": 128, "k": 8, "S": 1, "mask": False, "add": True},
+        # a long packed batch: loss by sequence, padded rows masked, 256 experts
+        {"name": "balance_131071x256_seqs", "op": "balance", "T": 131071, "E": 256, "k": 8, "S": 37, "mask": True, "add": True},
+        # one new token through the norm after one block and before the next: latency
+        {"name": "norm_fwd_1x2048", "op": "norm", "dir": "fwd", "T": 1, "d": 2048, "h": "bf16", "w": "bf16", "gate": "none", "post": True, "pre": True},
+        # a training micro-batch, forward: bf16 residual stream, a gate per channel
+        {"name": "norm_fwd_16384x2048", "op": "norm", "dir": "fwd", "T": 16384, "d": 2048, "h": "bf16", "w": "bf16", "gate": "channel", "post": True, "pre": True},
+        # its backward, with the gradients of both norms' weights and of the gate
+        {"name": "norm_bwd_16384x2048", "op": "norm", "dir": "bwd", "T": 16384, "d": 2048, "h": "bf16", "w": "bf16", "gate": "channel", "post": True, "pre": True},
+        # a wide model with an fp32 residual stream and a gate per token, ragged token count, backward
+        {"name": "norm_bwd_4099x7168_f32", "op": "norm", "dir": "bwd", "T": 4099, "d": 7168, "h": "f32", "w": "f32", "gate": "token", "post": True, "pre": True},
+        # clipping: many small tensors of odd sizes (norm weights, biases)
+        {"name": "grad_norm_small", "op": "grad_norm", "tensors": 40, "elements": 100003, "g": "f32"},
+        # clipping: the gradients of the whole 128-expert layer, its gate and its two norms
+        {"name": "grad_norm_layer", "op": "grad_norm", "E": 128, "d": 2048, "f": 768, "g": "bf16"},
+        # the update of many small tensors of odd sizes: latency
+        {"name": "adamw_small", "op": "adamw", "tensors": 60, "elements": 200003, "p": "f32", "g": "f32", "state": "f32", "master": False},
+        # the update of the whole 128-expert layer: bf16 weights with fp32 master copies, fp32 states
+        {"name": "adamw_layer_f32", "op": "adamw", "E": 128, "d": 2048, "f": 768, "p": "bf16", "g": "bf16", "state": "f32", "master": True},
+        # the same with 8-bit states
+        {"name": "adamw_layer_8bit", "op": "adamw", "E": 128, "d": 2048, "f": 768, "p": "bf16", "g": "bf16", "state": "8bit", "master": True},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))))
+
+
+def draw(rng):
+    op = rng.choice(["balance", "norm", "norm", "grad_norm", "adamw", "adamw"])
+    if op == "balance":
+        E = _log_int(rng, 8, 512)
+        T = _log_int(rng, 1, min(131071, 131071 * 256 // E))
+        return {"op": op, "T": T, "E": E, "k": rng.randint(1, 8), "S": rng.choice([1, 1, rng.randint(2, 64)]),
+                "mask": rng.random() < 0.5, "add": rng.random() < 0.7}
+    if op == "norm":
+        d = 8 * _log_int(rng, 8, 1024)
+        T = _log_int(rng, 1, min(65536, 16384 * 2048 // d))
+        post = rng.random() < 0.8
+        return {"op": op, "dir": rng.choice(["fwd", "bwd"]), "T": T, "d": d, "h": rng.choice(["bf16", "f32"]),
+                "w": rng.choice(["bf16", "f32"]), "gate": rng.choice(["none", "channel", "token", "full"]) if post else "none",
+                "post": post, "pre": not post or rng.random() < 0.8}
+    tensors = _log_int(rng, 1, 200)
+    elements = _log_int(rng, 1000, 400_000_000) + tensors
+    if op == "grad_norm":
+        return {"op": op, "tensors": tensors, "elements": elements, "g": rng.choice(["bf16", "f32"])}
+    p = rng.choice(["bf16", "f32"])
+    return {"op": op, "tensors": tensors, "elements": elements, "p": p, "g": rng.choice(["bf16", "f32"]),
+            "state": rng.choice(["f32", "8bit"]), "master": p == "bf16" and rng.random() < 0.6}
+
+
+def _sizes(case):
+    """Numbers of values of the tensors: a layer's own, or a spread with odd ones among them."""
+    if "E" in case:
+        E, d, f = case["E"], case["d"], case["f"]
+        return [E * d * 2 * f, E * f * d, d * E, d, d]
+    n = case["tensors"]
+    weights = [1.0 / (1 + i) for i in range(n)]
+    total = sum(weights)
+    return [max(1, int(case["elements"] * w / total)) for w in weights]
+
+
+def _starts(sizes, step):
+    """First values of the tensors in one long buffer, each a multiple of `step`; and its length."""
+    at, got = 0, []
+    for n in sizes:
+        got.append(at)
+        at += -(-n // step) * step
+    return got, at
+
+
+# ------------------------------------------------------------------ inputs
+def _rand(shape, gen, dtype=F32, scale=1.0, shift=0.0):
+    return torch.randn(shape, generator=gen, device=device).mul_(scale).add_(shift).to(dtype)
+
+
+def _inputs(case, seed):
+    gen = torch.Generator(device=device)
+    gen.manual_seed(seed)
+    if case["op"] == "balance":
+        T, E, k, S = (case[n] for n in "TEkS")
+        # a gate that prefers some experts
+        logits = _rand((T, E), gen) + _rand((E,), gen, scale=0.5)
+        s = {"logits": logits, "ids": torch.topk(logits, k, dim=1).indices.to(torch.int32),
+             "d_losses": torch.tensor([0.01, 0.001], device=device) * (1 + torch.rand(2, generator=gen, device=device)),
+             "mask": None, "offsets": None, "d_in": None}
+        if case["mask"]:  # padding: about a sixteenth of the tokens; their logits are whatever was there
+            s["mask"] = (torch.rand(T, generator=gen, device=device) > 1 / 16).to(torch.uint8)
+            s["logits"][s["mask"] == 0] = math.nan
+        if S > 1:
+            cuts = torch.randint(0, T + 1, (S + 1,), generator=gen, device=device).sort().values
+            cuts[0] = 0
+            s["offsets"] = cuts.to(torch.int32)  # rows behind the last sequence belong to none
+        if case["add"]:
+            s["d_in"] = _rand((T, E), gen, scale=1e-3)
+        return s
+    if case["op"] == "norm":
+        T, d, ht, wt = case["T"], case["d"], TYPES[case["h"]], TYPES[case["w"]]
+        spread = torch.exp(_rand((d,), gen, scale=0.5))  # channels of unlike size, as a residual stream has them
+        s = {n: None for n in ("y", "h", "h_out", "dh_out", "dx", "w_post", "gate", "w_pre")}
+        h = (_rand((T, d), gen, scale=2.0) * spread).to(ht)
+        if case["post"]:
+            s["y"] = _rand((T, d), gen, BF16, scale=0.7)
+            s["w_post"] = _rand((d,), gen, wt, scale=0.2, shift=1.0)
+            shape = {"none": None, "channel": (d,), "token": (T,), "full": (T, d)}[case["gate"]]
+            if shape:
+                s["gate"] = _rand(shape, gen, wt, scale=0.3, shift=0.6)
+        if case["pre"]:
+            s["w_pre"] = _rand((d,), gen, wt, scale=0.2, shift=1.0)
+        if case["dir"] == "fwd":
+            s["h"] = h
+        else:
+            s["h_out"] = h if case["pre"] else None
+            s["dh_out"] = _rand((T, d), gen, ht, scale=0.1)
+            s["dx"] = _rand((T, d), gen, BF16, scale=0.1) if case["pre"] else None
+        return s
+    sizes = _sizes(case)
+    starts, total = _starts(sizes, 16)
+    s = {"sizes": sizes, "starts": starts, "g": _rand((total,), gen, TYPES[case["g"]], scale=1e-3)}
+    if case["op"] == "grad_norm":
+        return s
+    sstarts, stotal = _starts(sizes, BLOCK)
+    s.update(sstarts=sstarts, step=20, seed=seed, grad_scale=torch.rand(1, generator=gen, device=device) * 0.5 + 0.5)
+    w = _rand((total,), gen, scale=0.02)
+    s["p"] = w.to(TYPES[case["p"]])
+    s["master"] = w if case["master"] else None
+    m, r = _rand((stotal,), gen, scale=3e-4), _rand((stotal,), gen, scale=1e-3).abs_().add_(1e-5)
+    if case["state"] == "f32":
+        s["m"], s["v"] = m, r.square_()
+    else:
+        for name, x in (("m", m), ("v", r)):
+            x = x.view(-1, BLOCK)
+            scale = x.abs().amax(1) / 448
+            s[name], s[name + "_scale"] = (x / scale[:, None]).to(F8).view(-1), scale
+    return s
+
+
+def prepare(case, seed):
+    s = _inputs(case, seed)
+    s["case"] = case
+    if own:
+        _handles(case, s)
+    return s
+
+
+HYPER = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8)
+NORM = dict(eps=1e-6, res_scale=1.0, out_scale=0.5)
+MAX_NORM = 1.0
+DECAY = (0.1, 0.0)   # of every tensor but the last ones / of the last two (norm weights have none)
+
+
+def _decay(i, n):
+    return DECAY[0] if i < n - 2 else DECAY[1]
+
+
+def _handles(case, s):
+    """What a program keeps beside its inputs: output buffers, workspaces and descriptors."""
+    import grouped_gemm_expert_router_amd as moe
+
+    def new(*shape, dtype=F32):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+    def ws(n):
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+    if case["op"] == "balance":
+        T, E, k, S = (case[n] for n in "TEkS")
+        dm = moe.dims(T, 128, 128, E, k)
+        s.update(dm=dm, losses=new(2), lse=new(T), counts=new(S, E, dtype=torch.int32),
+                 tokens=new(S + 2, dtype=torch.int32), d_logits=new(T, E), ws=ws(moe.moe_balance_workspace_bytes(dm, S)))
+    elif case["op"] == "norm":
+        T, d, ht, wt = case["T"], case["d"], TYPES[case["h"]], TYPES[case["w"]]
+        kinds = {"none": moe.MOE_GATE_NONE, "channel": moe.MOE_GATE_CHANNEL, "token": moe.MOE_GATE_TOKEN, "full": moe.MOE_GATE_FULL}
+        types = {"bf16": moe.MOE_BF16, "f32": moe.MOE_F32}
+        nd = moe.norm_desc(T, d, types[case["h"]], types[case["w"]], kinds[case["gate"]], **NORM)
+        s["nd"] = nd
+        if case["dir"] == "fwd":
+            s["out"] = {"h_out": new(T, d, dtype=ht) if case["post"] else None, "x": new(T, d, dtype=BF16) if case["pre"] else None}
+        else:
+            gate = None if s["gate"] is None else new(*s["gate"].shape, dtype=wt)
+            s["out"] = {"dh": new(T, d, dtype=ht), "dy": new(T, d, dtype=BF16) if case["post"] else None,
+                        "dw_post": new(d, dtype=wt) if case["post"] else None, "dgate": gate,
+                        "dw_pre": new(d, dtype=wt) if case["pre"] else None}
+            s["ws"] = ws(moe.moe_norm_workspace_bytes(nd))
+    else:
+        n, adam = len(s["sizes"]), case["op"] == "adamw"
+        rows = []
+        for i, (size, at) in enumerate(zip(s["sizes"], s["starts"])):
+            cut = lambda name, a=at, z=size: None if s.get(name) is None else s[name][a:a + z]  # noqa: E731
+            row = {"g": cut("g")}
+            if adam:
+                a = s["sstarts"][i]
+                row.update(p=cut("p"), master=cut("master"), m=s["m"][a:a + size], v=s["v"][a:a + size], weight_decay=_decay(i, n))
+                if case["state"] == "8bit":
+                    b = slice(a // BLOCK, (a + size + BLOCK - 1) // BLOCK)
+                    row.update(m_scale=s["m_scale"][b], v_scale=s["v_scale"][b])
+            rows.append(moe.adamw_tensor(**row))
+        s["list"] = moe.adamw_tensors(rows)
+        if not adam:
+            s.update(norm=new(1), scale=new(1), ws=ws(moe.moe_grad_norm_workspace_bytes(s["list"])))
+
+
+# ------------------------------------------------------------------ one pass
+def run(s):
+    return globals()[("_own_" if own else "_plain_") + s["case"]["op"]](s)
+
+
+def _own_balance(s):
+    import grouped_gemm_expert_router_amd as moe
+    S = s["case"]["S"]
+    moe.moe_balance_forward(s["dm"], s["logits"], s["ids"], s["mask"], s["offsets"], S, s["counts"], s["tokens"], s["losses"], s["lse"], s["ws"])
+    moe.moe_balance_backward(s["dm"], s["logits"], s["lse"], s["offsets"], S, s["counts"], s["tokens"], s["d_losses"], s["d_in"], s["d_logits"])
+    return {n: s[n] for n in ("losses", "counts", "tokens", "lse", "d_logits")}
+
+
+def _own_norm(s):
+    import grouped_gemm_expert_router_amd as moe
+    o = s["out"]
+    if s["case"]["dir"] == "fwd":
+        moe.moe_norm_forward(s["nd"], s["y"], s["h"], s["w_post"], s["gate"], s["w_pre"], o["h_out"], o["x"])
+    else:
+        moe.moe_norm_backward(s["nd"], s["y"], s["h_out"], s["w_post"], s["gate"], s["w_pre"], s["dh_out"], s["dx"],
+                              o["dh"], o["dy"], o["dw_post"], o["dgate"], o["dw_pre"], s["ws"])
+    return {n: t for n, t in o.items() if t is not None}
+
+
+def _own_grad_norm(s):
+    import grouped_gemm_expert_router_amd as moe
+    moe.moe_grad_norm(s["list"], MAX_NORM, s["norm"], s["scale"], s["ws"])
+    return {"norm": s["norm"], "scale": s["scale"]}
+
+
+def _own_adamw(s):
+    import grouped_gemm_expert_router_amd as moe
+    hp = moe.adamw_hyper(step=s["step"], seed=s["seed"], stochastic=True, d_grad_scale=s["grad_scale"], **HYPER)
+    moe.moe_adamw_step(hp, s["list"])
+    s["step"] += 1
+    return {n: s[n] for n in ("p", "master", "m", "v", "m_scale", "v_scale") if s.get(n) is not None}
+
+
+def _groups(s, T, S):
+    """Each token's group, -1 for none."""
+    if s["offsets"] is None:
+        return torch.zeros(T, dtype=torch.int64, device=device)
+    t = torch.arange(T, device=device)
+    g = (t[:, None] >= s["offsets"][None, :]).sum(1) - 1
+    return torch.where(g < S, g, -1)
+
+
+def _plain_balance(s):
+    T, E, k, S = (s["case"][n] for n in "TEkS")
+    x, ids = s["logits"], s["ids"].long()
+    group = _groups(s, T, S)
+    top = x.amax(1)
+    ok = (group >= 0) & ~(top == -math.inf)
+    if s["mask"] is not None:
+        ok &= s["mask"] != 0
+    safe = torch.where(ok[:, None], x, 0.0)
+    top = torch.where(ok, top, 0.0)
+    e = torch.exp(safe - top[:, None])
+    total = e.sum(1)
+    lse = torch.log(total) + top
+    p = torch.where(ok[:, None], e / total[:, None], 0.0)
+    g = torch.where(ok, group, S)  # a last row for what counts nowhere
+    slot = torch.where((ids >= 0) & (ids < E) & ok[:, None], g[:, None] * E + ids, S * E)
+    counts = torch.bincount(slot.reshape(-1), minlength=S * E + 1)[:S * E].view(S, E)
+    if S == 1:
+        P = p.double().sum(0, keepdim=True)
+    else:  # a product with the tokens' membership, in 64 parts of the tokens that are added at the end
+        member = (torch.arange(S, device=device)[:, None] == g).double()
+        parts = [torch.nn.functional.pad(v, pad).view(shape) for v, pad, shape in
+                 ((member, (0, -T % 64), (S, 64, -1)), (p.double(), (0, 0, 0, -T % 64), (64, -1, E)))]
+        P = torch.bmm(parts[0].transpose(0, 1).contiguous(), parts[1]).sum(0)
+    n = torch.bincount(g, minlength=S + 1)[:S]
+    nd, G, N = n.double(), (n > 0).sum().double(), n.sum().double()
+    a = torch.where(n > 0, E / (k * nd.square().clamp(min=1) * G.clamp(min=1)), 0.0)
+    balance = (a * (counts * P).sum(1)).sum()
+    z = torch.where(ok, lse.double().square(), 0.0).sum() / N.clamp(min=1)
+    # gradient: the counts less their mean, which drops out since p sums to 1
+    c = (counts - torch.div(k * n, E, rounding_mode="floor")[:, None]).float()
+    c = torch.cat([c, c.new_zeros(1, E)])[g]
+    af = torch.cat([a, a.new_zeros(1)]).float()[g] * s["d_losses"][0]
+    bz = torch.where(ok, lse, 0.0) * (2 * s["d_losses"][1] / N.float().clamp(min=1))
+    d = p * (af[:, None] * (c - (c * p).sum(1, keepdim=True)) + bz[:, None])
+    if s["d_in"] is not None:
+        d = s["d_in"] + d
+    tokens = torch.cat([n, n.sum()[None], (n > 0).sum()[None]]).int()
+    return {"losses": torch.stack([balance, z]).float(), "counts": counts.int(), "tokens": tokens,
+            "lse": torch.where(ok, lse, -math.inf), "d_logits": d}
+
+
+def _f(t):
+    return None if t is None else t.float()
+
+
+def _gate(s):
+    g = _f(s["gate"])
+    return 1.0 if g is None else g[:, None] if s["case"]["gate"] == "token" else g
+
+
+def _inv_rms(v):
+    return torch.rsqrt(v.square().mean(1, keepdim=True) + NORM["eps"])
+
+
+def _plain_norm(s):
+    case, r, o = s["case"], NORM["res_scale"], NORM["out_scale"]
+    ht, wt = TYPES[case["h"]], TYPES[case["w"]]
+    out = {}
+    if case["post"]:
+        y, wq = _f(s["y"]), _f(s["w_post"])
+        sq = _inv_rms(y)
+        yh = y * sq
+    if case["dir"] == "fwd":
+        h = _f(s["h"])
+        if case["post"]:
+            h = r * h + o * _gate(s) * (wq * yh)
+            out["h_out"] = h.to(ht)
+        if case["pre"]:
+            out["x"] = (h * _inv_rms(h) * _f(s["w_pre"])).to(BF16)
+        return out
+    D = _f(s["dh_out"])
+    if case["pre"]:
+        h, dx = _f(s["h_out"]), _f(s["dx"])
+        sp = _inv_rms(h)
+        hh = h * sp
+        t = _f(s["w_pre"]) * dx
+        D = D + sp * (t - hh * (hh * t).mean(1, keepdim=True))
+        out["dw_pre"] = (dx * hh).sum(0).to(wt)
+    out["dh"] = ((r if case["post"] else 1.0) * D).to(ht)
+    if case["post"]:
+        if case["gate"] != "none":
+            dg = o * D * (wq * yh)
+            out["dgate"] = {"channel": lambda: dg.sum(0), "token": lambda: dg.sum(1), "full": lambda: dg}[case["gate"]]().to(wt)
+        dn = o * _gate(s) * D
+        out["dw_post"] = (dn * yh).sum(0).to(wt)
+        t = wq * dn
+        out["dy"] = (sq * (t - yh * (yh * t).mean(1, keepdim=True))).to(BF16)
+    return out
+
+
+def _plain_grad_norm(s):
+    total = sum(s["g"][a:a + n].double().square().sum() for a, n in zip(s["starts"], s["sizes"]))
+    norm = torch.sqrt(total)
+    return {"norm": norm.float().view(1), "scale": torch.clamp(MAX_NORM / (norm + 1e-6), max=1.0).float().view(1)}
+
+
+def _noise(seed, step, tensor, n):
+    """Two words of 32 bits for each value, from the step's seed, the tensor's place and the value's:
+    the keys by splitmix64's finaliser, the words by multiplications and shifts."""
+    M = (1 << 64) - 1
+    z = ((seed ^ (step << 32) ^ tensor) + 0x9E3779B97F4A7C15) & M
+    z = ((z ^ (z >> 30)) * 0xBF58476D1CE4E5B9) & M
+    z = ((z ^ (z >> 27)) * 0x94D049BB133111EB) & M
+    z ^= z >> 31
+    k0, k1 = z & MASK32, z >> 32
+    u = torch.arange(n, device=device) ^ k0
+    u = (u ^ (u >> 16)) * 0x9E3779B9 & MASK32
+    u = (u ^ (u >> 15) ^ k1) * 0x6A09E667 & MASK32
+    u = u ^ (u >> 16)
+    w = (u ^ k0) * 0xBB67AE85 & MASK32
+    return u, w ^ (w >> 15)
+
+
+def _codes(x, noise, keep):
+    """e4m3 codes and scales of blocks of `x`, rounded up with the probability of the remainder;
+    `keep`: what is above 0 gets a code above 0."""
+    n = x.numel()
+    b = torch.nn.functional.pad(x, (0, -n % BLOCK)).view(-1, BLOCK)
+    top = b.abs().amax(1)
+    scale = torch.where(top > 0, torch.clamp(top / 448, min=2.0 ** -126), 1.0)
+    y = (b.abs() * (1 / scale)[:, None]).view(-1)[:n].clamp(max=448.0)
+    low = y < 2.0 ** -6  # below the normal codes the steps are even: an added 2^-6 makes them those of one binade
+    bits = torch.where(low, y + 2.0 ** -6, y).view(torch.int32).long() + (noise << 4)
+    code = (bits >> 20) - torch.where(low, 968, 960)
+    if keep:
+        code = torch.where((code == 0) & (y > 0), 1, code)
+    return (code | (x < 0).long() << 7).to(torch.uint8).view(F8), scale
+
+
+def _plain_adamw(s):
+    case, n = s["case"], len(s["sizes"])
+    lr, b1, b2, eps = (HYPER[k] for k in ("lr", "beta1", "beta2", "eps"))
+    c1, c2 = 1 - b1 ** s["step"], 1 - b2 ** s["step"]
+    eight = case["state"] == "8bit"
+    for i, (size, at, sat) in enumerate(zip(s["sizes"], s["starts"], s["sstarts"])):
+        part, state = slice(at, at + size), slice(sat, sat + size)
+        blocks = slice(sat // BLOCK, (sat + size + BLOCK - 1) // BLOCK)
+        g = s["g"][part].float() * s["grad_scale"]
+        m, v = s["m"][state].float(), s["v"][state].float()
+        if eight:
+            m = m * s["m_scale"][blocks].repeat_interleave(BLOCK)[:size]
+            v = (v * s["v_scale"][blocks].repeat_interleave(BLOCK)[:size]).square()
+        m = b1 * m + (1 - b1) * g
+        v = b2 * v + (1 - b2) * g * g
+        root = torch.sqrt(v)
+        w = (s["p"] if s["master"] is None else s["master"])[part].float()
+        w = w * (1 - lr * _decay(i, n)) - (lr / c1) * m / (root / math.sqrt(c2) + eps)
+        u = None
+        if eight or (case["p"] == "bf16" and s["master"] is None):
+            u, u2 = _noise(s["seed"], s["step"], i, size)
+        if case["p"] == "bf16" and s["master"] is None:  # stochastic rounding to bf16
+            s["p"][part] = ((w.view(torch.int32).long() + (u2 & 0xFFFF)) >> 16).to(torch.int16).view(BF16)
+        else:
+            s["p"][part] = w.to(s["p"].dtype)
+            if s["master"] is not None:
+                s["master"][part] = w
+        if eight:
+            s["m"][state], s["m_scale"][blocks] = _codes(m, u & 0xFFFF, False)
+            s["v"][state], s["v_scale"][blocks] = _codes(root, u >> 16, True)
+        else:
+            s["m"][state], s["v"][state] = m, v
+    s["step"] += 1
+    return {k: s[k] for k in ("p", "master", "m", "v", "m_scale", "v_scale") if s.get(k) is not None}
+
+
+# ------------------------------------------------------------------ what a pass cannot do without
+def work(case):
+    size = {"bf16": 2, "f32": 4}
+    if case["op"] == "balance":
+        T, E, k, S = (case[n] for n in "TEkS")
+        # the logits, once for each direction (the backward needs what all tokens' forward gives); the
+        # slots, the mask, the other gradient; the gradient, lse, counts
+        b = T * E * 4 * (3 + case["add"]) + T * k * 4 + T * case["mask"] + T * 4 * 2 + S * E * 8
+        return {"bytes": b, "flops": 14 * T * E}
+    if case["op"] == "norm":
+        T, d, h, w = case["T"], case["d"], size[case["h"]], size[case["w"]]
+        gate = {"none": 0, "channel": d, "token": T, "full": T * d}[case["gate"]] * w
+        ws = d * w * (case["post"] + case["pre"]) + gate
+        if case["dir"] == "fwd":
+            return {"bytes": T * d * (h + (2 + h if case["post"] else 0) + (2 if case["pre"] else 0)) + ws,
+                    "flops": T * d * 6 * (case["post"] + case["pre"])}
+        return {"bytes": T * d * (2 * h + (4 if case["post"] else 0) + (2 + h if case["pre"] else 0)) + 2 * ws,
+                "flops": T * d * 14 * (case["post"] + case["pre"])}
+    n = sum(_sizes(case))
+    if case["op"] == "grad_norm":
+        return {"bytes": n * size[case["g"]], "flops": 2 * n}
+    weights = size[case["p"]] + 8 if case["master"] else 2 * size[case["p"]]
+    states = 16 if case["state"] == "f32" else 4 + 16 / BLOCK
+    return {"bytes": n * (size[case["g"]] + weights + states), "flops": 16 * n}
+
+
+# ------------------------------------------------------------------ 64 bits
+def exact(case, seed):
+    s = _inputs(case, seed)
+    return globals()["_exact_" + case["op"]](case, s)
+
+
+def _d(t):
+    return None if t is None else t.double()
+
+
+def _exact_balance(case, s):
+    """The losses written down from the definition; the gradient by differentiating them."""
+    T, E, k, S = (case[n] for n in "TEkS")
+    x = s["logits"].double()
+    ok = torch.ones(T, dtype=torch.bool, device=device) if s["mask"] is None else s["mask"].bool()
+    x = torch.where(ok[:, None], x, 0.0).requires_grad_()
+    lse = torch.logsumexp(x, 1)
+    p = torch.softmax(x, 1)
+    ends = [0, T] if s["offsets"] is None else s["offsets"].tolist()
+    inside = torch.zeros(T, dtype=torch.bool, device=device)
+    parts, counts, ns = [], [], []
+    for a, z in zip(ends[:-1], ends[1:]):
+        inside[a:z] = True
+        n = int(ok[a:z].sum())
+        ids = s["ids"][a:z][ok[a:z]].long().reshape(-1)
+        c = torch.bincount(ids, minlength=E)
+        counts.append(c)
+        ns.append(n)
+        if n:
+            parts.append(((c.double() / (n * k)) * p[a:z][ok[a:z]].mean(0)).sum() * E)
+    ok = ok & inside
+    zero = x.sum() * 0
+    balance = torch.stack(parts).mean() if parts else zero
+    z = lse[ok].square().mean() if sum(ns) else zero
+    w = s["d_losses"].double()
+    d, = torch.autograd.grad(w[0] * balance + w[1] * z, x)
+    if s["d_in"] is not None:
+        d = d + s["d_in"].double()
+    tokens = torch.tensor(ns + [sum(ns), sum(n > 0 for n in ns)], dtype=torch.int32, device=device)
+    return {"losses": torch.stack([balance, z]).detach(), "counts": torch.stack(counts).int(), "tokens": tokens,
+            "lse": torch.where(ok, lse.detach(), -math.inf), "d_logits": d}
+
+
+def _exact_norm(case, s):
+    """Forward from the definition; backward by differentiating it at an h that gives the h_out in hand."""
+    def rms_norm(v, w):
+        return v / torch.sqrt((v * v).sum(1, keepdim=True) / case["d"] + NORM["eps"]) * w
+
+    y, wq, g, wp = (_d(s[n]) for n in ("y", "w_post", "gate", "w_pre"))
+    if case["dir"] == "bwd":
+        for t in (y, wq, g, wp):
+            if t is not None:
+                t.requires_grad_()
+    branch = 0.0
+    if case["post"]:
+        branch = rms_norm(y, wq) * (1.0 if g is None else g[:, None] if case["gate"] == "token" else g) * NORM["out_scale"]
+    if case["dir"] == "fwd":
+        h = _d(s["h"]) * NORM["res_scale"] + branch if case["post"] else _d(s["h"])
+        return {**({"h_out": h} if case["post"] else {}), **({"x": rms_norm(h, wp)} if case["pre"] else {})}
+    h = torch.zeros_like(_d(s["dh_out"])).requires_grad_()
+    out = h * NORM["res_scale"] + branch if case["post"] else h
+    if case["pre"]:
+        out = out + (_d(s["h_out"]) - out).detach()
+    value = (out * _d(s["dh_out"])).sum()
+    if case["pre"]:
+        value = value + (rms_norm(out, wp) * _d(s["dx"])).sum()
+    names = [("dh", h)] + ([("dy", y), ("dw_post", wq)] if case["post"] else [])
+    names += [("dgate", g)] if g is not None else []
+    names += [("dw_pre", wp)] if case["pre"] else []
+    return dict(zip([n for n, _ in names], torch.autograd.grad(value, [t for _, t in names])))
+
+
+def _exact_grad_norm(case, s):
+    norm = math.sqrt(sum(float((s["g"][a:a + n].double() ** 2).sum()) for a, n in zip(s["starts"], s["sizes"])))
+    as_one = lambda v: torch.tensor([v], dtype=torch.float64)  # noqa: E731
+    return {"norm": as_one(norm), "scale": as_one(min(1.0, MAX_NORM / (norm + 1e-6)))}
+
+
+def _exact_adamw(case, s):
+    """New weights and moments by the definition; an 8-bit code is a random one of two and has no such value."""
+    n, t = len(s["sizes"]), s["step"]
+    eight, rounds = case["state"] == "8bit", case["p"] == "bf16" and not case["master"]
+    new = {k: s[k].double() for k in ("p", "master", "m", "v", "m_scale", "v_scale") if s.get(k) is not None}
+    source = new["master"] if case["master"] else new["p"]
+    for i, (size, at, sat) in enumerate(zip(s["sizes"], s["starts"], s["sstarts"])):
+        b = torch.arange(size, device=device) // BLOCK + sat // BLOCK if eight else None
+        m0 = new["m"][sat:sat + size] * (new["m_scale"][b] if eight else 1)
+        v0 = (new["v"][sat:sat + size] * new["v_scale"][b]) ** 2 if eight else new["v"][sat:sat + size]
+        g = s["g"][at:at + size].double() * s["grad_scale"].double()
+        m = m0 + (1 - HYPER["beta1"]) * (g - m0)
+        v = v0 + (1 - HYPER["beta2"]) * (g ** 2 - v0)
+        mean, var = m / (1 - HYPER["beta1"] ** t), v / (1 - HYPER["beta2"] ** t)
+        w = source[at:at + size]
+        w = w - HYPER["lr"] * (mean / (var ** 0.5 + HYPER["eps"]) + _decay(i, n) * w)
+        if not rounds:
+            new["p"][at:at + size] = w
+            if case["master"]:
+                new["master"][at:at + size] = w
+        if eight:
+            for name, x in (("m_scale", m.abs()), ("v_scale", v ** 0.5)):
+                k = -(-size // BLOCK)
+                x = torch.cat([x, x.new_zeros(k * BLOCK - size)]).view(k, BLOCK)
+                new[name][sat // BLOCK:sat // BLOCK + k] = x.max(1).values / 448
+        else:
+            new["m"][sat:sat + size], new["v"][sat:sat + size] = m, v
+    if eight:
+        new["m"] = new["v"] = None
+    if rounds:
+        new["p"] = None
+    return new
