@@ -376,8 +376,8 @@ def _noise(seed, step, tensor, n):
     z ^= z >> 31
     k0, k1 = z & MASK32, z >> 32
     u = torch.arange(n, device=device) ^ k0
-    u = (u ^ (u >> 16)) * 0x9E3779B9 & MASK32
-    u = (u ^ (u >> 15) ^ k1) * 0x6A09E667 & MASK32
+    u = (u ^ (u >> 16)) * 0x32A0CD0B & MASK32
+    u = (u ^ (u >> 14) ^ k1) * 0x2F37D463 & MASK32
     u = u ^ (u >> 16)
     w = (u ^ k0) * 0xBB67AE85 & MASK32
     return u, w ^ (w >> 15)
