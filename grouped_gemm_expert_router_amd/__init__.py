@@ -13,13 +13,18 @@ from typing import Optional
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
-MOE_BF16, MOE_FP8_E4M3, MOE_MXFP8 = 0, 1, 2
+MOE_BF16, MOE_FP8_E4M3, MOE_MXFP8, MOE_F32 = 0, 1, 2, 3
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
+MOE_STATE_F32, MOE_STATE_8BIT = 0, 1
 MOE_WS_ROUTE, MOE_WS_FORWARD, MOE_WS_BACKWARD, MOE_WS_ROUTER = 0, 1, 2, 3
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_WORKSPACE, MOE_ERR_HIP, MOE_ERR_ALIGN = 0, -1, -2, -3, -4, -5, -6
 
 ENTRY_POINTS = ("moe_workspace_bytes", "moe_saved_bytes", "moe_route", "moe_route_noalloc", "moe_plan",
                 "moe_forward", "moe_forward_fused", "moe_backward", "moe_router_logits", "moe_router_backward",
-                "moe_permute", "moe_combine", "moe_mxfp8_quantize", "moe_mxfp8_quantize_weights", "moe_set_stage_hook",
+                "moe_permute", "moe_combine", "moe_mxfp8_quantize", "moe_mxfp8_quantize_weights",
+                "moe_balance_workspace_bytes", "moe_balance_forward", "moe_balance_backward",
+                "moe_norm_workspace_bytes", "moe_norm_forward", "moe_norm_backward",
+                "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_adamw_step", "moe_set_stage_hook",
                 "moe_status_string")
 
 
@@ -29,6 +34,25 @@ class MoeDims(ctypes.Structure):
 
     def __repr__(self):
         return f"MoeDims(T={self.T}, d={self.d}, f={self.f}, E={self.E}, k={self.k}, dtype={self.dtype})"
+
+
+class MoeNormDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int64), ("h_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("reserved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("out_scale", ctypes.c_float)]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "m", "v", "m_scale", "v_scale", "master")] + [
+        ("n", ctypes.c_int64), ("p_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("state", ctypes.c_int32),
+        ("weight_decay", ctypes.c_float)]
+
+
+class MoeAdamW(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("stochastic", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("d_lr", ctypes.c_void_p), ("d_step", ctypes.c_void_p),
+        ("d_grad_scale", ctypes.c_void_p)]
 
 
 # void hook(const char* stage, int begin, void* stream, void* user)
@@ -69,6 +93,17 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_combine.argtypes = [dp, vp, vp, vp, vp]
     lib.moe_mxfp8_quantize.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, i32, vp, vp, vp]
     lib.moe_mxfp8_quantize_weights.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64] + [vp] * 5
+    i64, szp = ctypes.c_int64, ctypes.POINTER(sz)
+    np_, tp, ap = ctypes.POINTER(MoeNormDesc), ctypes.POINTER(MoeTensor), ctypes.POINTER(MoeAdamW)
+    lib.moe_balance_workspace_bytes.argtypes = [dp, i64, szp]
+    lib.moe_balance_forward.argtypes = [dp] + [vp] * 4 + [i64] + [vp] * 5 + [sz, vp]
+    lib.moe_balance_backward.argtypes = [dp] + [vp] * 3 + [i64] + [vp] * 5 + [vp]
+    lib.moe_norm_workspace_bytes.argtypes = [np_, szp]
+    lib.moe_norm_forward.argtypes = [np_] + [vp] * 7 + [vp]
+    lib.moe_norm_backward.argtypes = [np_] + [vp] * 13 + [sz, vp]
+    lib.moe_grad_norm_workspace_bytes.argtypes = [tp, i64, szp]
+    lib.moe_grad_norm.argtypes = [tp, i64, ctypes.c_float, vp, vp, vp, sz, vp]
+    lib.moe_adamw_step.argtypes = [ap, tp, i64, vp]
     lib.moe_set_stage_hook.argtypes = [STAGE_HOOK, vp]
     lib.moe_status_string.argtypes = [i32]
     lib.moe_status_string.restype = ctypes.c_char_p
@@ -197,6 +232,118 @@ def moe_mxfp8_quantize_weights(src, batch, rows, cols, col_codes, col_exps, row_
                                                      _ptr(row_codes), _ptr(row_words), _stream(stream)))
 
 
+def moe_balance_workspace_bytes(dm: MoeDims, S: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_balance_workspace_bytes",
+           load_library().moe_balance_workspace_bytes(ctypes.byref(dm), S, ctypes.byref(out)))
+    return out.value
+
+
+def moe_balance_forward(dm, logits, topk_ids, token_mask, group_offsets, S, counts, group_tokens, losses, lse, ws,
+                        ws_bytes=None, stream=None):
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check("moe_balance_forward", load_library().moe_balance_forward(
+        ctypes.byref(dm), _ptr(logits), _ptr(topk_ids), _ptr(token_mask), _ptr(group_offsets), S, _ptr(counts),
+        _ptr(group_tokens), _ptr(losses), _ptr(lse), _ptr(ws), nb, _stream(stream)))
+
+
+def moe_balance_backward(dm, logits, lse, group_offsets, S, counts, group_tokens, d_losses, d_logits_in, d_logits,
+                         stream=None):
+    _check("moe_balance_backward", load_library().moe_balance_backward(
+        ctypes.byref(dm), _ptr(logits), _ptr(lse), _ptr(group_offsets), S, _ptr(counts), _ptr(group_tokens),
+        _ptr(d_losses), _ptr(d_logits_in), _ptr(d_logits), _stream(stream)))
+
+
+def norm_desc(T: int, d: int, h_dtype: int = MOE_BF16, w_dtype: int = MOE_BF16, gate: int = MOE_GATE_NONE,
+              eps: float = 1e-6, res_scale: float = 1.0, out_scale: float = 1.0) -> MoeNormDesc:
+    return MoeNormDesc(T, d, h_dtype, w_dtype, gate, 0, eps, res_scale, out_scale)
+
+
+def moe_norm_workspace_bytes(nd: MoeNormDesc) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_norm_workspace_bytes", load_library().moe_norm_workspace_bytes(ctypes.byref(nd), ctypes.byref(out)))
+    return out.value
+
+
+def moe_norm_forward(nd, y, h, w_post, gate, w_pre, h_out, x, stream=None):
+    _check("moe_norm_forward", load_library().moe_norm_forward(
+        ctypes.byref(nd), _ptr(y), _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(h_out), _ptr(x),
+        _stream(stream)))
+
+
+def moe_norm_backward(nd, y, h_out, w_post, gate, w_pre, dh_out, dx, dh, dy, dw_post, dgate, dw_pre, ws,
+                      ws_bytes=None, stream=None):
+    nb = (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
+    _check("moe_norm_backward", load_library().moe_norm_backward(
+        ctypes.byref(nd), _ptr(y), _ptr(h_out), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(dh_out), _ptr(dx),
+        _ptr(dh), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), _ptr(ws), nb, _stream(stream)))
+
+
+class TensorList:
+    """A host array of moe_tensor and the torch tensors it points to, which it keeps alive."""
+
+    def __init__(self, rows):
+        self.rows = list(rows)
+        self.array = (MoeTensor * max(len(self.rows), 1))(*(r for r, _ in self.rows))
+
+    def __len__(self):
+        return len(self.rows)
+
+
+def adamw_tensor(g, p=None, m=None, v=None, master=None, m_scale=None, v_scale=None, weight_decay: float = 0.0):
+    """One row for adamw_tensors(): torch tensors of one parameter, its gradient and its states.  m and
+    v with scales (float8_e4m3fn or uint8) are 8-bit states.  moe_grad_norm needs g alone."""
+    import torch
+    types = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+    n = g.numel()
+    eight = m_scale is not None or v_scale is not None
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    state = codes if eight else (torch.float32,)
+    blocks = (n + 255) // 256
+    for name, t, size, allowed in (("g", g, n, types), ("p", p, n, types), ("m", m, n, state), ("v", v, n, state),
+                                   ("master", master, n, (torch.float32,)),
+                                   ("m_scale", m_scale, blocks, (torch.float32,)),
+                                   ("v_scale", v_scale, blocks, (torch.float32,))):
+        if t is None:
+            continue
+        if t.numel() != size or not t.is_contiguous() or t.dtype not in allowed or t.device != g.device:
+            raise ValueError(f"adamw_tensor: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, expected {size} "
+                             f"contiguous values on {g.device} of {sorted(map(str, allowed))}")
+    row = MoeTensor(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale), _ptr(master), n,
+                    types[p.dtype] if p is not None else MOE_F32, types[g.dtype],
+                    MOE_STATE_8BIT if eight else MOE_STATE_F32, weight_decay)
+    return row, (g, p, m, v, master, m_scale, v_scale)
+
+
+def adamw_tensors(rows) -> TensorList:
+    """The list that moe_grad_norm and moe_adamw_step take, from adamw_tensor() rows."""
+    return TensorList(rows)
+
+
+def adamw_hyper(lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8, step: int = 1, seed: int = 0,
+                stochastic: bool = False, d_lr=None, d_step=None, d_grad_scale=None) -> MoeAdamW:
+    return MoeAdamW(lr, beta1, beta2, eps, step, seed, int(stochastic), 0, _ptr(d_lr), _ptr(d_step),
+                    _ptr(d_grad_scale))
+
+
+def moe_grad_norm_workspace_bytes(tensors: TensorList) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_grad_norm_workspace_bytes",
+           load_library().moe_grad_norm_workspace_bytes(tensors.array, len(tensors), ctypes.byref(out)))
+    return out.value
+
+
+def moe_grad_norm(tensors: TensorList, max_norm, norm, scale, ws, ws_bytes=None, stream=None):
+    nb = (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
+    _check("moe_grad_norm", load_library().moe_grad_norm(tensors.array, len(tensors), max_norm, _ptr(norm),
+                                                         _ptr(scale), _ptr(ws), nb, _stream(stream)))
+
+
+def moe_adamw_step(hyper: MoeAdamW, tensors: TensorList, stream=None):
+    _check("moe_adamw_step", load_library().moe_adamw_step(ctypes.byref(hyper), tensors.array, len(tensors),
+                                                           _stream(stream)))
+
+
 _hook_ref = None
 
 
@@ -253,6 +400,11 @@ __all__ = ["MoeDims", "MoEError", "dims", "load_library", "status_string", "moe_
            "moe_router_logits",
            "moe_router_backward", "moe_permute", "moe_combine",
            "moe_mxfp8_quantize", "moe_mxfp8_quantize_weights", "moe_set_stage_hook", "alloc_layer_buffers",
+           "moe_balance_workspace_bytes", "moe_balance_forward", "moe_balance_backward", "MoeNormDesc", "norm_desc",
+           "moe_norm_workspace_bytes", "moe_norm_forward", "moe_norm_backward", "MoeTensor", "MoeAdamW", "TensorList",
+           "adamw_tensor", "adamw_tensors", "adamw_hyper", "moe_grad_norm_workspace_bytes", "moe_grad_norm",
+           "moe_adamw_step", "MOE_F32", "MOE_GATE_NONE", "MOE_GATE_CHANNEL", "MOE_GATE_TOKEN", "MOE_GATE_FULL",
+           "MOE_STATE_F32", "MOE_STATE_8BIT",
            "ENTRY_POINTS", "MOE_BF16",
            "MOE_FP8_E4M3", "MOE_MXFP8", "MOE_WS_ROUTE", "MOE_WS_FORWARD",
            "MOE_WS_BACKWARD", "MOE_WS_ROUTER", "MOE_OK", "MOE_ERR_NULL", "MOE_ERR_SHAPE", "MOE_ERR_DTYPE", "MOE_ERR_WORKSPACE",

@@ -1,5 +1,6 @@
 // C ABI (include/moe.h): host-side validation, workspace carving and stream-ordered launches.
 // Nothing here synchronises the host or reads device memory.
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -18,7 +19,10 @@ thread_local hipError_t g_last_hip = hipSuccess;
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 bool al256p(const void* p) { return ((uintptr_t)p & 255u) == 0; }
+
+bool is_elem(int32_t dtype) { return dtype == MOE_BF16 || dtype == MOE_F32; }
 
 int check_dims(const moe_dims* d) {
   if (!d) return MOE_ERR_NULL;
@@ -676,6 +680,211 @@ int moe_mxfp8_quantize_weights(const void* src, int64_t batch, int64_t rows, int
   hipStream_t st = (hipStream_t)stream;
   MOE_TRY("mx_quant", launch_mx_quant_dual((const uint16_t*)src, batch, (int)rows, (int)cols, (uint8_t*)col_codes,
                                            (uint8_t*)col_exps, (uint8_t*)row_codes, (uint8_t*)row_words, st));
+  return MOE_OK;
+}
+
+// S groups of tokens: at most one grid row each
+static int check_balance(const moe_dims* dims, int64_t S) {
+  const int rc = check_dims(dims);
+  if (rc) return rc;
+  return S < 1 || S > 65535 ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+int moe_balance_workspace_bytes(const moe_dims* dims, int64_t S, size_t* out) {
+  const int rc = check_balance(dims, S);
+  if (rc) return rc;
+  if (!out) return MOE_ERR_NULL;
+  *out = al256(balance_ws_bytes(dims->T, dims->E, S));
+  return MOE_OK;
+}
+
+int moe_balance_forward(const moe_dims* dims, const float* logits, const int32_t* topk_ids, const uint8_t* token_mask,
+                        const int32_t* group_offsets, int64_t S, int32_t* counts, int32_t* group_tokens,
+                        float* losses, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_balance(dims, S);
+  if (rc) return rc;
+  if (!counts || !group_tokens || !losses || !ws || (!group_offsets && S > 1)) return MOE_ERR_NULL;
+  if (dims->T > 0 && (!logits || !topk_ids || !lse)) return MOE_ERR_NULL;
+  if (ws_bytes < al256(balance_ws_bytes(dims->T, dims->E, S))) return MOE_ERR_WORKSPACE;
+  if (!al16(logits) || !al16(topk_ids) || !al16(counts) || !al16(lse) || !al4(group_offsets) || !al4(group_tokens) ||
+      !al4(losses) || !al256p(ws))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("balance", launch_balance_forward(logits, topk_ids, token_mask, group_offsets, (int)dims->T, (int)dims->E,
+                                            (int)dims->k, (int)S, counts, group_tokens, losses, lse, ws, st));
+  return MOE_OK;
+}
+
+int moe_balance_backward(const moe_dims* dims, const float* logits, const float* lse, const int32_t* group_offsets,
+                         int64_t S, const int32_t* counts, const int32_t* group_tokens, const float* d_losses,
+                         const float* d_logits_in, float* d_logits, void* stream) {
+  const int rc = check_balance(dims, S);
+  if (rc) return rc;
+  if (!group_offsets && S > 1) return MOE_ERR_NULL;
+  if (dims->T == 0) return MOE_OK;
+  if (!logits || !lse || !counts || !group_tokens || !d_losses || !d_logits) return MOE_ERR_NULL;
+  if (!al16(logits) || !al16(lse) || !al16(counts) || !al16(d_logits_in) || !al16(d_logits) || !al4(group_offsets) ||
+      !al4(group_tokens) || !al4(d_losses))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("balance_bwd", launch_balance_backward(logits, lse, group_offsets, counts, group_tokens, d_losses,
+                                                 (int)dims->T, (int)dims->E, (int)dims->k, (int)S, d_logits_in,
+                                                 d_logits, st));
+  return MOE_OK;
+}
+
+static int check_norm(const moe_norm_desc* d) {
+  if (!d) return MOE_ERR_NULL;
+  if (d->reserved != 0) return MOE_ERR_SHAPE;
+  if (d->T < 0 || d->T >= ((int64_t)1 << 31) || d->d < 8 || d->d % 8 || d->d > kNormMaxD) return MOE_ERR_SHAPE;
+  if (d->T * d->d >= ((int64_t)1 << 40)) return MOE_ERR_SHAPE;
+  if (!is_elem(d->h_dtype) || !is_elem(d->w_dtype)) return MOE_ERR_DTYPE;
+  if (d->gate < MOE_GATE_NONE || d->gate > MOE_GATE_FULL) return MOE_ERR_SHAPE;
+  if (!(d->eps > 0.0f) || !isfinite(d->eps) || !isfinite(d->res_scale) || !isfinite(d->out_scale)) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+static NormArgs norm_args(const moe_norm_desc* d, bool branch) {
+  NormArgs p;
+  p.T = d->T;
+  p.d = (int)d->d;
+  p.gate = d->gate;
+  p.h_f32 = d->h_dtype == MOE_F32;
+  p.w_f32 = d->w_dtype == MOE_F32;
+  p.eps = d->eps;
+  p.inv_d = 1.0f / (float)d->d;
+  p.res_scale = branch ? d->res_scale : 1.0f;
+  p.out_scale = d->out_scale;
+  return p;
+}
+
+int moe_norm_workspace_bytes(const moe_norm_desc* desc, size_t* out) {
+  const int rc = check_norm(desc);
+  if (rc) return rc;
+  if (!out) return MOE_ERR_NULL;
+  *out = al256(norm_ws_bytes(desc->T, (int)desc->d, desc->gate));
+  return MOE_OK;
+}
+
+int moe_norm_forward(const moe_norm_desc* desc, const void* y, const void* h, const void* w_post, const void* gate,
+                     const void* w_pre, void* h_out, void* x, void* stream) {
+  const int rc = check_norm(desc);
+  if (rc) return rc;
+  // nothing to do for a row, or a part of the block behind it without the block's output
+  if (!y && (w_post || gate || h_out || desc->gate != MOE_GATE_NONE)) return MOE_ERR_SHAPE;
+  if (!y && !w_pre) return MOE_ERR_NULL;
+  if ((gate != nullptr) != (desc->gate != MOE_GATE_NONE) && desc->T > 0) return MOE_ERR_NULL;
+  if (desc->T == 0) return MOE_OK;
+  if (!h || (y && !h_out) || (w_pre != nullptr) != (x != nullptr)) return MOE_ERR_NULL;
+  if (!al16(y) || !al16(h) || !al16(w_post) || !al16(gate) || !al16(w_pre) || !al16(h_out) || !al16(x))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("norm", launch_norm_forward(norm_args(desc, y != nullptr), (const uint16_t*)y, h, w_post, gate, w_pre, h_out,
+                                      (uint16_t*)x, st));
+  return MOE_OK;
+}
+
+int moe_norm_backward(const moe_norm_desc* desc, const void* y, const void* h_out, const void* w_post,
+                      const void* gate, const void* w_pre, const void* dh_out, const void* dx, void* dh, void* dy,
+                      void* dw_post, void* dgate, void* dw_pre, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_norm(desc);
+  if (rc) return rc;
+  const bool rows = desc->T > 0;
+  if (rows && !y && (w_post || gate || dy || dw_post || dgate || desc->gate != MOE_GATE_NONE)) return MOE_ERR_SHAPE;
+  if (rows && !w_pre && (h_out || dx || dw_pre)) return MOE_ERR_SHAPE;
+  if (rows && w_pre && (!h_out || !dx)) return MOE_ERR_NULL;
+  if (rows && !w_pre && !dh_out) return MOE_ERR_NULL;  // no gradient comes in
+  if (rows && !w_post && dw_post) return MOE_ERR_NULL;
+  if (rows && (gate != nullptr) != (desc->gate != MOE_GATE_NONE)) return MOE_ERR_NULL;
+  if (desc->gate == MOE_GATE_NONE && dgate) return MOE_ERR_NULL;
+  const bool sums = dw_pre || dw_post || (dgate && desc->gate == MOE_GATE_CHANNEL);
+  const size_t need = sums ? al256(norm_ws_bytes(desc->T, (int)desc->d, desc->gate)) : 0;
+  if (need > 0 && !ws) return MOE_ERR_NULL;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (!al16(y) || !al16(h_out) || !al16(w_post) || !al16(gate) || !al16(w_pre) || !al16(dh_out) || !al16(dx) ||
+      !al16(dh) || !al16(dy) || !al16(dw_post) || !al16(dgate) || !al16(dw_pre) || !al256p(ws))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("norm_bwd", launch_norm_backward(norm_args(desc, y != nullptr), (const uint16_t*)y, h_out, w_post, gate,
+                                           w_pre, dh_out, (const uint16_t*)dx, dh, (uint16_t*)dy, dw_post, dgate,
+                                           dw_pre, (float*)ws, st));
+  return MOE_OK;
+}
+
+// Host checks of a list of tensors; with `grads` only the gradients are looked at.
+static int check_tensors(const moe_tensor* t, int64_t n, bool grads) {
+  if (n < 0 || n > (1 << 20)) return MOE_ERR_SHAPE;
+  if (n > 0 && !t) return MOE_ERR_NULL;
+  int64_t total = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const moe_tensor& q = t[i];
+    if (q.n < 0 || q.n > ((int64_t)1 << 40)) return MOE_ERR_SHAPE;
+    total += q.n;
+    if (total > ((int64_t)1 << 44)) return MOE_ERR_SHAPE;
+    if (!is_elem(q.g_dtype)) return MOE_ERR_DTYPE;
+    if (q.n > 0 && !q.g) return MOE_ERR_NULL;
+    if (!al16(q.g)) return MOE_ERR_ALIGN;
+    if (grads) continue;
+    if (!is_elem(q.p_dtype) || (q.state != MOE_STATE_F32 && q.state != MOE_STATE_8BIT)) return MOE_ERR_DTYPE;
+    if (q.master && q.p_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+    if (q.state == MOE_STATE_F32 && (q.m_scale || q.v_scale)) return MOE_ERR_DTYPE;
+    if (!(q.weight_decay >= 0.0f) || !isfinite(q.weight_decay)) return MOE_ERR_SHAPE;
+    if (q.n > 0 && (!q.p || !q.m || !q.v || (q.state == MOE_STATE_8BIT && (!q.m_scale || !q.v_scale)))) return MOE_ERR_NULL;
+    if (!al16(q.p) || !al16(q.m) || !al16(q.v) || !al16(q.master) || !al4(q.m_scale) || !al4(q.v_scale))
+      return MOE_ERR_ALIGN;
+  }
+  return MOE_OK;
+}
+
+int moe_grad_norm_workspace_bytes(const moe_tensor* tensors, int64_t n_tensors, size_t* out) {
+  const int rc = check_tensors(tensors, n_tensors, true);
+  if (rc) return rc;
+  if (!out) return MOE_ERR_NULL;
+  *out = al256(grad_norm_ws_bytes(tensors, n_tensors));
+  return MOE_OK;
+}
+
+int moe_grad_norm(const moe_tensor* tensors, int64_t n_tensors, float max_norm, float* norm, float* scale, void* ws,
+                  size_t ws_bytes, void* stream) {
+  const int rc = check_tensors(tensors, n_tensors, true);
+  if (rc) return rc;
+  if (!(max_norm > 0.0f) || !isfinite(max_norm)) return MOE_ERR_SHAPE;
+  const size_t need = al256(grad_norm_ws_bytes(tensors, n_tensors));
+  if (!norm || (need > 0 && !ws)) return MOE_ERR_NULL;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (!al4(norm) || !al4(scale) || !al256p(ws)) return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("grad_norm", launch_grad_norm(tensors, n_tensors, max_norm, norm, scale, (double*)ws, st));
+  return MOE_OK;
+}
+
+int moe_adamw_step(const moe_adamw* hyper, const moe_tensor* tensors, int64_t n_tensors, void* stream) {
+  if (!hyper) return MOE_ERR_NULL;
+  const moe_adamw& h = *hyper;
+  if (h.reserved != 0 || (h.stochastic != 0 && h.stochastic != 1)) return MOE_ERR_SHAPE;
+  if (!h.d_lr && (!(h.lr >= 0.0) || !isfinite((float)h.lr))) return MOE_ERR_SHAPE;
+  // a beta that fp32 rounds to 1 would leave nothing of the gradient
+  if (!(h.beta1 >= 0.0) || !((float)h.beta1 < 1.0f) || !(h.beta2 >= 0.0) || !((float)h.beta2 < 1.0f))
+    return MOE_ERR_SHAPE;
+  if (!((float)h.eps > 0.0f) || !isfinite((float)h.eps)) return MOE_ERR_SHAPE;
+  if (!h.d_step && h.step < 1) return MOE_ERR_SHAPE;
+  const int rc = check_tensors(tensors, n_tensors, false);
+  if (rc) return rc;
+  if (!al4(h.d_lr) || ((uintptr_t)h.d_step & 7u) || !al4(h.d_grad_scale)) return MOE_ERR_ALIGN;
+  AdamScalars a;
+  memset(&a, 0, sizeof a);
+  a.b1 = (float)h.beta1, a.b2 = (float)h.beta2;
+  a.a1 = (float)(1.0 - h.beta1), a.a2 = (float)(1.0 - h.beta2);
+  a.lr = (float)h.lr, a.eps = (float)h.eps;
+  a.b1d = h.beta1, a.b2d = h.beta2;
+  a.step = (uint64_t)h.step, a.seed = h.seed, a.stochastic = h.stochastic;
+  a.d_lr = h.d_lr, a.d_step = h.d_step, a.d_grad_scale = h.d_grad_scale;
+  if (!h.d_step) {
+    a.inv_c1 = (float)(1.0 / (1.0 - pow(h.beta1, (double)h.step)));
+    a.inv_rc2 = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)h.step)));
+  }
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("adamw", launch_adamw(tensors, n_tensors, a, st));
   return MOE_OK;
 }
 

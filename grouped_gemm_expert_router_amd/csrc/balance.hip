@@ -1,0 +1,436 @@
+// Load-balancing loss of the gate: balance loss, z-loss, per-expert counts, and their gradient.
+//
+// With l = logits, a token counts if its mask is set, it lies in a group (a run of tokens: a
+// sequence, or the whole batch) and it has a logit above -inf:
+//   lse_t = log sum_e exp(l_te)        p_te = exp(l_te - lse_t)
+//   c_ge  = routed slots of g's counted tokens at expert e,   P_ge = sum of their p_te,   N_g
+//   balance = 1/G sum_{N_g > 0} E / (k N_g^2) sum_e c_ge P_ge      z = 1/N sum_t lse_t^2
+//   dl_te = p_te [ a E/(k N_g^2 G) (c_ge - sum_i c_gi p_ti) + 2 b lse_t / N ],  counts constant.
+// A router that scores the experts and keeps the top K: page "Az NVIDIA szerint tízszer gyorsabb
+// lett a dropless MoE tanítása JAX-ban", section "A dropless MoE minden tokent feldolgoz"; uneven
+// loads slow training: section "Az egyenetlen terhelés lassítja a tanítást".
+#include "common.hpp"
+#include "kernels.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalRedThreads = 1024;
+
+int balance_tile(int64_t T) {
+  const int64_t t = (T + 511) / 512;  // at most 512 tiles, whose partial sums one block per 64 columns adds
+  return t < 64 ? 64 : (int)t;
+}
+
+int64_t al256i(int64_t x) { return (x + 255) & ~(int64_t)255; }
+
+struct BalWs {
+  float* P;        // [slots][E] partial sums of p
+  int32_t* C;      // [slots][E] partial counts
+  int32_t* n;      // [slots] counted tokens
+  float* z;        // [slots] sum of lse^2
+  double* part;    // [S][chunks] balance terms
+  double* zpart;   // [S]
+  uint32_t* done;  // finished blocks of the reduction
+  int64_t bytes;
+};
+
+BalWs bal_ws(int64_t T, int64_t E, int64_t S, char* ws) {
+  const int64_t tiles = T > 0 ? (T + balance_tile(T) - 1) / balance_tile(T) : 0;
+  const int64_t slots = tiles + S, chunks = (E + 63) / 64;
+  BalWs w{};
+  int64_t off = 0;
+  w.P = (float*)(ws + off);
+  off += al256i(slots * E * 4);
+  w.C = (int32_t*)(ws + off);
+  off += al256i(slots * E * 4);
+  w.n = (int32_t*)(ws + off);
+  off += al256i(slots * 4);
+  w.z = (float*)(ws + off);
+  off += al256i(slots * 4);
+  w.part = (double*)(ws + off);
+  off += al256i(S * chunks * 8);
+  w.zpart = (double*)(ws + off);
+  off += al256i(S * 8);
+  w.done = (uint32_t*)(ws + off);
+  off += 256;
+  w.bytes = off;
+  return w;
+}
+
+// Last group whose first token is at or before t (-1: none).
+__device__ __forceinline__ int group_of(const int32_t* off, int S, int t) {
+  int lo = 0, hi = S + 1;  // off[0..S]
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= t) lo = mid + 1; else hi = mid;
+  }
+  return lo - 1;
+}
+
+// A row of E values over L lanes: lane l holds the columns (n*L + l)*V + v.
+template <int V, int L, int N>
+__device__ __forceinline__ void load_row(const float* row, int E, int l, float fill, float (&x)[V * N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * L + l) * V;
+    if (V == 4) {
+      if (c < E) {
+        const float4 q = *(const float4*)(row + c);
+        x[n * V] = q.x, x[n * V + 1] = q.y, x[n * V + 2] = q.z, x[n * V + 3] = q.w;
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[n * V + v] = fill;
+      }
+    } else {
+      x[n] = c < E ? row[c] : fill;
+    }
+  }
+}
+
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int m = L / 2; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
+  return v;
+}
+
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int m = L / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+// One block per tile of consecutive tokens, L lanes per token; each lane keeps the sums of p of
+// its own columns.  A tile is cut where a group ends; the piece of tile b in group g has the slot
+// b + g, which no other piece has (both grow along the tokens).
+template <int V, int L, int N>
+__global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
+    const int32_t* __restrict__ goff, int T, int E, int k, int S, int tile, float* __restrict__ lse_out,
+    float* __restrict__ Pp, int32_t* __restrict__ Cp, int32_t* __restrict__ np, float* __restrict__ zp,
+    uint32_t* __restrict__ done) {
+  constexpr int kRows = kBalThreads / L;
+  constexpr int kCols = V * N * L;
+  __shared__ float shP[4][kCols];
+  __shared__ int32_t hist[kCols];
+  __shared__ int32_t sh_n[4];
+  __shared__ float sh_z[4];
+  const int tid = threadIdx.x, wv = tid >> 6, l = tid % L, r = tid / L;
+  if (blockIdx.x == 0 && tid == 0) *done = 0;  // for the reduction that follows on the stream
+  const int t0 = blockIdx.x * tile, t1 = T - t0 < tile ? T : t0 + tile;
+  int g = goff ? group_of(goff, S, t0) : 0;
+  int a = t0;
+  while (a < t1) {
+    // the piece [a, z) of the tile: one group, or tokens of none (before the first, behind the last)
+    int z = t1;
+    if (goff) {
+      const int e = g < 0 ? goff[0] : (g < S ? goff[g + 1] : t1);
+      if (g < S && e < z) z = e;
+      if (z <= a) {  // an empty group
+        if (g >= S) break;
+        ++g;
+        continue;
+      }
+    }
+    const bool in = !goff || (g >= 0 && g < S);
+    for (int c = tid; c < kCols; c += kBalThreads) hist[c] = 0;
+    __syncthreads();
+    float acc[V * N];
+#pragma unroll
+    for (int i = 0; i < V * N; ++i) acc[i] = 0.0f;
+    float zs = 0.0f;
+    int cnt = 0;
+    for (int t = a + r; t < z; t += kRows) {
+      float lse = -INFINITY;
+      if (in && (!mask || mask[t] != 0)) {
+        float x[V * N];
+        load_row<V, L, N>(logits + (int64_t)t * E, E, l, -INFINITY, x);
+        float mx = x[0];
+#pragma unroll
+        for (int i = 1; i < V * N; ++i) mx = fmaxf(mx, x[i]);
+        mx = group_max<L>(mx);
+        if (mx != -INFINITY) {  // the same for the token's lanes
+          float s = 0.0f;
+#pragma unroll
+          for (int i = 0; i < V * N; ++i) {
+            x[i] = __expf(x[i] - mx);
+            s += x[i];
+          }
+          s = group_sum<L>(s);
+          const float inv = 1.0f / s;
+#pragma unroll
+          for (int i = 0; i < V * N; ++i) acc[i] += x[i] * inv;
+          lse = mx + logf(s);
+          zs += lse * lse;
+          ++cnt;
+          for (int j = l; j < k; j += L) {
+            const int e = ids[(int64_t)t * k + j];
+            if (e >= 0 && e < E) atomicAdd(&hist[e], 1);  // integers: any order gives the same
+          }
+        }
+      }
+      if (l == 0) lse_out[t] = lse;
+    }
+    if (in) {
+      // the rows of a wave, then the four waves, in fixed order
+#pragma unroll
+      for (int m = L; m < 64; m <<= 1) {
+#pragma unroll
+        for (int i = 0; i < V * N; ++i) acc[i] += __shfl_xor(acc[i], m, 64);
+        zs += __shfl_xor(zs, m, 64);
+        cnt += __shfl_xor(cnt, m, 64);
+      }
+      if ((tid & 63) < L) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int v = 0; v < V; ++v) shP[wv][(n * L + l) * V + v] = acc[n * V + v];
+        if (l == 0) sh_n[wv] = cnt, sh_z[wv] = zs;
+      }
+      __syncthreads();
+      const int64_t slot = (int64_t)blockIdx.x + g;
+      for (int c = tid; c < E; c += kBalThreads) {
+        Pp[slot * E + c] = (shP[0][c] + shP[1][c]) + (shP[2][c] + shP[3][c]);
+        Cp[slot * E + c] = hist[c];
+      }
+      if (tid == 0) {
+        np[slot] = sh_n[0] + sh_n[1] + sh_n[2] + sh_n[3];
+        zp[slot] = (sh_z[0] + sh_z[1]) + (sh_z[2] + sh_z[3]);
+      }
+    }
+    __syncthreads();
+    a = z;
+    ++g;
+  }
+}
+
+// One block per (64 columns, group): adds the pieces of the group's tiles in a fixed order (64-bit
+// sums), writes the counts, and the block that finishes last adds the groups' terms.
+__global__ __launch_bounds__(kBalRedThreads) void balance_reduce_kernel(
+    const float* __restrict__ Pp, const int32_t* __restrict__ Cp, const int32_t* __restrict__ np,
+    const float* __restrict__ zp, const int32_t* __restrict__ goff, int T, int E, int k, int S, int tile,
+    int32_t* __restrict__ counts, int32_t* __restrict__ tokens, float* __restrict__ losses, double* part,
+    double* zpart, uint32_t* done) {
+  constexpr int kW = kBalRedThreads / 64;
+  __shared__ double shP[kW][64];
+  __shared__ int32_t shC[kW][64];
+  __shared__ int32_t sh_n[kW];
+  __shared__ double sh_z[kW];
+  __shared__ bool last;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int g = blockIdx.y, c = blockIdx.x * 64 + lane, chunks = gridDim.x;
+  int a = 0, z = T;
+  if (goff) {
+    a = goff[g] < 0 ? 0 : goff[g];
+    z = goff[g + 1] > T ? T : goff[g + 1];
+  }
+  const int b0 = z > a ? a / tile : 0, b1 = z > a ? (z - 1) / tile + 1 : 0;
+  double P = 0.0;
+  int32_t C = 0;
+#pragma unroll 4
+  for (int b = b0 + wv; b < b1; b += kW) {
+    const int64_t slot = (int64_t)b + g;
+    if (c < E) {
+      P += (double)Pp[slot * E + c];
+      C += Cp[slot * E + c];
+    }
+  }
+  int32_t n = 0;
+  double zs = 0.0;
+  for (int b = b0 + tid; b < b1; b += kBalRedThreads) {
+    n += np[b + g];
+    zs += (double)zp[b + g];
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    n += __shfl_xor(n, m, 64);
+    zs += __shfl_xor(zs, m, 64);
+  }
+  shP[wv][lane] = P;
+  shC[wv][lane] = C;
+  if (lane == 0) sh_n[wv] = n, sh_z[wv] = zs;
+  __syncthreads();
+  if (wv == 0) {
+    n = 0;
+    zs = 0.0;
+#pragma unroll
+    for (int w = 1; w < kW; ++w) P += shP[w][lane], C += shC[w][lane];
+#pragma unroll
+    for (int w = 0; w < kW; ++w) n += sh_n[w], zs += sh_z[w];
+    if (c < E) counts[(int64_t)g * E + c] = C;
+    double dot = c < E ? (double)C * P : 0.0;
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) dot += __shfl_xor(dot, m, 64);
+    if (lane == 0) {
+      part[(int64_t)g * chunks + blockIdx.x] = n > 0 ? dot * (double)E / ((double)k * (double)n * (double)n) : 0.0;
+      if (blockIdx.x == 0) tokens[g] = n, zpart[g] = zs;
+      __threadfence();
+      last = atomicAdd(done, 1u) == (uint32_t)(gridDim.x * gridDim.y) - 1u;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  // every block's values are in memory; added in a fixed order whichever block this is
+  double bal = 0.0;
+  int32_t groups = 0, total = 0;
+  zs = 0.0;
+  for (int64_t i = tid; i < (int64_t)S * chunks; i += kBalRedThreads) bal += ((volatile double*)part)[i];
+  for (int i = tid; i < S; i += kBalRedThreads) {
+    const int32_t m = ((volatile int32_t*)tokens)[i];
+    total += m;
+    groups += m > 0;
+    zs += ((volatile double*)zpart)[i];
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    bal += __shfl_xor(bal, m, 64);
+    zs += __shfl_xor(zs, m, 64);
+    total += __shfl_xor(total, m, 64);
+    groups += __shfl_xor(groups, m, 64);
+  }
+  __syncthreads();
+  if (lane == 0) shP[wv][0] = bal, shP[wv][1] = zs, shC[wv][0] = total, shC[wv][1] = groups;
+  __syncthreads();
+  if (tid == 0) {
+    bal = 0.0, zs = 0.0, total = 0, groups = 0;
+    for (int w = 0; w < kW; ++w) bal += shP[w][0], zs += shP[w][1], total += shC[w][0], groups += shC[w][1];
+    losses[0] = groups > 0 ? (float)(bal / groups) : 0.0f;
+    losses[1] = total > 0 ? (float)(zs / total) : 0.0f;
+    tokens[S] = total;
+    tokens[S + 1] = groups;
+  }
+}
+
+// The gradient: L lanes per token.  Since sum_e p = 1, an integer near their mean is taken off the
+// counts first, which loses nothing and keeps the difference from cancelling.
+template <int V, int L, int N>
+__global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
+    const float* __restrict__ logits, const float* __restrict__ lse_in, const int32_t* __restrict__ goff,
+    const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens, const float* __restrict__ d_losses, int T,
+    int E, int k, int S, int tile, const float* d_in, float* d_out) {
+  constexpr int kRows = kBalThreads / L;
+  const int tid = threadIdx.x, l = tid % L, r = tid / L;
+  const int t0 = blockIdx.x * tile, t1 = T - t0 < tile ? T : t0 + tile;
+  int g = -1, lo = 0, hi = -1;  // no group yet
+  float c[V * N];
+#pragma unroll
+  for (int i = 0; i < V * N; ++i) c[i] = 0.0f;
+  float ca = 0.0f;
+  const int32_t total = tokens[S];
+  const float cb = total > 0 ? 2.0f * d_losses[1] / (float)total : 0.0f;
+  for (int t = t0 + r; t < t1; t += kRows) {
+    const int64_t row = (int64_t)t * E;
+    float d[V * N];
+    if (d_in) {
+      load_row<V, L, N>(d_in + row, E, l, 0.0f, d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V * N; ++i) d[i] = 0.0f;
+    }
+    const float lse = lse_in[t];
+    if (lse != -INFINITY) {
+      if (t < lo || t >= hi) {
+        g = goff ? group_of(goff, S, t) : 0;
+        g = g < 0 ? 0 : (g >= S ? S - 1 : g);  // a counted token lies in a group
+        lo = goff ? goff[g] : 0;
+        hi = goff ? goff[g + 1] : T;
+        const int32_t n = tokens[g];
+        const int32_t mean = (int32_t)((int64_t)k * n / E);
+        const int32_t* cg = counts + (int64_t)g * E;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const int col = (i * L + l) * V + v;
+            c[i * V + v] = col < E ? (float)(cg[col] - mean) : 0.0f;
+          }
+        ca = n > 0 ? (float)((double)d_losses[0] * (double)E / ((double)k * n * (double)n * (double)tokens[S + 1])) : 0.0f;
+      }
+      float p[V * N];
+      load_row<V, L, N>(logits + row, E, l, -INFINITY, p);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V * N; ++i) {
+        p[i] = __expf(p[i] - lse);
+        dot += c[i] * p[i];
+      }
+      dot = group_sum<L>(dot);
+      const float zc = cb * lse;
+#pragma unroll
+      for (int i = 0; i < V * N; ++i) d[i] += p[i] * (ca * (c[i] - dot) + zc);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int col = (n * L + l) * V;
+      if (col >= E) continue;
+      if (V == 4)
+        *(float4*)(d_out + row + col) = make_float4(d[n * V], d[n * V + 1], d[n * V + 2], d[n * V + 3]);
+      else
+        d_out[row + col] = d[n];
+    }
+  }
+}
+
+// The smallest group of lanes that holds a row in few registers; rows of a multiple of 4 columns
+// are 16-byte aligned and move as vectors.
+#define MOE_BAL_DISPATCH(E, CALL)                              \
+  do {                                                         \
+    if ((E) % 4 == 0) {                                        \
+      if ((E) <= 32) { CALL(4, 8, 1); }                        \
+      else if ((E) <= 64) { CALL(4, 16, 1); }                  \
+      else if ((E) <= 128) { CALL(4, 32, 1); }                 \
+      else if ((E) <= 256) { CALL(4, 64, 1); }                 \
+      else if ((E) <= 512) { CALL(4, 64, 2); }                 \
+      else { CALL(4, 64, 4); }                                 \
+    } else {                                                   \
+      if ((E) <= 64) { CALL(1, 64, 1); }                       \
+      else if ((E) <= 128) { CALL(1, 64, 2); }                 \
+      else if ((E) <= 256) { CALL(1, 64, 4); }                 \
+      else if ((E) <= 512) { CALL(1, 64, 8); }                 \
+      else { CALL(1, 64, 16); }                                \
+    }                                                          \
+  } while (0)
+
+}  // namespace
+
+size_t balance_ws_bytes(int64_t T, int64_t E, int64_t S) { return (size_t)bal_ws(T, E, S, nullptr).bytes; }
+
+hipError_t launch_balance_forward(const float* logits, const int32_t* ids, const uint8_t* mask, const int32_t* goff,
+                                  int T, int E, int k, int S, int32_t* counts, int32_t* tokens, float* losses,
+                                  float* lse, void* ws, hipStream_t st) {
+  const BalWs w = bal_ws(T, E, S, (char*)ws);
+  const int tile = balance_tile(T);
+  // an empty batch still runs one block, which sets the counter of the reduction
+  const unsigned tiles = T > 0 ? (unsigned)((T + tile - 1) / tile) : 1u;
+#define MOE_BAL_CALL(V, L, N)                                                                                       \
+  balance_stats_kernel<V, L, N><<<tiles, kBalThreads, 0, st>>>(logits, ids, mask, goff, T, E, k, S, tile, lse, w.P, \
+                                                               w.C, w.n, w.z, w.done)
+  MOE_BAL_DISPATCH(E, MOE_BAL_CALL);
+#undef MOE_BAL_CALL
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  balance_reduce_kernel<<<dim3((E + 63) / 64, S), kBalRedThreads, 0, st>>>(
+      w.P, w.C, w.n, w.z, goff, T, E, k, S, tile, counts, tokens, losses, w.part, w.zpart, w.done);
+  return hipGetLastError();
+}
+
+hipError_t launch_balance_backward(const float* logits, const float* lse, const int32_t* goff, const int32_t* counts,
+                                   const int32_t* tokens, const float* d_losses, int T, int E, int k, int S,
+                                   const float* d_in, float* d_out, hipStream_t st) {
+  if (T == 0) return hipSuccess;
+  const int tile = 64;
+  const unsigned tiles = (unsigned)((T + (int64_t)tile - 1) / tile);
+#define MOE_BAL_CALL(V, L, N)                                                                                       \
+  balance_grad_kernel<V, L, N><<<tiles, kBalThreads, 0, st>>>(logits, lse, goff, counts, tokens, d_losses, T, E, k, \
+                                                              S, tile, d_in, d_out)
+  MOE_BAL_DISPATCH(E, MOE_BAL_CALL);
+#undef MOE_BAL_CALL
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/moe.h"
+
 namespace moe {
 
 // routing and plan
@@ -165,5 +167,46 @@ hipError_t launch_combine(const uint16_t* op, const int32_t* inv_perm, int T, in
                           hipStream_t st);
 hipError_t launch_dlogits(const float* dwp, int nparts, const int32_t* inv_perm, const int32_t* ids,
                           const float* topk_w, int T, int E, int k, float* d_topk_w, float* d_logits, hipStream_t st);
+
+// balance loss of the gate (S groups of tokens; goff NULL: one group of all T)
+size_t balance_ws_bytes(int64_t T, int64_t E, int64_t S);
+hipError_t launch_balance_forward(const float* logits, const int32_t* ids, const uint8_t* mask, const int32_t* goff,
+                                  int T, int E, int k, int S, int32_t* counts, int32_t* tokens, float* losses,
+                                  float* lse, void* ws, hipStream_t st);
+hipError_t launch_balance_backward(const float* logits, const float* lse, const int32_t* goff, const int32_t* counts,
+                                   const int32_t* tokens, const float* d_losses, int T, int E, int k, int S,
+                                   const float* d_in, float* d_out, hipStream_t st);
+
+// norms before and after a block: rows of d values (a multiple of 8, at most kNormMaxD)
+constexpr int kNormMaxD = 16384;
+struct NormArgs {
+  int64_t T;
+  int d, gate;  // gate: as moe_gate
+  bool h_f32, w_f32;
+  float eps, inv_d, res_scale, out_scale;
+};
+size_t norm_ws_bytes(int64_t T, int d, int gate);
+hipError_t launch_norm_forward(const NormArgs& p, const uint16_t* y, const void* h, const void* w_post,
+                               const void* gate, const void* w_pre, void* h_out, uint16_t* x, hipStream_t st);
+hipError_t launch_norm_backward(const NormArgs& p, const uint16_t* y, const void* h_out, const void* w_post,
+                                const void* gate, const void* w_pre, const void* dh_out, const uint16_t* dx, void* dh,
+                                uint16_t* dy, void* dw_post, void* dgate, void* dw_pre, float* part, hipStream_t st);
+
+// gradient norm and AdamW over a list of tensors, kAdamBatch of them in a launch's arguments
+constexpr int kAdamBatch = 48;
+struct AdamScalars {
+  float b1, b2, a1, a2, lr, eps, inv_c1, inv_rc2;  // a = 1 - b; 1 / (1 - b1^step), 1 / sqrt(1 - b2^step)
+  double b1d, b2d;
+  uint64_t step, seed;
+  int64_t first_tensor;
+  const float* d_lr;
+  const int64_t* d_step;
+  const float* d_grad_scale;
+  int32_t stochastic;
+};
+hipError_t launch_adamw(const moe_tensor* t, int64_t n, const AdamScalars& hp, hipStream_t st);
+size_t grad_norm_ws_bytes(const moe_tensor* t, int64_t n);
+hipError_t launch_grad_norm(const moe_tensor* t, int64_t n, float max_norm, float* norm, float* scale, double* part,
+                            hipStream_t st);
 
 }  // namespace moe

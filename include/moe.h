@@ -70,7 +70,7 @@
 extern "C" {
 #endif
 
-typedef enum { MOE_BF16 = 0, MOE_FP8_E4M3 = 1, MOE_MXFP8 = 2 } moe_dtype;
+typedef enum { MOE_BF16 = 0, MOE_FP8_E4M3 = 1, MOE_MXFP8 = 2, MOE_F32 = 3 } moe_dtype;
 
 typedef struct {
   int64_t T, d, f, E, k;
@@ -216,6 +216,143 @@ int moe_permute(const moe_dims* dims, const void* x, const int32_t* inv_perm, vo
  * tanítást").  op is bf16 [T*k, d] in pair (slot) order. */
 int moe_combine(const moe_dims* dims, const void* op, const int32_t* inv_perm, void* y,
                 void* stream);
+
+/* Load-balancing loss of the gate, with per-expert counts ([JAX] "Az egyenetlen terhelés lassítja a
+ * tanítást" [uneven load slows training]).  The tokens come in S groups (sequences, or one group
+ * for the whole batch): group g holds tokens group_offsets[g] .. group_offsets[g+1]-1 (int32
+ * [S+1], never decreasing, within [0, T]; NULL with S = 1: all T tokens); tokens before the first
+ * or behind the last group belong to none.  A token counts if it lies in a group, its token_mask
+ * byte is not 0 (uint8 [T]; NULL: every token) and it has a logit above -inf.  With
+ * p = softmax(logits) over all E, over the counted tokens:
+ *   counts[g, e] = slots of g's tokens with topk_ids = e,  P[g, e] = sum of p[t, e],  N_g = tokens
+ *   losses[0] = 1/G sum_{g: N_g > 0} E / (k N_g^2) sum_e counts[g, e] P[g, e],  G = such groups
+ *   losses[1] = 1/N sum_t lse_t^2,  lse_t = log sum_e exp(logits[t, e]),  N = sum_g N_g
+ * (both 0 when nothing counts).  losses[0] is 1 for an even load, losses[1] the router's z-loss.
+ * Outputs: counts int32 [S, E]; group_tokens int32 [S+2]: N_g, then N, then G; losses fp32 [2];
+ * lse fp32 [T], -inf for a token that does not count.  Nothing is read of the logits and ids of a
+ * token that is masked or lies in no group.  A logit of -inf is an expert that cannot be chosen (p = 0);
+ * NaN or +inf in a counted token makes the losses NaN.  Sums run in a fixed order (bitwise
+ * reproducible), across tokens in 64 bits.  dims: T, E and k are used.  S: 1 .. 65535
+ * (MOE_ERR_SHAPE).  ws: moe_balance_workspace_bytes.  logits, topk_ids, counts and lse 16-byte
+ * aligned, the other arrays to their type. */
+int moe_balance_workspace_bytes(const moe_dims* dims, int64_t S, size_t* out);
+int moe_balance_forward(const moe_dims* dims, const float* logits, const int32_t* topk_ids,
+                        const uint8_t* token_mask, const int32_t* group_offsets, int64_t S, int32_t* counts,
+                        int32_t* group_tokens, float* losses, float* lse, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Gradient of d_losses[0] * losses[0] + d_losses[1] * losses[1] (d_losses: fp32 [2] on the device)
+ * with respect to the logits, added to d_logits_in (fp32 [T, E]; NULL: zeros) and written to
+ * d_logits, which may be d_logits_in itself (pass moe_backward's d_logits as both):
+ *   d_logits = d_logits_in + p (d_losses[0] E / (k N_g^2 G) (counts[g, e] - sum_i counts[g, i] p_i)
+ *                               + 2 d_losses[1] lse / N)
+ * The counts carry no gradient.  Rows of tokens that do not count are those of d_logits_in.
+ * logits, topk routing and groups as in the forward call, with its lse, counts and group_tokens
+ * (counts and group_tokens may have been summed over other GPUs' tokens in between, for the loss of
+ * the joint batch: N_g, N and the counts summed, G the number of joint groups). */
+int moe_balance_backward(const moe_dims* dims, const float* logits, const float* lse,
+                         const int32_t* group_offsets, int64_t S, const int32_t* counts,
+                         const int32_t* group_tokens, const float* d_losses, const float* d_logits_in,
+                         float* d_logits, void* stream);
+
+/* RMS norms before and after a block, fused with the block's gate and the scaled residual ([TE]: the
+ * expert layer is the feed-forward part of a transformer block).  For each of T rows of d values,
+ * with rms(v) = sqrt(mean(v^2) + eps):
+ *   n     = w_post * y / rms(y)                     (n = y when w_post is NULL)
+ *   h_out = res_scale * h + out_scale * gate * n    (gate 1 for MOE_GATE_NONE)
+ *   x     = w_pre * h_out / rms(h_out)
+ * h: the residual stream before the block, y: the block's output (bf16, moe_forward's y), h_out: the
+ * stream behind it, x: the next block's input (bf16).  Without y (NULL, with h_out, w_post and gate
+ * NULL too) only the norm before a block is taken: x = w_pre * h / rms(h).  Without w_pre and x
+ * (both NULL) only the part behind the block.  x comes from h_out before its rounding.  h_out may be
+ * h itself; otherwise outputs overlap no input.  Sums and statistics are fp32, each output is
+ * rounded once. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate;
+
+typedef struct {
+  int64_t T, d;        /* rows, values in a row: a multiple of 8, 8 .. 16384; T*d < 2^40, T < 2^31 */
+  int32_t h_dtype;     /* MOE_BF16 or MOE_F32: h, h_out, dh_out, dh */
+  int32_t w_dtype;     /* MOE_BF16 or MOE_F32: w_post, w_pre, gate and their gradients */
+  int32_t gate;        /* moe_gate: NONE, CHANNEL [d], TOKEN [T], FULL [T, d] */
+  int32_t reserved;    /* must be 0 */
+  float eps;           /* > 0 and finite */
+  float res_scale, out_scale; /* finite; used when y is given */
+} moe_norm_desc;
+
+int moe_norm_workspace_bytes(const moe_norm_desc* desc, size_t* out);
+int moe_norm_forward(const moe_norm_desc* desc, const void* y, const void* h, const void* w_post,
+                     const void* gate, const void* w_pre, void* h_out, void* x, void* stream);
+
+/* Backward of moe_norm_forward.  dh_out: gradient of h_out from its other uses (the residual stream
+ * above; NULL: zeros), dx: gradient of x (bf16, moe_backward's dx), h_out as the forward wrote it
+ * (h itself when there was no y).  With D the whole gradient of h_out:
+ *   dh = res_scale * D (D when there is no y)    dy = out_scale * gate * D through the norm of y
+ *   dw_pre, dw_post [d], dgate (the gate's shape): summed over what the weight or gate is shared by
+ * Any output may be NULL (not wanted).  dh may be dh_out itself; otherwise outputs overlap no input.
+ * The sums over tokens are fp32 in a fixed order (bitwise reproducible).  h_out and dx go with w_pre: all three or
+ * none (MOE_ERR_NULL; MOE_ERR_SHAPE if dx or h_out come without w_pre).  T = 0 writes zeros to
+ * dw_pre, dw_post and a channel gate's dgate.  ws: moe_norm_workspace_bytes. */
+int moe_norm_backward(const moe_norm_desc* desc, const void* y, const void* h_out, const void* w_post,
+                      const void* gate, const void* w_pre, const void* dh_out, const void* dx, void* dh,
+                      void* dy, void* dw_post, void* dgate, void* dw_pre, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* One tensor of the lists below: n values, contiguous.  p: the parameter (p_dtype), g its gradient
+ * (g_dtype), each MOE_BF16 or MOE_F32.  master: an fp32 copy of a bf16 parameter that the update runs
+ * on (p is then its rounding), or NULL.  state = MOE_STATE_F32: m and v fp32 [n], scales NULL.
+ * state = MOE_STATE_8BIT: m and v hold e4m3 codes [n] of m and of sqrt(v) (never negative), with one fp32 scale for each
+ * 256 values (m_scale, v_scale: [(n + 255) / 256]; value = code * scale, scale = the block's largest
+ * magnitude / 448, or 1 for a block of zeros).  All bytes 0 is the state before the first step.
+ * ([TE] "צמצום הזיכרון ותקורות הכימות" [reducing memory and quantisation overheads]) */
+typedef enum { MOE_STATE_F32 = 0, MOE_STATE_8BIT = 1 } moe_state;
+
+typedef struct {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float* master;
+  int64_t n;              /* 0 .. 2^40 */
+  int32_t p_dtype, g_dtype, state;
+  float weight_decay;     /* >= 0 and finite */
+} moe_tensor;
+
+/* L2 norm of the gradients of n_tensors tensors together (g, n and g_dtype are read; the other
+ * members may be NULL), norm = sqrt(sum g^2) (fp32 [1] on the device, sums in 64 bits in a fixed
+ * order), and the factor that clips it, scale = min(1, max_norm / (norm + 1e-6)) (fp32 [1], or NULL
+ * if not wanted), NaN when the norm is not finite.  The scale is what moe_adamw_step takes as
+ * d_grad_scale.  `tensors` is a host array.  ws: moe_grad_norm_workspace_bytes. */
+int moe_grad_norm_workspace_bytes(const moe_tensor* tensors, int64_t n_tensors, size_t* out);
+int moe_grad_norm(const moe_tensor* tensors, int64_t n_tensors, float max_norm, float* norm, float* scale,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/* One AdamW step on n_tensors tensors (a host array; one launch for each 48 of them):
+ *   g' = s g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   w  = (1 - lr weight_decay) w - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32 on the master copy where there is one, else on p.  s = *d_grad_scale, or 1.  If
+ * *d_grad_scale is not finite the whole step is skipped: nothing changes.  8-bit states are
+ * rounded stochastically (a code up with the probability of the remainder; a nonzero sqrt(v) never
+ * becomes zero), and so is a bf16 parameter without a master copy if `stochastic` is 1 (to nearest
+ * if 0); the random bits are a function of seed, step, the tensor's place in the list and the
+ * value's index, so a step is bitwise reproducible.  lr and step may live on the device (d_lr,
+ * d_step) for a captured graph whose replays move on; they are read when the step runs.  The
+ * tensors overlap nowhere. */
+typedef struct {
+  double lr;              /* >= 0 and finite; unused with d_lr */
+  double beta1, beta2;    /* in [0, 1) */
+  double eps;             /* > 0 and finite (in fp32 too) */
+  int64_t step;           /* 1 for the first step; unused with d_step */
+  uint64_t seed;
+  int32_t stochastic;     /* 0 or 1 */
+  int32_t reserved;       /* must be 0 */
+  const float* d_lr;          /* fp32 [1] or NULL */
+  const int64_t* d_step;      /* int64 [1] (at least 1) or NULL */
+  const float* d_grad_scale;  /* fp32 [1] or NULL */
+} moe_adamw;
+
+int moe_adamw_step(const moe_adamw* hyper, const moe_tensor* tensors, int64_t n_tensors, void* stream);
 
 /* Optional profiling hook (process-wide; none by default).  When set, each call invokes
  * hook(stage, 1, stream, user) on the calling thread right before it enqueues a stage's kernel

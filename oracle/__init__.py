@@ -13,8 +13,9 @@ from .formats import (bf16_to_f64, e4m3_to_f64, dequant_rows_1x128, dequant_bloc
 from .moe_ref import (route, plan, Plan, forward, backward, token_forward, token_backward,
                       weight_grad_entries, expert_weight_grads, d_logits_from_dw, router_logits,
                       router_backward)
+from . import block_ref
 
-__all__ = ["bf16_to_f64", "e4m3_to_f64", "dequant_rows_1x128", "dequant_blocks_128x128", "e8m0_to_f64",
+__all__ = ["block_ref", "bf16_to_f64", "e4m3_to_f64", "dequant_rows_1x128", "dequant_blocks_128x128", "e8m0_to_f64",
            "e4m3_encode_rne", "mx_block_exponent", "mx_quantize", "mx_dequantize", "mx_roundtrip_rows", "route",
            "plan", "Plan", "forward", "backward", "token_forward", "token_backward",
            "weight_grad_entries", "expert_weight_grads", "d_logits_from_dw", "router_logits", "router_backward"]
