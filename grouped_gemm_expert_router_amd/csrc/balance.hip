@@ -33,7 +33,6 @@ struct BalWs {
   float* z;        // [slots] sum of lse^2
   double* part;    // [S][chunks] balance terms
   double* zpart;   // [S]
-  uint32_t* done;  // finished blocks of the reduction
   int64_t bytes;
 };
 
@@ -54,10 +53,17 @@ BalWs bal_ws(int64_t T, int64_t E, int64_t S, char* ws) {
   off += al256i(S * chunks * 8);
   w.zpart = (double*)(ws + off);
   off += al256i(S * 8);
-  w.done = (uint32_t*)(ws + off);
-  off += 256;
   w.bytes = off;
   return w;
+}
+
+// Columns of 64 a block of the reduction takes: all of them while its 16 waves then read few rows each
+// (one block, and no launch for the losses, if there is one group), else one.
+int balance_wide(int64_t T, int64_t E, int64_t S) {
+  const int64_t rows = T > 0 ? (T + balance_tile(T) - 1) / balance_tile(T) / S + 1 : 1;
+  int w = 1;
+  while (w * 64 < E) w *= 2;
+  return rows * w <= 512 ? w : 1;
 }
 
 // Last group whose first token is at or before t (-1: none).
@@ -70,57 +76,40 @@ __device__ __forceinline__ int group_of(const int32_t* off, int S, int t) {
   return lo - 1;
 }
 
-// A row of E values over L lanes: lane l holds the columns (n*L + l)*V + v.
-template <int V, int L, int N>
+constexpr int kL = 16;                      // lanes a token: a DPP row, so its sums need no LDS
+constexpr int kRows = kBalThreads / kL;     // tokens a block takes at a time
+
+// A row of E values over kL lanes: lane l holds the columns (n*kL + l)*V + v.
+template <int V, int N>
 __device__ __forceinline__ void load_row(const float* row, int E, int l, float fill, float (&x)[V * N]) {
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const int c = (n * L + l) * V;
+    const int c = (n * kL + l) * V;
     if (V == 4) {
-      if (c < E) {
-        const float4 q = *(const float4*)(row + c);
-        x[n * V] = q.x, x[n * V + 1] = q.y, x[n * V + 2] = q.z, x[n * V + 3] = q.w;
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[n * V + v] = fill;
-      }
+      float4 q = make_float4(fill, fill, fill, fill);
+      if (c < E) q = *(const float4*)(row + c);
+      x[n * V] = q.x, x[n * V + 1] = q.y, x[n * V + 2] = q.z, x[n * V + 3] = q.w;
     } else {
       x[n] = c < E ? row[c] : fill;
     }
   }
 }
 
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int m = L / 2; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
-  return v;
-}
-
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int m = L / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
-}
-
-// One block per tile of consecutive tokens, L lanes per token; each lane keeps the sums of p of
-// its own columns.  A tile is cut where a group ends; the piece of tile b in group g has the slot
-// b + g, which no other piece has (both grow along the tokens).
-template <int V, int L, int N>
+// One block per tile of consecutive tokens, kL lanes per token, U tokens of a lane group in flight;
+// each lane keeps the sums of p of its own columns.  A tile is cut where a group ends; the piece of
+// tile b in group g has the slot b + g, which no other piece has (both grow along the tokens).
+template <int V, int N>
 __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
     const int32_t* __restrict__ goff, int T, int E, int k, int S, int tile, float* __restrict__ lse_out,
-    float* __restrict__ Pp, int32_t* __restrict__ Cp, int32_t* __restrict__ np, float* __restrict__ zp,
-    uint32_t* __restrict__ done) {
-  constexpr int kRows = kBalThreads / L;
-  constexpr int kCols = V * N * L;
+    float* __restrict__ Pp, int32_t* __restrict__ Cp, int32_t* __restrict__ np, float* __restrict__ zp) {
+  constexpr int kCols = V * N * kL;
+  constexpr int U = V * N <= 16 ? 2 : 1;
   __shared__ float shP[4][kCols];
   __shared__ int32_t hist[kCols];
   __shared__ int32_t sh_n[4];
   __shared__ float sh_z[4];
-  const int tid = threadIdx.x, wv = tid >> 6, l = tid % L, r = tid / L;
-  if (blockIdx.x == 0 && tid == 0) *done = 0;  // for the reduction that follows on the stream
+  const int tid = threadIdx.x, wv = tid >> 6, l = tid % kL, r = tid / kL;
   const int t0 = blockIdx.x * tile, t1 = T - t0 < tile ? T : t0 + tile;
   int g = goff ? group_of(goff, S, t0) : 0;
   int a = t0;
@@ -144,51 +133,68 @@ __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
     for (int i = 0; i < V * N; ++i) acc[i] = 0.0f;
     float zs = 0.0f;
     int cnt = 0;
-    for (int t = a + r; t < z; t += kRows) {
-      float lse = -INFINITY;
-      if (in && (!mask || mask[t] != 0)) {
-        float x[V * N];
-        load_row<V, L, N>(logits + (int64_t)t * E, E, l, -INFINITY, x);
-        float mx = x[0];
+    for (int tb = a + r; tb < z; tb += kRows * U) {
+      float x[U][V * N];
+      int first[U];
+      bool on[U];
 #pragma unroll
-        for (int i = 1; i < V * N; ++i) mx = fmaxf(mx, x[i]);
-        mx = group_max<L>(mx);
-        if (mx != -INFINITY) {  // the same for the token's lanes
-          float s = 0.0f;
-#pragma unroll
-          for (int i = 0; i < V * N; ++i) {
-            x[i] = __expf(x[i] - mx);
-            s += x[i];
-          }
-          s = group_sum<L>(s);
-          const float inv = 1.0f / s;
-#pragma unroll
-          for (int i = 0; i < V * N; ++i) acc[i] += x[i] * inv;
-          lse = mx + logf(s);
-          zs += lse * lse;
-          ++cnt;
-          for (int j = l; j < k; j += L) {
-            const int e = ids[(int64_t)t * k + j];
-            if (e >= 0 && e < E) atomicAdd(&hist[e], 1);  // integers: any order gives the same
-          }
+      for (int u = 0; u < U; ++u) {  // every load before the first use
+        const int t = tb + u * kRows;
+        on[u] = t < z && in && (!mask || mask[t] != 0);
+        first[u] = -1;
+        if (on[u]) {
+          load_row<V, N>(logits + (int64_t)t * E, E, l, -INFINITY, x[u]);
+          if (l < k) first[u] = ids[(int64_t)t * k + l];
         }
       }
-      if (l == 0) lse_out[t] = lse;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u * kRows;
+        if (t >= z) break;
+        float lse = -INFINITY;
+        if (on[u]) {
+          float mx = x[u][0];
+#pragma unroll
+          for (int i = 1; i < V * N; ++i) mx = fmaxf(mx, x[u][i]);
+          mx = row16_max(mx);
+          if (mx != -INFINITY) {  // the same for the token's lanes
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V * N; ++i) {
+              x[u][i] = __expf(x[u][i] - mx);
+              s += x[u][i];
+            }
+            s = row16_sum(s);
+            const float inv = 1.0f / s;
+#pragma unroll
+            for (int i = 0; i < V * N; ++i) acc[i] += x[u][i] * inv;
+            lse = mx + logf(s);
+            zs += lse * lse;
+            ++cnt;
+            if (first[u] >= 0 && first[u] < E) atomicAdd(&hist[first[u]], 1);  // integers: any order gives the same
+            for (int j = l + kL; j < k; j += kL) {
+              const int e = ids[(int64_t)t * k + j];
+              if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+            }
+          }
+        }
+        if (l == 0) lse_out[t] = lse;
+      }
     }
     if (in) {
       // the rows of a wave, then the four waves, in fixed order
 #pragma unroll
-      for (int m = L; m < 64; m <<= 1) {
+      for (int m = kL; m < 64; m <<= 1) {
 #pragma unroll
         for (int i = 0; i < V * N; ++i) acc[i] += __shfl_xor(acc[i], m, 64);
         zs += __shfl_xor(zs, m, 64);
         cnt += __shfl_xor(cnt, m, 64);
       }
-      if ((tid & 63) < L) {
+      if ((tid & 63) < kL) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
-          for (int v = 0; v < V; ++v) shP[wv][(n * L + l) * V + v] = acc[n * V + v];
+          for (int v = 0; v < V; ++v) shP[wv][(n * kL + l) * V + v] = acc[n * V + v];
         if (l == 0) sh_n[wv] = cnt, sh_z[wv] = zs;
       }
       __syncthreads();
@@ -208,21 +214,56 @@ __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
   }
 }
 
-// One block per (64 columns, group): adds the pieces of the group's tiles in a fixed order (64-bit
-// sums), writes the counts, and the block that finishes last adds the groups' terms.
+// The losses from the groups' terms, by one block in a fixed order; sh: 64 doubles.
+__device__ __forceinline__ void write_losses(const double* part, const double* zpart, int32_t* tokens, int S, int chunks,
+                                             float* losses, double* sh) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  double bal = 0.0, zs = 0.0;
+  int32_t groups = 0, total = 0;
+  for (int64_t i = tid; i < (int64_t)S * chunks; i += kBalRedThreads) bal += part[i];
+  for (int i = tid; i < S; i += kBalRedThreads) {
+    const int32_t m = tokens[i];
+    total += m;
+    groups += m > 0;
+    zs += zpart[i];
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    bal += __shfl_xor(bal, m, 64);
+    zs += __shfl_xor(zs, m, 64);
+    total += __shfl_xor(total, m, 64);
+    groups += __shfl_xor(groups, m, 64);
+  }
+  __syncthreads();
+  if (lane == 0) sh[wv] = bal, sh[16 + wv] = zs, sh[32 + wv] = total, sh[48 + wv] = groups;
+  __syncthreads();
+  if (tid != 0) return;
+  bal = 0.0, zs = 0.0;
+  double n = 0.0, g = 0.0;
+  for (int w = 0; w < kBalRedThreads / 64; ++w) bal += sh[w], zs += sh[16 + w], n += sh[32 + w], g += sh[48 + w];
+  losses[0] = g > 0.0 ? (float)(bal / g) : 0.0f;
+  losses[1] = n > 0.0 ? (float)(zs / n) : 0.0f;
+  tokens[S] = (int32_t)n;
+  tokens[S + 1] = (int32_t)g;
+}
+
+// One block per (chunk of 64 * W columns, group): its 16 waves are W columns of 64 by 16 / W rows; adds
+// the pieces of the group's tiles in a fixed order (64-bit sums) and writes the counts.  A grid of one
+// block writes the losses too; else balance_final_kernel does.
+template <int W>
 __global__ __launch_bounds__(kBalRedThreads) void balance_reduce_kernel(
     const float* __restrict__ Pp, const int32_t* __restrict__ Cp, const int32_t* __restrict__ np,
     const float* __restrict__ zp, const int32_t* __restrict__ goff, int T, int E, int k, int S, int tile,
     int32_t* __restrict__ counts, int32_t* __restrict__ tokens, float* __restrict__ losses, double* part,
-    double* zpart, uint32_t* done) {
-  constexpr int kW = kBalRedThreads / 64;
+    double* zpart) {
+  constexpr int kW = kBalRedThreads / 64, kR = kW / W;
   __shared__ double shP[kW][64];
   __shared__ int32_t shC[kW][64];
   __shared__ int32_t sh_n[kW];
   __shared__ double sh_z[kW];
-  __shared__ bool last;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int g = blockIdx.y, c = blockIdx.x * 64 + lane, chunks = gridDim.x;
+  __shared__ double sh[64];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, row = wv / W;
+  const int g = blockIdx.y, c = (blockIdx.x * W + wv % W) * 64 + lane, chunks = gridDim.x;
   int a = 0, z = T;
   if (goff) {
     a = goff[g] < 0 ? 0 : goff[g];
@@ -231,12 +272,12 @@ __global__ __launch_bounds__(kBalRedThreads) void balance_reduce_kernel(
   const int b0 = z > a ? a / tile : 0, b1 = z > a ? (z - 1) / tile + 1 : 0;
   double P = 0.0;
   int32_t C = 0;
-#pragma unroll 4
-  for (int b = b0 + wv; b < b1; b += kW) {
-    const int64_t slot = (int64_t)b + g;
-    if (c < E) {
-      P += (double)Pp[slot * E + c];
-      C += Cp[slot * E + c];
+  if (c < E) {
+#pragma unroll 8
+    for (int b = b0 + row; b < b1; b += kR) {
+      const int64_t at = ((int64_t)b + g) * E + c;
+      P += (double)Pp[at];
+      C += Cp[at];
     }
   }
   int32_t n = 0;
@@ -254,69 +295,50 @@ __global__ __launch_bounds__(kBalRedThreads) void balance_reduce_kernel(
   shC[wv][lane] = C;
   if (lane == 0) sh_n[wv] = n, sh_z[wv] = zs;
   __syncthreads();
-  if (wv == 0) {
-    n = 0;
-    zs = 0.0;
+  n = 0;
+  zs = 0.0;
 #pragma unroll
-    for (int w = 1; w < kW; ++w) P += shP[w][lane], C += shC[w][lane];
+  for (int w = 0; w < kW; ++w) n += sh_n[w], zs += sh_z[w];
+  double dot = 0.0;
+  if (row == 0) {
 #pragma unroll
-    for (int w = 0; w < kW; ++w) n += sh_n[w], zs += sh_z[w];
-    if (c < E) counts[(int64_t)g * E + c] = C;
-    double dot = c < E ? (double)C * P : 0.0;
+    for (int q = 1; q < kR; ++q) P += shP[q * W + wv][lane], C += shC[q * W + wv][lane];
+    if (c < E) {
+      counts[(int64_t)g * E + c] = C;
+      dot = (double)C * P;
+    }
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) dot += __shfl_xor(dot, m, 64);
-    if (lane == 0) {
-      part[(int64_t)g * chunks + blockIdx.x] = n > 0 ? dot * (double)E / ((double)k * (double)n * (double)n) : 0.0;
-      if (blockIdx.x == 0) tokens[g] = n, zpart[g] = zs;
-      __threadfence();
-      last = atomicAdd(done, 1u) == (uint32_t)(gridDim.x * gridDim.y) - 1u;
-    }
+    if (lane == 0) sh[wv] = dot;
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // every block's values are in memory; added in a fixed order whichever block this is
-  double bal = 0.0;
-  int32_t groups = 0, total = 0;
-  zs = 0.0;
-  for (int64_t i = tid; i < (int64_t)S * chunks; i += kBalRedThreads) bal += ((volatile double*)part)[i];
-  for (int i = tid; i < S; i += kBalRedThreads) {
-    const int32_t m = ((volatile int32_t*)tokens)[i];
-    total += m;
-    groups += m > 0;
-    zs += ((volatile double*)zpart)[i];
-  }
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    bal += __shfl_xor(bal, m, 64);
-    zs += __shfl_xor(zs, m, 64);
-    total += __shfl_xor(total, m, 64);
-    groups += __shfl_xor(groups, m, 64);
-  }
-  __syncthreads();
-  if (lane == 0) shP[wv][0] = bal, shP[wv][1] = zs, shC[wv][0] = total, shC[wv][1] = groups;
   __syncthreads();
   if (tid == 0) {
-    bal = 0.0, zs = 0.0, total = 0, groups = 0;
-    for (int w = 0; w < kW; ++w) bal += shP[w][0], zs += shP[w][1], total += shC[w][0], groups += shC[w][1];
-    losses[0] = groups > 0 ? (float)(bal / groups) : 0.0f;
-    losses[1] = total > 0 ? (float)(zs / total) : 0.0f;
-    tokens[S] = total;
-    tokens[S + 1] = groups;
+    dot = 0.0;
+    for (int w = 0; w < W; ++w) dot += sh[w];
+    part[(int64_t)g * chunks + blockIdx.x] = n > 0 ? dot * (double)E / ((double)k * (double)n * (double)n) : 0.0;
+    if (blockIdx.x == 0) tokens[g] = n, zpart[g] = zs;
   }
+  if (gridDim.x * gridDim.y > 1) return;
+  __syncthreads();
+  write_losses(part, zpart, tokens, S, chunks, losses, sh);
 }
 
-// The gradient: L lanes per token.  Since sum_e p = 1, an integer near their mean is taken off the
+__global__ __launch_bounds__(kBalRedThreads) void balance_final_kernel(const double* part, const double* zpart, int S,
+                                                                       int chunks, int32_t* tokens, float* losses) {
+  __shared__ double sh[64];
+  write_losses(part, zpart, tokens, S, chunks, losses, sh);
+}
+
+// The gradient: kL lanes per token.  Since sum_e p = 1, an integer near their mean is taken off the
 // counts first, which loses nothing and keeps the difference from cancelling.
-template <int V, int L, int N>
+template <int V, int N>
 __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
     const float* __restrict__ logits, const float* __restrict__ lse_in, const int32_t* __restrict__ goff,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens, const float* __restrict__ d_losses, int T,
     int E, int k, int S, int tile, const float* d_in, float* d_out) {
-  constexpr int kRows = kBalThreads / L;
-  const int tid = threadIdx.x, l = tid % L, r = tid / L;
+  const int tid = threadIdx.x, l = tid % kL, r = tid / kL;
   const int t0 = blockIdx.x * tile, t1 = T - t0 < tile ? T : t0 + tile;
-  int g = -1, lo = 0, hi = -1;  // no group yet
+  int lo = 0, hi = -1;  // the group's tokens: no group yet
   float c[V * N];
 #pragma unroll
   for (int i = 0; i < V * N; ++i) c[i] = 0.0f;
@@ -325,17 +347,18 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
   const float cb = total > 0 ? 2.0f * d_losses[1] / (float)total : 0.0f;
   for (int t = t0 + r; t < t1; t += kRows) {
     const int64_t row = (int64_t)t * E;
-    float d[V * N];
+    const float lse = lse_in[t];
+    float p[V * N], d[V * N];
+    load_row<V, N>(logits + row, E, l, -INFINITY, p);
     if (d_in) {
-      load_row<V, L, N>(d_in + row, E, l, 0.0f, d);
+      load_row<V, N>(d_in + row, E, l, 0.0f, d);
     } else {
 #pragma unroll
       for (int i = 0; i < V * N; ++i) d[i] = 0.0f;
     }
-    const float lse = lse_in[t];
-    if (lse != -INFINITY) {
+    if (lse != -INFINITY) {  // else what was read of the logits is not used
       if (t < lo || t >= hi) {
-        g = goff ? group_of(goff, S, t) : 0;
+        int g = goff ? group_of(goff, S, t) : 0;
         g = g < 0 ? 0 : (g >= S ? S - 1 : g);  // a counted token lies in a group
         lo = goff ? goff[g] : 0;
         hi = goff ? goff[g + 1] : T;
@@ -346,27 +369,25 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
         for (int i = 0; i < N; ++i)
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            const int col = (i * L + l) * V + v;
+            const int col = (i * kL + l) * V + v;
             c[i * V + v] = col < E ? (float)(cg[col] - mean) : 0.0f;
           }
         ca = n > 0 ? (float)((double)d_losses[0] * (double)E / ((double)k * n * (double)n * (double)tokens[S + 1])) : 0.0f;
       }
-      float p[V * N];
-      load_row<V, L, N>(logits + row, E, l, -INFINITY, p);
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < V * N; ++i) {
         p[i] = __expf(p[i] - lse);
         dot += c[i] * p[i];
       }
-      dot = group_sum<L>(dot);
+      dot = row16_sum(dot);
       const float zc = cb * lse;
 #pragma unroll
       for (int i = 0; i < V * N; ++i) d[i] += p[i] * (ca * (c[i] - dot) + zc);
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int col = (n * L + l) * V;
+      const int col = (n * kL + l) * V;
       if (col >= E) continue;
       if (V == 4)
         *(float4*)(d_out + row + col) = make_float4(d[n * V], d[n * V + 1], d[n * V + 2], d[n * V + 3]);
@@ -376,24 +397,23 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
   }
 }
 
-// The smallest group of lanes that holds a row in few registers; rows of a multiple of 4 columns
-// are 16-byte aligned and move as vectors.
-#define MOE_BAL_DISPATCH(E, CALL)                              \
-  do {                                                         \
-    if ((E) % 4 == 0) {                                        \
-      if ((E) <= 32) { CALL(4, 8, 1); }                        \
-      else if ((E) <= 64) { CALL(4, 16, 1); }                  \
-      else if ((E) <= 128) { CALL(4, 32, 1); }                 \
-      else if ((E) <= 256) { CALL(4, 64, 1); }                 \
-      else if ((E) <= 512) { CALL(4, 64, 2); }                 \
-      else { CALL(4, 64, 4); }                                 \
-    } else {                                                   \
-      if ((E) <= 64) { CALL(1, 64, 1); }                       \
-      else if ((E) <= 128) { CALL(1, 64, 2); }                 \
-      else if ((E) <= 256) { CALL(1, 64, 4); }                 \
-      else if ((E) <= 512) { CALL(1, 64, 8); }                 \
-      else { CALL(1, 64, 16); }                                \
-    }                                                          \
+// The fewest columns a lane that hold a row; rows of a multiple of 4 columns are 16-byte aligned and
+// move as vectors.
+#define MOE_BAL_DISPATCH(E, CALL)                  \
+  do {                                             \
+    if ((E) % 4 == 0) {                            \
+      if ((E) <= 64) { CALL(4, 1); }               \
+      else if ((E) <= 128) { CALL(4, 2); }         \
+      else if ((E) <= 256) { CALL(4, 4); }         \
+      else if ((E) <= 512) { CALL(4, 8); }         \
+      else { CALL(4, 16); }                        \
+    } else {                                       \
+      if ((E) <= 64) { CALL(1, 4); }               \
+      else if ((E) <= 128) { CALL(1, 8); }         \
+      else if ((E) <= 256) { CALL(1, 16); }        \
+      else if ((E) <= 512) { CALL(1, 32); }        \
+      else { CALL(1, 64); }                        \
+    }                                              \
   } while (0)
 
 }  // namespace
@@ -405,17 +425,31 @@ hipError_t launch_balance_forward(const float* logits, const int32_t* ids, const
                                   float* lse, void* ws, hipStream_t st) {
   const BalWs w = bal_ws(T, E, S, (char*)ws);
   const int tile = balance_tile(T);
-  // an empty batch still runs one block, which sets the counter of the reduction
-  const unsigned tiles = T > 0 ? (unsigned)((T + tile - 1) / tile) : 1u;
-#define MOE_BAL_CALL(V, L, N)                                                                                       \
-  balance_stats_kernel<V, L, N><<<tiles, kBalThreads, 0, st>>>(logits, ids, mask, goff, T, E, k, S, tile, lse, w.P, \
-                                                               w.C, w.n, w.z, w.done)
-  MOE_BAL_DISPATCH(E, MOE_BAL_CALL);
+  const unsigned tiles = (unsigned)((T + (int64_t)tile - 1) / tile);
+  if (tiles > 0) {
+#define MOE_BAL_CALL(V, N)                                                                                       \
+  balance_stats_kernel<V, N><<<tiles, kBalThreads, 0, st>>>(logits, ids, mask, goff, T, E, k, S, tile, lse, w.P, \
+                                                            w.C, w.n, w.z)
+    MOE_BAL_DISPATCH(E, MOE_BAL_CALL);
 #undef MOE_BAL_CALL
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  balance_reduce_kernel<<<dim3((E + 63) / 64, S), kBalRedThreads, 0, st>>>(
-      w.P, w.C, w.n, w.z, goff, T, E, k, S, tile, counts, tokens, losses, w.part, w.zpart, w.done);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int wide = balance_wide(T, E, S);
+  const int chunks = (E + 64 * wide - 1) / (64 * wide);
+  const dim3 grid(chunks, S);
+#define MOE_BAL_CALL(W)                                                                                             \
+  balance_reduce_kernel<W><<<grid, kBalRedThreads, 0, st>>>(w.P, w.C, w.n, w.z, goff, T, E, k, S, tile, counts, \
+                                                            tokens, losses, w.part, w.zpart)
+  if (wide == 1) MOE_BAL_CALL(1);
+  else if (wide == 2) MOE_BAL_CALL(2);
+  else if (wide == 4) MOE_BAL_CALL(4);
+  else if (wide == 8) MOE_BAL_CALL(8);
+  else MOE_BAL_CALL(16);
+#undef MOE_BAL_CALL
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || chunks * S == 1) return e;
+  balance_final_kernel<<<1, kBalRedThreads, 0, st>>>(w.part, w.zpart, S, chunks, tokens, losses);
   return hipGetLastError();
 }
 
@@ -425,9 +459,9 @@ hipError_t launch_balance_backward(const float* logits, const float* lse, const 
   if (T == 0) return hipSuccess;
   const int tile = 64;
   const unsigned tiles = (unsigned)((T + (int64_t)tile - 1) / tile);
-#define MOE_BAL_CALL(V, L, N)                                                                                       \
-  balance_grad_kernel<V, L, N><<<tiles, kBalThreads, 0, st>>>(logits, lse, goff, counts, tokens, d_losses, T, E, k, \
-                                                              S, tile, d_in, d_out)
+#define MOE_BAL_CALL(V, N)                                                                                       \
+  balance_grad_kernel<V, N><<<tiles, kBalThreads, 0, st>>>(logits, lse, goff, counts, tokens, d_losses, T, E, k, \
+                                                           S, tile, d_in, d_out)
   MOE_BAL_DISPATCH(E, MOE_BAL_CALL);
 #undef MOE_BAL_CALL
   return hipGetLastError();

@@ -52,6 +52,42 @@ __device__ __forceinline__ T wave_shfl_xor(T v, int mask) {
   return __shfl_xor(v, mask, kWave);
 }
 
+// Lane exchanges in the vector ALU (DPP): rotations within a row of 16 lanes, and the running
+// combination of a wave's four rows that ends in lane 63.  No LDS round trip, unlike a shuffle.
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(old), __float_as_uint(v), kCtrl, kRowMask, 0xf,
+                                                     kRowMask == 0xf));
+}
+
+// Sum or maximum of 16 neighbouring lanes, the same in each of them.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += dpp<0x128, 0xf>(0.0f, v);
+  v += dpp<0x124, 0xf>(0.0f, v);
+  v += dpp<0x122, 0xf>(0.0f, v);
+  return v + dpp<0x121, 0xf>(0.0f, v);
+}
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, dpp<0x128, 0xf>(0.0f, v));
+  v = fmaxf(v, dpp<0x124, 0xf>(0.0f, v));
+  v = fmaxf(v, dpp<0x122, 0xf>(0.0f, v));
+  return fmaxf(v, dpp<0x121, 0xf>(0.0f, v));
+}
+
+// Sum or maximum (of values >= 0) of a whole wave, as a scalar.
+__device__ __forceinline__ float wave_sum_dpp(float v) {
+  v = row16_sum(v);
+  v += dpp<0x142, 0xa>(0.0f, v);  // lane 15 of each row into the next: rows 1 and 3
+  v += dpp<0x143, 0xc>(0.0f, v);  // lane 31 into rows 2 and 3
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_max_dpp(float v) {
+  v = row16_max(v);
+  v = fmaxf(v, dpp<0x142, 0xa>(0.0f, v));
+  v = fmaxf(v, dpp<0x143, 0xc>(0.0f, v));
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+
 // Exclusive scan of one int per thread over a 1024-thread block; returns the block total.
 __device__ __forceinline__ int block_excl_scan_1024(int v, int* sh, int* excl) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
