@@ -86,69 +86,28 @@ __device__ __forceinline__ uint32_t code_of(float y, uint32_t r16) {
   return (b >> 20) - (low ? 968u : 960u);
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
-  return v;
-}
-
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// 4 consecutive values from element i; with `ok` < 4 only the first ones exist
-__device__ __forceinline__ void load4(const void* p, int64_t i, int ok, bool f32, float (&x)[4]) {
-  if (ok == 4) {
-    if (f32) {
-      const float4 q = *(const float4*)((const float*)p + i);
-      x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
-    } else {
-      const uint2 q = *(const uint2*)((const uint16_t*)p + i);
-      x[0] = lo_bf16(q.x), x[1] = hi_bf16(q.x), x[2] = lo_bf16(q.y), x[3] = hi_bf16(q.y);
-    }
-  } else {
+// 4 consecutive values from element i
+template <bool F32>
+__device__ __forceinline__ void load4(const void* p, int64_t i, float (&x)[4]) {
+  if (F32) {
+    const f32x4_t q = __builtin_nontemporal_load((const f32x4_t*)((const float*)p + i));
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      x[j] = j < ok ? (f32 ? ((const float*)p)[i + j] : bf16_to_f32(((const uint16_t*)p)[i + j])) : 0.0f;
+    for (int j = 0; j < 4; ++j) x[j] = q[j];
+  } else {
+    const u32x2_t q = __builtin_nontemporal_load((const u32x2_t*)((const uint16_t*)p + i));
+    x[0] = lo_bf16(q[0]), x[1] = hi_bf16(q[0]), x[2] = lo_bf16(q[1]), x[3] = hi_bf16(q[1]);
   }
 }
 
-__device__ __forceinline__ void store4f(float* p, int64_t i, int ok, const float (&x)[4]) {
-  if (ok == 4) {
-    *(float4*)(p + i) = make_float4(x[0], x[1], x[2], x[3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < ok) p[i + j] = x[j];
-  }
+__device__ __forceinline__ void store4(void* p, int64_t i, const float (&x)[4]) {
+  __builtin_nontemporal_store(f32x4_t{x[0], x[1], x[2], x[3]}, (f32x4_t*)((float*)p + i));
 }
 
-__device__ __forceinline__ void store4h(uint16_t* p, int64_t i, int ok, uint32_t a, uint32_t b) {
-  if (ok == 4) {
-    *(uint2*)(p + i) = make_uint2(a, b);
-  } else {
-    const uint32_t w[2] = {a, b};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < ok) p[i + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-  }
-}
-
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int ok) {
-  if (ok == 4) return *(const uint32_t*)(p + i);
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (j < ok) w |= (uint32_t)p[i + j] << (8 * j);
-  return w;
-}
-
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int ok, uint32_t w) {
-  if (ok == 4) {
-    *(uint32_t*)(p + i) = w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < ok) p[i + j] = (uint8_t)(w >> (8 * j));
-  }
+__device__ __forceinline__ void store4(void* p, int64_t i, uint32_t a, uint32_t b) {
+  __builtin_nontemporal_store(u32x2_t{a, b}, (u32x2_t*)((uint16_t*)p + i));
 }
 
 __device__ __forceinline__ void decode4(uint32_t w, float scale, float (&x)[4]) {
@@ -161,118 +120,281 @@ __device__ __forceinline__ float block_scale(float top) {
   return top > 0.0f ? fmaxf(top * (1.0f / 448.0f), 1.17549435e-38f) : 1.0f;
 }
 
-// Products and sums round one by one (no fused multiply-add): a state's code then follows from
-// single fp32 operations, and the same step written out in them gives the same bits.
-__global__ __launch_bounds__(256) void adamw_kernel(AdamBatch batch, AdamScalars hp) {
+// 1 / s for a normal s: the hardware's reciprocal (1 ulp) and one Newton step
+__device__ __forceinline__ float inverse(float s) {
+  const float r = __builtin_amdgcn_rcpf(s);
+  return __fmaf_rn(__fmaf_rn(-s, r, 1.0f), r, r);
+}
+
+// What a step needs beside the tensors, the same for a whole launch or tensor
+struct Step {
+  float b1, b2, a1, a2, eps, gs, keep, rate, inv_rc2;
+  uint32_t k0, k1;
+  bool random_p;
+};
+
+// Four values' update; `w` holds the master copy or the parameter.  Products and sums round one by
+// one (no fused multiply-add): a state's code then follows from single fp32 operations, and the same
+// step written out in them gives the same bits.
+__device__ __forceinline__ void update4(const Step& h, float (&g)[4], float (&m)[4], float (&v)[4], float (&w)[4],
+                                        float (&root)[4]) {
 #pragma clang fp contract(off)
-  float gs = 1.0f;
-  if (hp.d_grad_scale) {
-    gs = *hp.d_grad_scale;
-    if (!(fabsf(gs) < INFINITY)) return;  // a step to skip: nothing changes
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    g[j] *= h.gs;
+    m[j] = h.b1 * m[j] + h.a1 * g[j];
+    v[j] = h.b2 * v[j] + (h.a2 * g[j]) * g[j];
+    root[j] = sqrtf(v[j]);
+    w[j] = w[j] * h.keep - (h.rate * m[j]) * __builtin_amdgcn_rcpf(root[j] * h.inv_rc2 + h.eps);
   }
-  const int which = tensor_of(batch, blockIdx.x);
-  const AdamTensor& T = batch.t[which];
-  const float lr = hp.d_lr ? *hp.d_lr : hp.lr;
-  float inv_c1 = hp.inv_c1, inv_rc2 = hp.inv_rc2;
-  uint64_t step = hp.step;
-  if (hp.d_step) {
-    step = (uint64_t)*hp.d_step;
-    inv_c1 = (float)(1.0 / one_less_power(hp.b1d, step));
-    inv_rc2 = (float)(1.0 / sqrt(one_less_power(hp.b2d, step)));
+}
+
+// Four values' codes of m and sqrt(v) and their 256 values' scales (a whole wave calls it).
+__device__ __forceinline__ void encode4(const float (&m)[4], const float (&root)[4], const uint32_t (&u)[4],
+                                        uint32_t& cm, uint32_t& cr, float& sm, float& sr) {
+#pragma clang fp contract(off)
+  sm = block_scale(wave_max_dpp(fmaxf(fmaxf(fabsf(m[0]), fabsf(m[1])), fmaxf(fabsf(m[2]), fabsf(m[3])))));
+  sr = block_scale(wave_max_dpp(fmaxf(fmaxf(root[0], root[1]), fmaxf(root[2], root[3]))));
+  const float im = inverse(sm), ir = inverse(sr);
+  cm = cr = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t a = code_of(fminf(fabsf(m[j]) * im, 448.0f), u[j] & 0xFFFFu);
+    cm |= (a | (m[j] < 0.0f ? 0x80u : 0u)) << (8 * j);
+    const float y = fminf(root[j] * ir, 448.0f);
+    uint32_t b = code_of(y, u[j] >> 16);
+    if (b == 0 && y > 0.0f) b = 1;  // a root above 0 stays above 0: it divides the next step
+    cr |= b << (8 * j);
   }
-  const uint64_t key = step_key(hp.seed, step, (uint64_t)(hp.first_tensor + which));
-  const uint32_t k0 = (uint32_t)key, k1 = (uint32_t)(key >> 32);
-  const float keep = 1.0f - lr * T.weight_decay, rate = lr * inv_c1;
-  const bool p32 = T.flags & kAdamP32, g32 = T.flags & kAdamG32, eight = T.flags & kAdam8bit;
-  const bool random_p = !p32 && !T.master && hp.stochastic;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t base = (int64_t)(blockIdx.x - batch.first[which]) * kChunk;
-#pragma unroll 2
-  for (int it = 0; it < kChunk / 1024; ++it) {
-    const int64_t i0 = base + (it * 4 + wv) * 256, i = i0 + lane * 4;
-    if (i0 >= T.n) return;
-    const int64_t left = T.n - i;
-    const int ok = left >= 4 ? 4 : left > 0 ? (int)left : 0;
-    float g[4], m[4], v[4], w[4], root[4];
-    load4(T.g, i, ok, g32, g);
-    if (T.master) load4(T.master, i, ok, true, w);
-    else load4(T.p, i, ok, p32, w);
-    if (eight) {
-      decode4(load_codes((const uint8_t*)T.m, i, ok), T.m_scale[i0 / 256], m);
-      decode4(load_codes((const uint8_t*)T.v, i, ok), T.v_scale[i0 / 256], v);
+}
+
+// Two bf16 pairs of w, stochastically rounded with the second words of u
+__device__ __forceinline__ void random4(const float (&w)[4], const uint32_t (&u)[4], uint32_t k0, uint32_t& a, uint32_t& b) {
+  uint32_t q[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] *= v[j];
+  for (int j = 0; j < 4; ++j) q[j] = (__float_as_uint(w[j]) + (noise2(u[j], k0) & 0xFFFFu)) >> 16;
+  a = q[0] | q[1] << 16;
+  b = q[2] | q[3] << 16;
+}
+
+// U runs of 256 whole values of a wave, `stride` values apart: every load is issued before the first
+// use.  The streams are read and written once (non-temporal).
+template <bool P32, bool MASTER, bool G32, bool EIGHT, int U>
+__device__ __forceinline__ void adamw_runs(const AdamTensor& T, const Step& h, int64_t i0, int64_t stride, int lane) {
+  float g[U][4], m[U][4], v[U][4], w[U][4];
+  uint32_t qm[U], qv[U];
+  float sm[U], sv[U];
+#pragma unroll
+  for (int r = 0; r < U; ++r) {
+    const int64_t b = i0 + r * stride, i = b + lane * 4;
+    load4<G32>(T.g, i, g[r]);
+    if (MASTER) load4<true>(T.master, i, w[r]);
+    else load4<P32>(T.p, i, w[r]);
+    if (EIGHT) {
+      qm[r] = __builtin_nontemporal_load((const uint32_t*)((const uint8_t*)T.m + i));
+      qv[r] = __builtin_nontemporal_load((const uint32_t*)((const uint8_t*)T.v + i));
+      sm[r] = T.m_scale[b / 256];
+      sv[r] = T.v_scale[b / 256];
     } else {
-      load4(T.m, i, ok, true, m);
-      load4(T.v, i, ok, true, v);
+      load4<true>(T.m, i, m[r]);
+      load4<true>(T.v, i, v[r]);
     }
-    uint32_t u[4] = {0, 0, 0, 0};
-    if (eight || random_p)
+  }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = noise(k0, k1, i + j);
+  for (int r = 0; r < U; ++r) {
+    const int64_t b = i0 + r * stride, i = b + lane * 4;
+    if (EIGHT) {
+      decode4(qm[r], sm[r], m[r]);
+      decode4(qv[r], sv[r], v[r]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      g[j] *= gs;
-      m[j] = hp.b1 * m[j] + hp.a1 * g[j];
-      v[j] = hp.b2 * v[j] + (hp.a2 * g[j]) * g[j];
-      root[j] = sqrtf(v[j]);
-      w[j] = w[j] * keep - rate * m[j] / (root[j] * inv_rc2 + hp.eps);
+      for (int j = 0; j < 4; ++j) v[r][j] *= v[r][j];
     }
-    if (T.master) store4f(T.master, i, ok, w);
-    if (p32) {
-      store4f((float*)T.p, i, ok, w);
-    } else if (random_p) {
-      uint32_t b[4];
+    float root[4];
+    update4(h, g[r], m[r], v[r], w[r], root);
+    uint32_t u[4];
+    if (EIGHT || (!P32 && !MASTER))
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = (__float_as_uint(w[j]) + (noise2(u[j], k0) & 0xFFFFu)) >> 16;
-      store4h((uint16_t*)T.p, i, ok, b[0] | b[1] << 16, b[2] | b[3] << 16);
+      for (int j = 0; j < 4; ++j) u[j] = noise(h.k0, h.k1, i + j);
+    if (MASTER) store4(T.master, i, w[r]);
+    if (P32) {
+      store4(T.p, i, w[r]);
+    } else if (!MASTER && h.random_p) {
+      uint32_t x, y;
+      random4(w[r], u, h.k0, x, y);
+      store4(T.p, i, x, y);
     } else {
-      store4h((uint16_t*)T.p, i, ok, pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
+      store4(T.p, i, pack_bf16x2(w[r][0], w[r][1]), pack_bf16x2(w[r][2], w[r][3]));
     }
-    if (eight) {
-      float tm = 0.0f, tr = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < ok) tm = fmaxf(tm, fabsf(m[j])), tr = fmaxf(tr, root[j]);
-      const float sm = block_scale(wave_max(tm)), sr = block_scale(wave_max(tr));
-      const float im = 1.0f / sm, ir = 1.0f / sr;
-      uint32_t cm = 0, cr = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t a = code_of(fminf(fabsf(m[j]) * im, 448.0f), u[j] & 0xFFFFu);
-        cm |= (a | (m[j] < 0.0f ? 0x80u : 0u)) << (8 * j);
-        const float y = fminf(root[j] * ir, 448.0f);
-        uint32_t b = code_of(y, u[j] >> 16);
-        if (b == 0 && y > 0.0f) b = 1;  // a root above 0 stays above 0: it divides the next step
-        cr |= b << (8 * j);
-      }
-      store_codes((uint8_t*)T.m, i, ok, cm);
-      store_codes((uint8_t*)T.v, i, ok, cr);
-      if (lane == 0) T.m_scale[i0 / 256] = sm, T.v_scale[i0 / 256] = sr;
+    if (EIGHT) {
+      encode4(m[r], root, u, qm[r], qv[r], sm[r], sv[r]);
+      __builtin_nontemporal_store(qm[r], (uint32_t*)((uint8_t*)T.m + i));
+      __builtin_nontemporal_store(qv[r], (uint32_t*)((uint8_t*)T.v + i));
+      if (lane == 0) T.m_scale[b / 256] = sm[r], T.v_scale[b / 256] = sv[r];
     } else {
-      store4f((float*)T.m, i, ok, m);
-      store4f((float*)T.v, i, ok, v);
+      store4(T.m, i, m[r]);
+      store4(T.v, i, v[r]);
     }
   }
 }
 
+// The last run of a tensor, shorter than 256: value by value.
+__device__ __forceinline__ void adamw_tail(const AdamTensor& T, const Step& h, int64_t i0, int lane) {
+  const bool p32 = T.flags & kAdamP32, g32 = T.flags & kAdamG32, eight = T.flags & kAdam8bit;
+  const int64_t i = i0 + lane * 4;
+  float g[4], m[4], v[4], w[4], root[4];
+  uint32_t u[4], cm = 0, cr = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    g[j] = m[j] = v[j] = w[j] = 0.0f;
+    u[j] = noise(h.k0, h.k1, i + j);
+    if (i + j >= T.n) continue;
+    g[j] = g32 ? ((const float*)T.g)[i + j] : bf16_to_f32(((const uint16_t*)T.g)[i + j]);
+    w[j] = T.master ? T.master[i + j] : p32 ? ((const float*)T.p)[i + j] : bf16_to_f32(((const uint16_t*)T.p)[i + j]);
+    if (eight) {
+      cm |= (uint32_t)((const uint8_t*)T.m)[i + j] << (8 * j);
+      cr |= (uint32_t)((const uint8_t*)T.v)[i + j] << (8 * j);
+    } else {
+      m[j] = ((const float*)T.m)[i + j];
+      v[j] = ((const float*)T.v)[i + j];
+    }
+  }
+  if (eight) {
+    decode4(cm, T.m_scale[i0 / 256], m);
+    decode4(cr, T.v_scale[i0 / 256], v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] *= v[j];
+  }
+  update4(h, g, m, v, w, root);  // 0 stays 0 behind the last value
+  uint32_t b[2] = {pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3])};
+  if (h.random_p) random4(w, u, h.k0, b[0], b[1]);
+  float sm = 0.0f, sr = 0.0f;
+  if (eight) {
+    encode4(m, root, u, cm, cr, sm, sr);
+    if (lane == 0) T.m_scale[i0 / 256] = sm, T.v_scale[i0 / 256] = sr;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (i + j >= T.n) continue;
+    if (T.master) T.master[i + j] = w[j];
+    if (p32) ((float*)T.p)[i + j] = w[j];
+    else ((uint16_t*)T.p)[i + j] = (uint16_t)(b[j >> 1] >> (16 * (j & 1)));
+    if (eight) {
+      ((uint8_t*)T.m)[i + j] = (uint8_t)(cm >> (8 * j));
+      ((uint8_t*)T.v)[i + j] = (uint8_t)(cr >> (8 * j));
+    } else {
+      ((float*)T.m)[i + j] = m[j];
+      ((float*)T.v)[i + j] = v[j];
+    }
+  }
+}
+
+template <bool P32, bool MASTER, bool G32, bool EIGHT>
+__device__ __forceinline__ void adamw_chunk(const AdamTensor& T, const Step& h, int64_t base, int wv, int lane) {
+  constexpr int U = 2;
+  if (T.n - base >= kChunk) {
+#pragma unroll 1
+    for (int it = 0; it < kChunk / 1024; it += U)
+      adamw_runs<P32, MASTER, G32, EIGHT, U>(T, h, base + (it * 4 + wv) * 256, 1024, lane);
+    return;
+  }
+#pragma unroll 1
+  for (int it = 0; it < kChunk / 1024; ++it) {
+    const int64_t i0 = base + (it * 4 + wv) * 256;
+    if (i0 >= T.n) return;
+    if (T.n - i0 >= 256) adamw_runs<P32, MASTER, G32, EIGHT, 1>(T, h, i0, 0, lane);
+    else adamw_tail(T, h, i0, lane);
+  }
+}
+
+__global__ __launch_bounds__(256) void adamw_kernel(AdamBatch batch, AdamScalars hp) {
+  Step h;
+  h.gs = 1.0f;
+  if (hp.d_grad_scale) {
+    h.gs = *hp.d_grad_scale;
+    if (!(fabsf(h.gs) < INFINITY)) return;  // a step to skip: nothing changes
+  }
+  const int which = tensor_of(batch, blockIdx.x);
+  const AdamTensor& T = batch.t[which];
+  const float lr = hp.d_lr ? *hp.d_lr : hp.lr;
+  float inv_c1 = hp.inv_c1;
+  h.inv_rc2 = hp.inv_rc2;
+  uint64_t step = hp.step;
+  if (hp.d_step) {
+    step = (uint64_t)*hp.d_step;
+    inv_c1 = (float)(1.0 / one_less_power(hp.b1d, step));
+    h.inv_rc2 = (float)(1.0 / sqrt(one_less_power(hp.b2d, step)));
+  }
+  const uint64_t key = step_key(hp.seed, step, (uint64_t)(hp.first_tensor + which));
+  h.k0 = (uint32_t)key, h.k1 = (uint32_t)(key >> 32);
+  h.b1 = hp.b1, h.b2 = hp.b2, h.a1 = hp.a1, h.a2 = hp.a2, h.eps = hp.eps;
+  h.keep = 1.0f - lr * T.weight_decay;
+  h.rate = lr * inv_c1;
+  h.random_p = !(T.flags & kAdamP32) && !T.master && hp.stochastic;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t base = (int64_t)(blockIdx.x - batch.first[which]) * kChunk;
+  // one straight body for each combination of types (the same for the whole block)
+#define MOE_ADAM_CASE(P32, MASTER)                                                     \
+  switch (T.flags & (kAdamG32 | kAdam8bit)) {                                          \
+    case 0: adamw_chunk<P32, MASTER, false, false>(T, h, base, wv, lane); break;       \
+    case kAdamG32: adamw_chunk<P32, MASTER, true, false>(T, h, base, wv, lane); break; \
+    case kAdam8bit: adamw_chunk<P32, MASTER, false, true>(T, h, base, wv, lane); break; \
+    default: adamw_chunk<P32, MASTER, true, true>(T, h, base, wv, lane);               \
+  }
+  if (T.flags & kAdamP32) { MOE_ADAM_CASE(true, false) }
+  else if (T.master) { MOE_ADAM_CASE(false, true) }
+  else { MOE_ADAM_CASE(false, false) }
+#undef MOE_ADAM_CASE
+}
+
 // Sum of g^2 of one chunk, in 64 bits (no square of an fp32 value overflows or vanishes there).
+// Each thread has U loads of 16 bytes in flight; the values behind the last of them go one by one.
+template <bool G32>
+__device__ __forceinline__ double square_sum(const void* g, int64_t a, int64_t z) {
+  constexpr int V = G32 ? 4 : 8, U = 8;
+  double s = 0.0;
+  int64_t i = a + threadIdx.x * V;
+  const auto add = [&](const u32x4_nt& q) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (G32) {
+        const double x = (double)__uint_as_float(q[j]);
+        s += x * x;
+      } else {
+        const double x = (double)lo_bf16(q[j]), y = (double)hi_bf16(q[j]);
+        s += x * x;
+        s += y * y;
+      }
+    }
+  };
+  const char* p = (const char*)g;
+  constexpr int kSize = G32 ? 4 : 2;
+  for (; i + (U - 1) * 256 * V + V <= z; i += U * 256 * V) {
+    u32x4_nt q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) q[u] = __builtin_nontemporal_load((const u32x4_nt*)(p + (i + u * 256 * V) * kSize));
+#pragma unroll
+    for (int u = 0; u < U; ++u) add(q[u]);
+  }
+  for (; i < z; i += 256 * V) {
+    if (i + V <= z) {
+      add(*(const u32x4_nt*)(p + i * kSize));
+    } else {
+      for (int64_t j = i; j < z; ++j) {
+        const double x = G32 ? (double)((const float*)g)[j] : (double)bf16_to_f32(((const uint16_t*)g)[j]);
+        s += x * x;
+      }
+    }
+  }
+  return s;
+}
+
 __global__ __launch_bounds__(256) void grad_norm_kernel(AdamBatch batch, int chunk, double* __restrict__ part) {
   __shared__ double sh[4];
   const int which = tensor_of(batch, blockIdx.x);
   const AdamTensor& T = batch.t[which];
-  const bool g32 = T.flags & kAdamG32;
   const int64_t a = (int64_t)(blockIdx.x - batch.first[which]) * chunk;
   const int64_t z = T.n - a < chunk ? T.n : a + chunk;
-  double s = 0.0;
-#pragma unroll 4
-  for (int64_t i = a + threadIdx.x * 4; i < z; i += 1024) {
-    const int64_t left = z - i;
-    float g[4];
-    load4(T.g, i, left >= 4 ? 4 : (int)left, g32, g);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s += (double)g[j] * (double)g[j];
-  }
+  double s = T.flags & kAdamG32 ? square_sum<true>(T.g, a, z) : square_sum<false>(T.g, a, z);
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m, 64);
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
