@@ -17,7 +17,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kChunk = 4096;  // values a block updates: 4 waves x 4 runs of 256
+constexpr int kAdamThreads = 256;
+constexpr int kChunk = kAdamThreads * 4;  // values a block updates: 256 a wave
 
 enum { kAdamP32 = 1, kAdamG32 = 2, kAdam8bit = 4 };
 
@@ -36,15 +37,15 @@ struct AdamBatch {
   int32_t first[kAdamBatch + 1];  // first chunk of each tensor
   int32_t n;
 };
+static_assert(kAdamBatch < 64, "a lane for each tensor");
 static_assert(sizeof(AdamBatch) + sizeof(AdamScalars) <= 4096 - 64, "kernel arguments");
 
+// The tensor of a chunk: each lane compares one entry (the arguments may lie in host memory, where a
+// search's dependent reads cost a round trip each).
 __device__ __forceinline__ int tensor_of(const AdamBatch& b, int chunk) {
-  int lo = 0, hi = b.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (b.first[mid] <= chunk) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+  const int lane = threadIdx.x & 63;
+  const bool at = lane < b.n && b.first[lane] <= chunk;
+  return __popcll(__ballot(at)) - 1;
 }
 
 // 1 - beta^step by squaring, in 64 bits
@@ -177,63 +178,52 @@ __device__ __forceinline__ void random4(const float (&w)[4], const uint32_t (&u)
   b = q[2] | q[3] << 16;
 }
 
-// U runs of 256 whole values of a wave, `stride` values apart: every load is issued before the first
-// use.  The streams are read and written once (non-temporal).
-template <bool P32, bool MASTER, bool G32, bool EIGHT, int U>
-__device__ __forceinline__ void adamw_runs(const AdamTensor& T, const Step& h, int64_t i0, int64_t stride, int lane) {
-  float g[U][4], m[U][4], v[U][4], w[U][4];
-  uint32_t qm[U], qv[U];
-  float sm[U], sv[U];
+// The 256 whole values of a wave from b: every load is issued before the first use.  The streams are
+// read and written once (non-temporal).
+template <bool P32, bool MASTER, bool G32, bool EIGHT>
+__device__ __forceinline__ void adamw_run(const AdamTensor& T, const Step& h, int64_t b, int lane) {
+  const int64_t i = b + lane * 4;
+  float g[4], m[4], v[4], w[4], root[4];
+  uint32_t qm, qv, u[4];
+  float sm, sv;
+  load4<G32>(T.g, i, g);
+  if (MASTER) load4<true>(T.master, i, w);
+  else load4<P32>(T.p, i, w);
+  if (EIGHT) {
+    qm = __builtin_nontemporal_load((const uint32_t*)((const uint8_t*)T.m + i));
+    qv = __builtin_nontemporal_load((const uint32_t*)((const uint8_t*)T.v + i));
+    sm = T.m_scale[b / 256];
+    sv = T.v_scale[b / 256];
+    decode4(qm, sm, m);
+    decode4(qv, sv, v);
 #pragma unroll
-  for (int r = 0; r < U; ++r) {
-    const int64_t b = i0 + r * stride, i = b + lane * 4;
-    load4<G32>(T.g, i, g[r]);
-    if (MASTER) load4<true>(T.master, i, w[r]);
-    else load4<P32>(T.p, i, w[r]);
-    if (EIGHT) {
-      qm[r] = __builtin_nontemporal_load((const uint32_t*)((const uint8_t*)T.m + i));
-      qv[r] = __builtin_nontemporal_load((const uint32_t*)((const uint8_t*)T.v + i));
-      sm[r] = T.m_scale[b / 256];
-      sv[r] = T.v_scale[b / 256];
-    } else {
-      load4<true>(T.m, i, m[r]);
-      load4<true>(T.v, i, v[r]);
-    }
+    for (int j = 0; j < 4; ++j) v[j] *= v[j];
+  } else {
+    load4<true>(T.m, i, m);
+    load4<true>(T.v, i, v);
   }
+  if (EIGHT || (!P32 && !MASTER))
 #pragma unroll
-  for (int r = 0; r < U; ++r) {
-    const int64_t b = i0 + r * stride, i = b + lane * 4;
-    if (EIGHT) {
-      decode4(qm[r], sm[r], m[r]);
-      decode4(qv[r], sv[r], v[r]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[r][j] *= v[r][j];
-    }
-    float root[4];
-    update4(h, g[r], m[r], v[r], w[r], root);
-    uint32_t u[4];
-    if (EIGHT || (!P32 && !MASTER))
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = noise(h.k0, h.k1, i + j);
-    if (MASTER) store4(T.master, i, w[r]);
-    if (P32) {
-      store4(T.p, i, w[r]);
-    } else if (!MASTER && h.random_p) {
-      uint32_t x, y;
-      random4(w[r], u, h.k0, x, y);
-      store4(T.p, i, x, y);
-    } else {
-      store4(T.p, i, pack_bf16x2(w[r][0], w[r][1]), pack_bf16x2(w[r][2], w[r][3]));
-    }
-    if (EIGHT) {
-      encode4(m[r], root, u, qm[r], qv[r], sm[r], sv[r]);
-      __builtin_nontemporal_store(qm[r], (uint32_t*)((uint8_t*)T.m + i));
-      __builtin_nontemporal_store(qv[r], (uint32_t*)((uint8_t*)T.v + i));
-      if (lane == 0) T.m_scale[b / 256] = sm[r], T.v_scale[b / 256] = sv[r];
-    } else {
-      store4(T.m, i, m[r]);
-      store4(T.v, i, v[r]);
-    }
+    for (int j = 0; j < 4; ++j) u[j] = noise(h.k0, h.k1, i + j);
+  update4(h, g, m, v, w, root);
+  if (MASTER) store4(T.master, i, w);
+  if (P32) {
+    store4(T.p, i, w);
+  } else if (!MASTER && h.random_p) {
+    uint32_t x, y;
+    random4(w, u, h.k0, x, y);
+    store4(T.p, i, x, y);
+  } else {
+    store4(T.p, i, pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
+  }
+  if (EIGHT) {
+    encode4(m, root, u, qm, qv, sm, sv);
+    __builtin_nontemporal_store(qm, (uint32_t*)((uint8_t*)T.m + i));
+    __builtin_nontemporal_store(qv, (uint32_t*)((uint8_t*)T.v + i));
+    if (lane == 0) T.m_scale[b / 256] = sm, T.v_scale[b / 256] = sv;
+  } else {
+    store4(T.m, i, m);
+    store4(T.v, i, v);
   }
 }
 
@@ -288,25 +278,7 @@ __device__ __forceinline__ void adamw_tail(const AdamTensor& T, const Step& h, i
   }
 }
 
-template <bool P32, bool MASTER, bool G32, bool EIGHT>
-__device__ __forceinline__ void adamw_chunk(const AdamTensor& T, const Step& h, int64_t base, int wv, int lane) {
-  constexpr int U = 2;
-  if (T.n - base >= kChunk) {
-#pragma unroll 1
-    for (int it = 0; it < kChunk / 1024; it += U)
-      adamw_runs<P32, MASTER, G32, EIGHT, U>(T, h, base + (it * 4 + wv) * 256, 1024, lane);
-    return;
-  }
-#pragma unroll 1
-  for (int it = 0; it < kChunk / 1024; ++it) {
-    const int64_t i0 = base + (it * 4 + wv) * 256;
-    if (i0 >= T.n) return;
-    if (T.n - i0 >= 256) adamw_runs<P32, MASTER, G32, EIGHT, 1>(T, h, i0, 0, lane);
-    else adamw_tail(T, h, i0, lane);
-  }
-}
-
-__global__ __launch_bounds__(256) void adamw_kernel(AdamBatch batch, AdamScalars hp) {
+__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamBatch batch, AdamScalars hp) {
   Step h;
   h.gs = 1.0f;
   if (hp.d_grad_scale) {
@@ -330,15 +302,20 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamBatch batch, AdamScalars
   h.keep = 1.0f - lr * T.weight_decay;
   h.rate = lr * inv_c1;
   h.random_p = !(T.flags & kAdamP32) && !T.master && hp.stochastic;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t base = (int64_t)(blockIdx.x - batch.first[which]) * kChunk;
+  const int lane = threadIdx.x & 63;
+  const int64_t b = (int64_t)(blockIdx.x - batch.first[which]) * kChunk + (threadIdx.x >> 6) * 256;
+  if (b >= T.n) return;
+  if (T.n - b < 256) {
+    adamw_tail(T, h, b, lane);
+    return;
+  }
   // one straight body for each combination of types (the same for the whole block)
-#define MOE_ADAM_CASE(P32, MASTER)                                                     \
-  switch (T.flags & (kAdamG32 | kAdam8bit)) {                                          \
-    case 0: adamw_chunk<P32, MASTER, false, false>(T, h, base, wv, lane); break;       \
-    case kAdamG32: adamw_chunk<P32, MASTER, true, false>(T, h, base, wv, lane); break; \
-    case kAdam8bit: adamw_chunk<P32, MASTER, false, true>(T, h, base, wv, lane); break; \
-    default: adamw_chunk<P32, MASTER, true, true>(T, h, base, wv, lane);               \
+#define MOE_ADAM_CASE(P32, MASTER)                                              \
+  switch (T.flags & (kAdamG32 | kAdam8bit)) {                                   \
+    case 0: adamw_run<P32, MASTER, false, false>(T, h, b, lane); break;         \
+    case kAdamG32: adamw_run<P32, MASTER, true, false>(T, h, b, lane); break;   \
+    case kAdam8bit: adamw_run<P32, MASTER, false, true>(T, h, b, lane); break;  \
+    default: adamw_run<P32, MASTER, true, true>(T, h, b, lane);                 \
   }
   if (T.flags & kAdamP32) { MOE_ADAM_CASE(true, false) }
   else if (T.master) { MOE_ADAM_CASE(false, true) }
@@ -471,7 +448,7 @@ hipError_t launch_adamw(const moe_tensor* t, int64_t n, const AdamScalars& hp, h
   return for_batches(t, n, kChunk, [&](const AdamBatch& b, int64_t chunks, int64_t first) {
     AdamScalars h = hp;
     h.first_tensor = first;
-    adamw_kernel<<<(unsigned)chunks, 256, 0, st>>>(b, h);
+    adamw_kernel<<<(unsigned)chunks, kAdamThreads, 0, st>>>(b, h);
     return hipGetLastError();
   });
 }
