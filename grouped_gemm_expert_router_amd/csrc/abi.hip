@@ -762,7 +762,7 @@ int moe_norm_workspace_bytes(const moe_norm_desc* desc, size_t* out) {
   const int rc = check_norm(desc);
   if (rc) return rc;
   if (!out) return MOE_ERR_NULL;
-  *out = al256(norm_ws_bytes(desc->T, (int)desc->d, desc->gate));
+  *out = al256(norm_ws_bytes(desc->T, (int)desc->d));
   return MOE_OK;
 }
 
@@ -798,7 +798,7 @@ int moe_norm_backward(const moe_norm_desc* desc, const void* y, const void* h_ou
   if (rows && (gate != nullptr) != (desc->gate != MOE_GATE_NONE)) return MOE_ERR_NULL;
   if (desc->gate == MOE_GATE_NONE && dgate) return MOE_ERR_NULL;
   const bool sums = dw_pre || dw_post || (dgate && desc->gate == MOE_GATE_CHANNEL);
-  const size_t need = sums ? al256(norm_ws_bytes(desc->T, (int)desc->d, desc->gate)) : 0;
+  const size_t need = sums ? al256(norm_ws_bytes(desc->T, (int)desc->d)) : 0;
   if (need > 0 && !ws) return MOE_ERR_NULL;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   if (!al16(y) || !al16(h_out) || !al16(w_post) || !al16(gate) || !al16(w_pre) || !al16(dh_out) || !al16(dx) ||

@@ -17,8 +17,45 @@ namespace {
 
 enum { G_NONE = 0, G_CHANNEL = 1, G_TOKEN = 2, G_FULL = 3 };
 
-// 8 consecutive values of an array in fp32 or bf16, from element i (a multiple of 8)
-__device__ __forceinline__ void load8(const void* p, int64_t i, bool f32, float (&x)[8]) {
+// 8 consecutive values as they lie in memory, loaded once (non-temporal): a row's next loads are
+// in flight as these while the row before is worked on.
+template <bool F32>
+struct Raw8 {
+  u32x4_nt a, b;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const u32x4_nt* q = (const u32x4_nt*)((const char*)p + i * (F32 ? 4 : 2));
+    a = __builtin_nontemporal_load(q);
+    if (F32) b = __builtin_nontemporal_load(q + 1);
+  }
+  __device__ __forceinline__ void zero() {
+    a = u32x4_nt{0, 0, 0, 0};
+    b = a;
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (F32) x[j] = __uint_as_float(a[j]), x[4 + j] = __uint_as_float(b[j]);
+      else x[2 * j] = lo_bf16(a[j]), x[2 * j + 1] = hi_bf16(a[j]);
+    }
+  }
+};
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&x)[8]) {
+  u32x4_nt* q = (u32x4_nt*)((char*)p + i * (F32 ? 4 : 2));
+  if (F32) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      __builtin_nontemporal_store(u32x4_nt{__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                                           __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3])}, q + j);
+  } else {
+    __builtin_nontemporal_store(u32x4_nt{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                         pack_bf16x2(x[6], x[7])}, q);
+  }
+}
+
+// 8 values of a weight or a gate (its type is the same for a whole launch), which other rows read too
+__device__ __forceinline__ void load_w8(const void* p, int64_t i, bool f32, float (&x)[8]) {
   if (f32) {
     const float4 a = ((const float4*)((const float*)p + i))[0], b = ((const float4*)((const float*)p + i))[1];
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
@@ -27,17 +64,6 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, bool f32, float 
     const uint4 w = *(const uint4*)((const uint16_t*)p + i);
     x[0] = lo_bf16(w.x), x[1] = hi_bf16(w.x), x[2] = lo_bf16(w.y), x[3] = hi_bf16(w.y);
     x[4] = lo_bf16(w.z), x[5] = hi_bf16(w.z), x[6] = lo_bf16(w.w), x[7] = hi_bf16(w.w);
-  }
-}
-
-__device__ __forceinline__ void store8(void* p, int64_t i, bool f32, const float (&x)[8]) {
-  if (f32) {
-    float4* o = (float4*)((float*)p + i);
-    o[0] = make_float4(x[0], x[1], x[2], x[3]);
-    o[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    *(uint4*)((uint16_t*)p + i) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                             pack_bf16x2(x[6], x[7]));
   }
 }
 
@@ -50,20 +76,24 @@ __device__ __forceinline__ void store1(void* p, int64_t i, bool f32, float x) {
   else ((uint16_t*)p)[i] = f32_to_bf16(x);
 }
 
-// Sums of K values over a row's W waves, in the same order for every lane.  sh: [K][W] of the row;
-// the block's rows reach it together.
+// A barrier that waits for LDS alone: global loads and stores stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Sums of K values over a row's W waves, the same in every lane.  sh: [K][W] of the row and of this
+// sum (the next one uses another, so one barrier is enough); the block's rows reach it together.
 template <int W, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
 #pragma unroll
-  for (int q = 0; q < K; ++q)
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v[q] += __shfl_xor(v[q], m, 64);
+  for (int q = 0; q < K; ++q) v[q] = wave_sum_dpp(v[q]);
   if (W > 1) {
-    __syncthreads();  // the last sums have been read
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
       for (int q = 0; q < K; ++q) sh[q * W + wave] = v[q];
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int q = 0; q < K; ++q) {
       v[q] = sh[q * W];
@@ -73,65 +103,70 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
   }
 }
 
+constexpr int norm_threads(int W) { return W <= 4 ? 256 : 64 * W; }
+
 // W waves a row, NV times 8 values a lane: the row stays in registers between its passes.
-template <int W, int NV>
-__global__ __launch_bounds__(W <= 4 ? 256 : 512) void norm_forward_kernel(NormArgs p, const uint16_t* __restrict__ y,
-                                                                         const void* h, const void* __restrict__ w_post,
-                                                                         const void* __restrict__ gate,
-                                                                         const void* __restrict__ w_pre, void* h_out,
-                                                                         uint16_t* __restrict__ x) {
-  constexpr int kRows = W <= 4 ? 4 / W : 1;
-  __shared__ float sh[kRows][2 * W];
+template <int W, int NV, bool HF32>
+__global__ __launch_bounds__(norm_threads(W)) void norm_forward_kernel(
+    NormArgs p, const uint16_t* __restrict__ y, const void* h, const void* __restrict__ w_post,
+    const void* __restrict__ gate, const void* __restrict__ w_pre, void* h_out, uint16_t* __restrict__ x) {
+  constexpr int kRows = norm_threads(W) / (64 * W);
+  __shared__ float sh[kRows][2][W];
   const int slot = threadIdx.x / (64 * W), lane = threadIdx.x % (64 * W), wave = lane >> 6;
   const int64_t t = (int64_t)blockIdx.x * kRows + slot;
   const bool on = t < p.T;
   const int64_t base = on ? t * p.d : 0;
-  float yv[NV][8], hv[NV][8];
-  float s[1] = {0.0f};
+  Raw8<false> yr[NV];
+  Raw8<HF32> hr[NV];
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int c = (n * 64 * W + lane) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) yv[n][i] = 0.0f, hv[n][i] = 0.0f;
+    hr[n].zero();
+    yr[n].zero();
     if (on && c < p.d) {
-      load8(h, base + c, p.h_f32, hv[n]);
-      if (y) load8(y, base + c, false, yv[n]);
+      hr[n].load(h, base + c);
+      if (y) yr[n].load(y, base + c);
     }
   }
+  float hv[NV][8];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) hr[n].get(hv[n]);
+  float s[1] = {0.0f};
   if (y) {
-    float sq = 1.0f;
+    float sq = p.out_scale;
+    if (p.gate == G_TOKEN && on) sq *= load1(gate, t, p.w_f32);
     if (w_post) {
 #pragma unroll
-      for (int n = 0; n < NV; ++n)
+      for (int n = 0; n < NV; ++n) {
+        float yv[8];
+        yr[n].get(yv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += yv[n][i] * yv[n][i];
-      row_sum<W, 1>(s, sh[slot], wave);
-      sq = rsqrtf(s[0] * p.inv_d + p.eps);
+        for (int i = 0; i < 8; ++i) s[0] += yv[i] * yv[i];
+      }
+      row_sum<W, 1>(s, sh[slot][0], wave);
+      sq *= rsqrtf(s[0] * p.inv_d + p.eps);
     }
-    sq *= p.out_scale;
-    if (p.gate == G_TOKEN && on) sq *= load1(gate, t, p.w_f32);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * 64 * W + lane) * 8;
       if (!on || c >= p.d) continue;
-      float m[8];
+      float m[8], w[8], yv[8];
+      yr[n].get(yv);
 #pragma unroll
       for (int i = 0; i < 8; ++i) m[i] = sq;
       if (w_post) {
-        float w[8];
-        load8(w_post, c, p.w_f32, w);
+        load_w8(w_post, c, p.w_f32, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) m[i] *= w[i];
       }
       if (p.gate == G_CHANNEL || p.gate == G_FULL) {
-        float w[8];
-        load8(gate, p.gate == G_FULL ? base + c : c, p.w_f32, w);
+        load_w8(gate, p.gate == G_FULL ? base + c : c, p.w_f32, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) m[i] *= w[i];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) hv[n][i] = p.res_scale * hv[n][i] + yv[n][i] * m[i];
-      store8(h_out, base + c, p.h_f32, hv[n]);
+      for (int i = 0; i < 8; ++i) hv[n][i] = p.res_scale * hv[n][i] + yv[i] * m[i];
+      store8<HF32>(h_out, base + c, hv[n]);
     }
   }
   if (!x) return;
@@ -140,128 +175,184 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 512) void norm_forward_kernel(NormAr
   for (int n = 0; n < NV; ++n)
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[0] += hv[n][i] * hv[n][i];
-  row_sum<W, 1>(s, sh[slot], wave);
+  row_sum<W, 1>(s, sh[slot][1], wave);
   const float sp = rsqrtf(s[0] * p.inv_d + p.eps);
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int c = (n * 64 * W + lane) * 8;
     if (!on || c >= p.d) continue;
     float w[8];
-    load8(w_pre, c, p.w_f32, w);
+    load_w8(w_pre, c, p.w_f32, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] *= hv[n][i] * sp;
-    store8(x, base + c, false, w);
+    store8<false>(x, base + c, w);
   }
 }
 
-// A block walks rows a grid apart and keeps the weights' gradients of its columns in registers;
-// they leave once, as partial sums that norm_reduce_kernel adds in a fixed order.
-template <int W, int NV>
-__global__ __launch_bounds__(W <= 4 ? 256 : 512) void norm_backward_kernel(
+// What one row of the backward pass reads, as it lies in memory
+template <int NV, bool HF32, bool Y, bool P>
+struct RowIn {
+  Raw8<HF32> h[NV], D[NV];
+  Raw8<false> g[NV], y[NV];
+};
+
+// A block walks rows a grid apart, each row's loads issued before the row before is worked on, and
+// keeps the weights and the sums for their gradients of its columns in registers; the sums leave
+// once, as partial sums that norm_reduce_kernel adds in a fixed order.
+//
+// With cwg = out_scale gate w_post of a channel (the token's gate apart, as gt), one sum serves the norm
+// behind the block and a channel's gate: A = sum_t gt D yh gives dw_post = out_scale gate A and
+// dgate = out_scale w_post A.
+template <int W, int NV, bool HF32, bool Y, bool P, bool FULL>
+__global__ __launch_bounds__(norm_threads(W)) void norm_backward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* __restrict__ h_out, const void* __restrict__ w_post,
     const void* __restrict__ gate, const void* __restrict__ w_pre, const void* dh_out, const uint16_t* __restrict__ dx,
     void* dh, uint16_t* __restrict__ dy, void* __restrict__ dgate, float* __restrict__ part, int64_t part_stride) {
-  constexpr int kRows = W <= 4 ? 4 / W : 1;
-  __shared__ float sh[kRows][4 * W];
+  constexpr int kRows = norm_threads(W) / (64 * W);
+  __shared__ float sh[kRows][2][3 * W];
   const int slot = threadIdx.x / (64 * W), lane = threadIdx.x % (64 * W), wave = lane >> 6;
-  float a_pre[NV][8], a_post[NV][8], a_gate[NV][8];
+  float a_pre[NV][8], a_post[NV][8], wp[NV][8], cwg[NV][8];
 #pragma unroll
-  for (int n = 0; n < NV; ++n)
+  for (int n = 0; n < NV; ++n) {
+    const int c = (n * 64 * W + lane) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a_pre[n][i] = a_post[n][i] = a_gate[n][i] = 0.0f;
-  const bool each = p.gate == G_CHANNEL || p.gate == G_FULL;  // a gate value of its own for each channel
+    for (int i = 0; i < 8; ++i) a_pre[n][i] = a_post[n][i] = wp[n][i] = 0.0f, cwg[n][i] = FULL ? 1.0f : p.out_scale;
+    if (c >= p.d) continue;
+    if (P) load_w8(w_pre, c, p.w_f32, wp[n]);
+    if (Y && w_post) {
+      float w[8];
+      load_w8(w_post, c, p.w_f32, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cwg[n][i] *= w[i];
+    }
+    if (Y && p.gate == G_CHANNEL) {
+      float w[8];
+      load_w8(gate, c, p.w_f32, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cwg[n][i] *= w[i];
+    }
+  }
   const int64_t step = (int64_t)gridDim.x * kRows;
+  RowIn<NV, HF32, Y, P> cur;
+  const auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int c = (n * 64 * W + lane) * 8;
+      const int64_t at = t * p.d + c;
+      cur.D[n].zero();
+      if (P) cur.h[n].zero(), cur.g[n].zero();
+      if (Y) cur.y[n].zero();
+      if (t < p.T && c < p.d) {
+        if (dh_out) cur.D[n].load(dh_out, at);
+        if (P) cur.h[n].load(h_out, at), cur.g[n].load(dx, at);
+        if (Y) cur.y[n].load(y, at);
+      }
+    }
+  };
+  constexpr bool kAhead = NV == 1;  // two rows of 16 values a lane do not fit 1024 threads' registers
+  if (kAhead) fetch((int64_t)blockIdx.x * kRows + slot);
   for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += step) {
     const int64_t t = t0 + slot;
     const bool on = t < p.T;
     const int64_t base = on ? t * p.d : 0;
-    float D[NV][8], hv[NV][8], yv[NV][8];
-    float s[3] = {0.0f, 0.0f, 0.0f};  // h'^2, h' w_pre dx, y^2
+    if (!kAhead) fetch(t);
+    const RowIn<NV, HF32, Y, P> in = cur;
+    if (kAhead && t0 + step < p.T) fetch(t + step);
+    float gt = 1.0f;
+    if (Y && p.gate == G_TOKEN && on) gt = load1(gate, t, p.w_f32);
+    constexpr int kS = (P ? 2 : 0) + (Y ? 1 : 0);
+    float s[kS];  // (h'^2, h' w_pre dx), (y^2)
+#pragma unroll
+    for (int q = 0; q < kS; ++q) s[q] = 0.0f;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const int c = (n * 64 * W + lane) * 8;
+      if (P) {
+        float h[8], g[8];
+        in.h[n].get(h);
+        in.g[n].get(g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) D[n][i] = hv[n][i] = yv[n][i] = 0.0f;
-      if (!on || c >= p.d) continue;
-      if (dh_out) load8(dh_out, base + c, p.h_f32, D[n]);
-      if (w_post) {
-        load8(y, base + c, false, yv[n]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[2] += yv[n][i] * yv[n][i];
+        for (int i = 0; i < 8; ++i) s[0] += h[i] * h[i], s[P ? 1 : 0] += h[i] * g[i] * wp[n][i];
       }
-      if (w_pre) {
-        float w[8], g[8];
-        load8(h_out, base + c, p.h_f32, hv[n]);
-        load8(dx, base + c, false, g);
-        load8(w_pre, c, p.w_f32, w);
+      if (Y) {
+        float v[8];
+        in.y[n].get(v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += hv[n][i] * hv[n][i], s[1] += hv[n][i] * (w[i] * g[i]);
+        for (int i = 0; i < 8; ++i) s[kS - 1] += v[i] * v[i];
       }
     }
-    row_sum<W, 3>(s, sh[slot], wave);
-    const float sp = rsqrtf(s[0] * p.inv_d + p.eps), sq = w_post ? rsqrtf(s[2] * p.inv_d + p.eps) : 1.0f;
-    const float mp = s[1] * p.inv_d * sp * sp * sp;
-    float gt = p.out_scale;
-    if (p.gate == G_TOKEN && on) gt *= load1(gate, t, p.w_f32);
-    float e[2] = {0.0f, 0.0f};  // y w_post gate D (or without the token's gate), for dy's mean and a token's dgate
+    row_sum<W, kS>(s, sh[slot][0], wave);
+    const float sp = P ? rsqrtf(s[0] * p.inv_d + p.eps) : 0.0f, mp = P ? s[1] * p.inv_d * sp * sp * sp : 0.0f;
+    const float sq = Y && w_post ? rsqrtf(s[kS - 1] * p.inv_d + p.eps) : 1.0f, sqg = sq * gt;
+    float D[NV][8];
+    float e[1] = {0.0f};  // D cwg y
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * 64 * W + lane) * 8;
-      if (!on || c >= p.d) continue;
-      if (w_pre) {
-        float w[8], g[8];
-        load8(dx, base + c, false, g);
-        load8(w_pre, c, p.w_f32, w);
+      in.D[n].get(D[n]);
+      if (P) {
+        float h[8], g[8];
+        in.h[n].get(h);
+        in.g[n].get(g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          a_pre[n][i] += g[i] * (hv[n][i] * sp);
-          D[n][i] += sp * (w[i] * g[i]) - hv[n][i] * mp;
+          a_pre[n][i] += h[i] * g[i] * sp;
+          D[n][i] += wp[n][i] * g[i] * sp;
+          D[n][i] -= h[i] * mp;
         }
       }
-      if (dh) {
+      const bool in_row = on && c < p.d;
+      if (dh && in_row) {
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = p.res_scale * D[n][i];
-        store8(dh, base + c, p.h_f32, o);
+        store8<HF32>(dh, base + c, o);
       }
-      if (!y) continue;
-      // hv: now gate * out_scale of each channel;  D: dn = out_scale gate D
-      if (!w_post) load8(y, base + c, false, yv[n]);
-      float w[8], gv[8], dg[8];
+      if (Y) {
+        float v[8];
+        in.y[n].get(v);
+        if (FULL) {
+          // D: w_post' dn with the channel's own gate; the gate's gradient has the value itself
+          float gv[8], dg[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 1.0f, gv[i] = gt;
-      if (w_post) load8(w_post, c, p.w_f32, w);
-      if (each) {
-        load8(gate, p.gate == G_FULL ? base + c : c, p.w_f32, gv);
+          for (int i = 0; i < 8; ++i) gv[i] = 0.0f;
+          if (in_row) load_w8(gate, base + c, p.w_f32, gv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) gv[i] *= p.out_scale;
+          for (int i = 0; i < 8; ++i) {
+            const float q = p.out_scale * D[n][i] * (v[i] * sq);
+            dg[i] = q * cwg[n][i];
+            a_post[n][i] += q * gv[i];
+            e[0] += dg[i] * gv[i];
+            D[n][i] *= p.out_scale * gv[i];
+          }
+          if (dgate && in_row) {
+            if (p.w_f32) store8<true>(dgate, base + c, dg);
+            else store8<false>(dgate, base + c, dg);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float q = D[n][i] * v[i];
+            a_post[n][i] += q * sqg;
+            e[0] += q * cwg[n][i];
+          }
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float yh = yv[n][i] * sq;
-        dg[i] = p.out_scale * D[n][i] * (w[i] * yh);
-        e[1] += dg[i];
-        D[n][i] *= gv[i];
-        a_post[n][i] += D[n][i] * yh;
-        D[n][i] *= w[i];
-        e[0] += D[n][i] * yh;
-        a_gate[n][i] += dg[i];
-      }
-      if (p.gate == G_FULL && dgate) store8(dgate, base + c, p.w_f32, dg);
     }
-    if (!y) continue;
-    row_sum<W, 2>(e, sh[slot], wave);
-    if (p.gate == G_TOKEN && dgate && on && lane == 0) store1(dgate, t, p.w_f32, e[1]);
+    if (!Y) continue;
+    row_sum<W, 1>(e, sh[slot][1], wave);
+    if (!FULL) e[0] *= sq;
+    if (p.gate == G_TOKEN && dgate && on && lane == 0) store1(dgate, t, p.w_f32, e[0]);
     if (!dy) continue;
-    const float mq = w_post ? e[0] * p.inv_d * sq : 0.0f;
+    const float mq = w_post ? -e[0] * p.inv_d * sq * sqg : 0.0f;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * 64 * W + lane) * 8;
       if (!on || c >= p.d) continue;
-      float o[8];
+      float v[8], o[8];
+      in.y[n].get(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = sq * (D[n][i] - yv[n][i] * mq);
-      store8(dy, base + c, false, o);
+      for (int i = 0; i < 8; ++i) o[i] = D[n][i] * cwg[n][i] * sqg + v[i] * mq;
+      store8<false>(dy, base + c, o);
     }
   }
   if (!part) return;
@@ -270,31 +361,40 @@ __global__ __launch_bounds__(W <= 4 ? 256 : 512) void norm_backward_kernel(
   for (int n = 0; n < NV; ++n) {
     const int c = (n * 64 * W + lane) * 8;
     if (c >= p.d) continue;
-    store8(part, row * p.d + c, true, a_pre[n]);
-    store8(part, part_stride + row * p.d + c, true, a_post[n]);
-    if (p.gate == G_CHANNEL) store8(part, 2 * part_stride + row * p.d + c, true, a_gate[n]);
+    if (P) store8<true>(part, row * p.d + c, a_pre[n]);
+    if (Y) store8<true>(part, part_stride + row * p.d + c, a_post[n]);
   }
 }
 
-// out[q][c] = sum over rows of part[q][row][c]: 16 waves share the rows of 64 columns.
-__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restrict__ part, int64_t part_stride, int rows,
-                                                           int d, bool f32, void* o0, void* o1, void* o2) {
+// Sums over rows of the partial sums, 16 waves sharing the rows of 64 columns: of part[0] for dw_pre,
+// of part[1] for dw_post and a channel gate's gradient (out_scale gate A and out_scale w_post A; where
+// the rows' own gates are in the sum already, dw_post alone).
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(NormArgs p, const float* __restrict__ part,
+                                                           int64_t part_stride, int rows, int first,
+                                                           const void* w_post, const void* gate, void* dw_pre,
+                                                           void* dw_post, void* dgate) {
   __shared__ float sh[16][64];
-  void* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
-  if (!out) return;
+  const int which = first + blockIdx.y;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
-  const float* src = part + (int64_t)blockIdx.y * part_stride;
+  const float* src = part + which * part_stride;
   float a = 0.0f;
+  if (c < p.d) {
 #pragma unroll 8
-  for (int r = wv; r < rows; r += 16)
-    if (c < d) a += src[(int64_t)r * d + c];
+    for (int r = wv; r < rows; r += 16) a += src[(int64_t)r * p.d + c];
+  }
   sh[wv][lane] = a;
   __syncthreads();
-  if (wv == 0 && c < d) {
+  if (wv != 0 || c >= p.d) return;
 #pragma unroll
-    for (int w = 1; w < 16; ++w) a += sh[w][lane];
-    store1(out, c, f32, a);
+  for (int w = 1; w < 16; ++w) a += sh[w][lane];
+  if (which == 0) {
+    store1(dw_pre, c, p.w_f32, a);
+    return;
   }
+  float by = p.gate == G_FULL ? 1.0f : p.out_scale;
+  if (dgate) store1(dgate, c, p.w_f32, (w_post && rows ? load1(w_post, c, p.w_f32) : 1.0f) * p.out_scale * a);
+  if (p.gate == G_CHANNEL && rows) by *= load1(gate, c, p.w_f32);
+  if (dw_post) store1(dw_post, c, p.w_f32, by * a);
 }
 
 // waves a row and 8-value vectors a lane for rows of d values
@@ -303,31 +403,35 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restri
     if ((d) <= 512) { CALL(1, 1); }         \
     else if ((d) <= 1024) { CALL(2, 1); }   \
     else if ((d) <= 2048) { CALL(4, 1); }   \
-    else if ((d) <= 4096) { CALL(4, 2); }   \
-    else if ((d) <= 8192) { CALL(4, 4); }   \
-    else { CALL(8, 4); }                    \
+    else if ((d) <= 4096) { CALL(8, 1); }   \
+    else if ((d) <= 8192) { CALL(16, 1); }  \
+    else { CALL(16, 2); }                   \
   } while (0)
 
 int norm_rows_per_block(int d) { return d <= 512 ? 4 : d <= 1024 ? 2 : 1; }
 
+// Blocks of the backward pass: two a compute unit of 4 waves, fewer of more waves
 int norm_bwd_blocks(int64_t T, int d) {
   const int64_t b = (T + norm_rows_per_block(d) - 1) / norm_rows_per_block(d);
-  return (int)(b < 1024 ? b : 1024);
+  const int64_t most = d <= 4096 ? 512 : 256;
+  return (int)(b < most ? b : most);
 }
 
 }  // namespace
 
-size_t norm_ws_bytes(int64_t T, int d, int gate) {
-  const int64_t rows = (int64_t)norm_bwd_blocks(T, d) * norm_rows_per_block(d);
-  return (size_t)((gate == G_CHANNEL ? 3 : 2) * rows * d * 4);
+size_t norm_ws_bytes(int64_t T, int d) {
+  return (size_t)(2 * (int64_t)norm_bwd_blocks(T, d) * norm_rows_per_block(d) * d * 4);
 }
 
 hipError_t launch_norm_forward(const NormArgs& p, const uint16_t* y, const void* h, const void* w_post,
                                const void* gate, const void* w_pre, void* h_out, uint16_t* x, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
   const unsigned blocks = (unsigned)((p.T + norm_rows_per_block(p.d) - 1) / norm_rows_per_block(p.d));
-#define MOE_NORM_CALL(W, NV) \
-  norm_forward_kernel<W, NV><<<blocks, W <= 4 ? 256 : 512, 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x)
+#define MOE_NORM_CALL(W, NV)                                                                                       \
+  if (p.h_f32)                                                                                                     \
+    norm_forward_kernel<W, NV, true><<<blocks, norm_threads(W), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x);  \
+  else                                                                                                             \
+    norm_forward_kernel<W, NV, false><<<blocks, norm_threads(W), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x)
   MOE_NORM_DISPATCH(p.d, MOE_NORM_CALL);
 #undef MOE_NORM_CALL
   return hipGetLastError();
@@ -340,19 +444,32 @@ hipError_t launch_norm_backward(const NormArgs& p, const uint16_t* y, const void
   const int rows = blocks * norm_rows_per_block(p.d);
   const int64_t stride = (int64_t)rows * p.d;
   void* dg = p.gate == G_CHANNEL ? dgate : nullptr;
-  const bool sums = dw_pre || dw_post || dg;
+  const bool pre = dw_pre, post = dw_post || dg;
   if (p.T > 0) {
-#define MOE_NORM_CALL(W, NV)                                                                                      \
-  norm_backward_kernel<W, NV><<<blocks, W <= 4 ? 256 : 512, 0, st>>>(p, y, h_out, w_post, gate, w_pre, dh_out, dx, \
-                                                                     dh, dy, dgate, sums ? part : nullptr, stride)
+    const bool full = y && p.gate == G_FULL;
+#define MOE_NORM_RUN(W, NV, H, Y, P, F)                                                                              \
+  norm_backward_kernel<W, NV, H, Y, P, F><<<blocks, norm_threads(W), 0, st>>>(p, y, h_out, w_post, gate, w_pre, dh_out, \
+                                                                              dx, dh, dy, dgate,                       \
+                                                                              pre || post ? part : nullptr, stride)
+#define MOE_NORM_FORM(W, NV, H)                                 \
+  if (!y) MOE_NORM_RUN(W, NV, H, false, true, false);           \
+  else if (w_pre && full) MOE_NORM_RUN(W, NV, H, true, true, true); \
+  else if (w_pre) MOE_NORM_RUN(W, NV, H, true, true, false);    \
+  else if (full) MOE_NORM_RUN(W, NV, H, true, false, true);     \
+  else MOE_NORM_RUN(W, NV, H, true, false, false)
+#define MOE_NORM_CALL(W, NV)                   \
+  if (p.h_f32) { MOE_NORM_FORM(W, NV, true); } \
+  else { MOE_NORM_FORM(W, NV, false); }
     MOE_NORM_DISPATCH(p.d, MOE_NORM_CALL);
 #undef MOE_NORM_CALL
+#undef MOE_NORM_FORM
+#undef MOE_NORM_RUN
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (sums)
-    norm_reduce_kernel<<<dim3((p.d + 63) / 64, 3), 1024, 0, st>>>(part, stride, p.T > 0 ? rows : 0, p.d, p.w_f32,
-                                                                  dw_pre, dw_post, dg);
+  if (pre || post)
+    norm_reduce_kernel<<<dim3((p.d + 63) / 64, pre && post ? 2 : 1), 1024, 0, st>>>(
+        p, part, stride, p.T > 0 ? rows : 0, pre ? 0 : 1, w_post, gate, dw_pre, dw_post, dg);
   return hipGetLastError();
 }
 

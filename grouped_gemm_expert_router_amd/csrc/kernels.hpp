@@ -185,7 +185,7 @@ struct NormArgs {
   bool h_f32, w_f32;
   float eps, inv_d, res_scale, out_scale;
 };
-size_t norm_ws_bytes(int64_t T, int d, int gate);
+size_t norm_ws_bytes(int64_t T, int d);
 hipError_t launch_norm_forward(const NormArgs& p, const uint16_t* y, const void* h, const void* w_post,
                                const void* gate, const void* w_pre, void* h_out, uint16_t* x, hipStream_t st);
 hipError_t launch_norm_backward(const NormArgs& p, const uint16_t* y, const void* h_out, const void* w_post,
