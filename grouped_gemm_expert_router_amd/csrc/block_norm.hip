@@ -83,13 +83,25 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Sums of K values over a row's W waves, the same in every lane.  sh: [K][W] of the row and of this
-// sum (the next one uses another, so one barrier is enough); the block's rows reach it together.
-template <int W, int K>
+// Rows are spread over LR lanes of 8 values each, NV times: a part of a wave for short rows (heads), up
+// to 16 waves for long ones; a block of 256 threads or one row holds kRows rows.
+constexpr int norm_threads(int LR) { return LR <= 256 ? 256 : LR; }
+
+// Sums of K values over a row's LR lanes, the same in every lane.  sh: [K][LR / 64] of the row and of
+// this sum (the next one uses another, so one barrier is enough); the block's rows reach it together.
+template <int LR, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
 #pragma unroll
-  for (int q = 0; q < K; ++q) v[q] = wave_sum_dpp(v[q]);
-  if (W > 1) {
+  for (int q = 0; q < K; ++q) {
+    if (LR >= 64) {
+      v[q] = wave_sum_dpp(v[q]);
+    } else {
+      v[q] = row16_sum(v[q]);
+      if (LR == 32) v[q] += __shfl_xor(v[q], 16, 64);
+    }
+  }
+  if (LR > 64) {
+    constexpr int W = LR / 64;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
       for (int q = 0; q < K; ++q) sh[q * W + wave] = v[q];
@@ -103,16 +115,14 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
   }
 }
 
-constexpr int norm_threads(int W) { return W <= 4 ? 256 : 64 * W; }
-
-// W waves a row, NV times 8 values a lane: the row stays in registers between its passes.
-template <int W, int NV, bool HF32>
-__global__ __launch_bounds__(norm_threads(W)) void norm_forward_kernel(
+// The row stays in registers between its passes.
+template <int LR, int NV, bool HF32>
+__global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* h, const void* __restrict__ w_post,
     const void* __restrict__ gate, const void* __restrict__ w_pre, void* h_out, uint16_t* __restrict__ x) {
-  constexpr int kRows = norm_threads(W) / (64 * W);
+  constexpr int kRows = norm_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
   __shared__ float sh[kRows][2][W];
-  const int slot = threadIdx.x / (64 * W), lane = threadIdx.x % (64 * W), wave = lane >> 6;
+  const int slot = threadIdx.x / LR, lane = threadIdx.x % LR, wave = lane >> 6;
   const int64_t t = (int64_t)blockIdx.x * kRows + slot;
   const bool on = t < p.T;
   const int64_t base = on ? t * p.d : 0;
@@ -120,7 +130,7 @@ __global__ __launch_bounds__(norm_threads(W)) void norm_forward_kernel(
   Raw8<HF32> hr[NV];
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    const int c = (n * 64 * W + lane) * 8;
+    const int c = (n * LR + lane) * 8;
     hr[n].zero();
     yr[n].zero();
     if (on && c < p.d) {
@@ -143,12 +153,12 @@ __global__ __launch_bounds__(norm_threads(W)) void norm_forward_kernel(
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[0] += yv[i] * yv[i];
       }
-      row_sum<W, 1>(s, sh[slot][0], wave);
+      row_sum<LR, 1>(s, sh[slot][0], wave);
       sq *= rsqrtf(s[0] * p.inv_d + p.eps);
     }
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const int c = (n * 64 * W + lane) * 8;
+      const int c = (n * LR + lane) * 8;
       if (!on || c >= p.d) continue;
       float m[8], w[8], yv[8];
       yr[n].get(yv);
@@ -175,11 +185,11 @@ __global__ __launch_bounds__(norm_threads(W)) void norm_forward_kernel(
   for (int n = 0; n < NV; ++n)
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[0] += hv[n][i] * hv[n][i];
-  row_sum<W, 1>(s, sh[slot][1], wave);
+  row_sum<LR, 1>(s, sh[slot][1], wave);
   const float sp = rsqrtf(s[0] * p.inv_d + p.eps);
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    const int c = (n * 64 * W + lane) * 8;
+    const int c = (n * LR + lane) * 8;
     if (!on || c >= p.d) continue;
     float w[8];
     load_w8(w_pre, c, p.w_f32, w);
@@ -203,18 +213,18 @@ struct RowIn {
 // With cwg = out_scale gate w_post of a channel (the token's gate apart, as gt), one sum serves the norm
 // behind the block and a channel's gate: A = sum_t gt D yh gives dw_post = out_scale gate A and
 // dgate = out_scale w_post A.
-template <int W, int NV, bool HF32, bool Y, bool P, bool FULL>
-__global__ __launch_bounds__(norm_threads(W)) void norm_backward_kernel(
+template <int LR, int NV, bool HF32, bool Y, bool P, bool FULL>
+__global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* __restrict__ h_out, const void* __restrict__ w_post,
     const void* __restrict__ gate, const void* __restrict__ w_pre, const void* dh_out, const uint16_t* __restrict__ dx,
     void* dh, uint16_t* __restrict__ dy, void* __restrict__ dgate, float* __restrict__ part, int64_t part_stride) {
-  constexpr int kRows = norm_threads(W) / (64 * W);
+  constexpr int kRows = norm_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
   __shared__ float sh[kRows][2][3 * W];
-  const int slot = threadIdx.x / (64 * W), lane = threadIdx.x % (64 * W), wave = lane >> 6;
+  const int slot = threadIdx.x / LR, lane = threadIdx.x % LR, wave = lane >> 6;
   float a_pre[NV][8], a_post[NV][8], wp[NV][8], cwg[NV][8];
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    const int c = (n * 64 * W + lane) * 8;
+    const int c = (n * LR + lane) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) a_pre[n][i] = a_post[n][i] = wp[n][i] = 0.0f, cwg[n][i] = FULL ? 1.0f : p.out_scale;
     if (c >= p.d) continue;
@@ -237,7 +247,7 @@ __global__ __launch_bounds__(norm_threads(W)) void norm_backward_kernel(
   const auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const int c = (n * 64 * W + lane) * 8;
+      const int c = (n * LR + lane) * 8;
       const int64_t at = t * p.d + c;
       cur.D[n].zero();
       if (P) cur.h[n].zero(), cur.g[n].zero();
@@ -280,14 +290,14 @@ __global__ __launch_bounds__(norm_threads(W)) void norm_backward_kernel(
         for (int i = 0; i < 8; ++i) s[kS - 1] += v[i] * v[i];
       }
     }
-    row_sum<W, kS>(s, sh[slot][0], wave);
+    row_sum<LR, kS>(s, sh[slot][0], wave);
     const float sp = P ? rsqrtf(s[0] * p.inv_d + p.eps) : 0.0f, mp = P ? s[1] * p.inv_d * sp * sp * sp : 0.0f;
     const float sq = Y && w_post ? rsqrtf(s[kS - 1] * p.inv_d + p.eps) : 1.0f, sqg = sq * gt;
     float D[NV][8];
     float e[1] = {0.0f};  // D cwg y
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const int c = (n * 64 * W + lane) * 8;
+      const int c = (n * LR + lane) * 8;
       in.D[n].get(D[n]);
       if (P) {
         float h[8], g[8];
@@ -339,14 +349,14 @@ __global__ __launch_bounds__(norm_threads(W)) void norm_backward_kernel(
       }
     }
     if (!Y) continue;
-    row_sum<W, 1>(e, sh[slot][1], wave);
+    row_sum<LR, 1>(e, sh[slot][1], wave);
     if (!FULL) e[0] *= sq;
     if (p.gate == G_TOKEN && dgate && on && lane == 0) store1(dgate, t, p.w_f32, e[0]);
     if (!dy) continue;
     const float mq = w_post ? -e[0] * p.inv_d * sq * sqg : 0.0f;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const int c = (n * 64 * W + lane) * 8;
+      const int c = (n * LR + lane) * 8;
       if (!on || c >= p.d) continue;
       float v[8], o[8];
       in.y[n].get(v);
@@ -356,13 +366,33 @@ __global__ __launch_bounds__(norm_threads(W)) void norm_backward_kernel(
     }
   }
   if (!part) return;
-  const int64_t row = (int64_t)blockIdx.x * kRows + slot;
+  if (kRows == 1) {
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int c = (n * 64 * W + lane) * 8;
-    if (c >= p.d) continue;
-    if (P) store8<true>(part, row * p.d + c, a_pre[n]);
-    if (Y) store8<true>(part, part_stride + row * p.d + c, a_post[n]);
+    for (int n = 0; n < NV; ++n) {
+      const int c = (n * LR + lane) * 8;
+      if (c >= p.d) continue;
+      if (P) store8<true>(part, (int64_t)blockIdx.x * p.d + c, a_pre[n]);
+      if (Y) store8<true>(part, part_stride + (int64_t)blockIdx.x * p.d + c, a_post[n]);
+    }
+    return;
+  }
+  // the block's rows, in order (NV is 1 here)
+  __shared__ float red[kRows > 1 ? 2 * 2048 : 1];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (P) red[slot * LR * 8 + lane * 8 + i] = a_pre[0][i];
+    if (Y) red[2048 + slot * LR * 8 + lane * 8 + i] = a_post[0][i];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.d; c += norm_threads(LR)) {
+    float u = 0.0f, v = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (P) u += red[r * LR * 8 + c];
+      if (Y) v += red[2048 + r * LR * 8 + c];
+    }
+    if (P) part[(int64_t)blockIdx.x * p.d + c] = u;
+    if (Y) part[part_stride + (int64_t)blockIdx.x * p.d + c] = v;
   }
 }
 
@@ -397,18 +427,20 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormArgs p, const flo
   if (dw_post) store1(dw_post, c, p.w_f32, by * a);
 }
 
-// waves a row and 8-value vectors a lane for rows of d values
-#define MOE_NORM_DISPATCH(d, CALL)          \
-  do {                                      \
-    if ((d) <= 512) { CALL(1, 1); }         \
-    else if ((d) <= 1024) { CALL(2, 1); }   \
-    else if ((d) <= 2048) { CALL(4, 1); }   \
-    else if ((d) <= 4096) { CALL(8, 1); }   \
-    else if ((d) <= 8192) { CALL(16, 1); }  \
-    else { CALL(16, 2); }                   \
+// lanes a row and 8-value vectors a lane for rows of d values
+#define MOE_NORM_DISPATCH(d, CALL)           \
+  do {                                       \
+    if ((d) <= 128) { CALL(16, 1); }         \
+    else if ((d) <= 256) { CALL(32, 1); }    \
+    else if ((d) <= 512) { CALL(64, 1); }    \
+    else if ((d) <= 1024) { CALL(128, 1); }  \
+    else if ((d) <= 2048) { CALL(256, 1); }  \
+    else if ((d) <= 4096) { CALL(512, 1); }  \
+    else if ((d) <= 8192) { CALL(1024, 1); } \
+    else { CALL(1024, 2); }                  \
   } while (0)
 
-int norm_rows_per_block(int d) { return d <= 512 ? 4 : d <= 1024 ? 2 : 1; }
+int norm_rows_per_block(int d) { return d <= 128 ? 16 : d <= 256 ? 8 : d <= 512 ? 4 : d <= 1024 ? 2 : 1; }
 
 // Blocks of the backward pass: two a compute unit of 4 waves, fewer of more waves
 int norm_bwd_blocks(int64_t T, int d) {
@@ -420,18 +452,18 @@ int norm_bwd_blocks(int64_t T, int d) {
 }  // namespace
 
 size_t norm_ws_bytes(int64_t T, int d) {
-  return (size_t)(2 * (int64_t)norm_bwd_blocks(T, d) * norm_rows_per_block(d) * d * 4);
+  return (size_t)(2 * (int64_t)norm_bwd_blocks(T, d) * d * 4);
 }
 
 hipError_t launch_norm_forward(const NormArgs& p, const uint16_t* y, const void* h, const void* w_post,
                                const void* gate, const void* w_pre, void* h_out, uint16_t* x, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
   const unsigned blocks = (unsigned)((p.T + norm_rows_per_block(p.d) - 1) / norm_rows_per_block(p.d));
-#define MOE_NORM_CALL(W, NV)                                                                                       \
+#define MOE_NORM_CALL(LR, NV)                                                                                       \
   if (p.h_f32)                                                                                                     \
-    norm_forward_kernel<W, NV, true><<<blocks, norm_threads(W), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x);  \
+    norm_forward_kernel<LR, NV, true><<<blocks, norm_threads(LR), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x);  \
   else                                                                                                             \
-    norm_forward_kernel<W, NV, false><<<blocks, norm_threads(W), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x)
+    norm_forward_kernel<LR, NV, false><<<blocks, norm_threads(LR), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x)
   MOE_NORM_DISPATCH(p.d, MOE_NORM_CALL);
 #undef MOE_NORM_CALL
   return hipGetLastError();
@@ -441,25 +473,24 @@ hipError_t launch_norm_backward(const NormArgs& p, const uint16_t* y, const void
                                 const void* gate, const void* w_pre, const void* dh_out, const uint16_t* dx, void* dh,
                                 uint16_t* dy, void* dw_post, void* dgate, void* dw_pre, float* part, hipStream_t st) {
   const int blocks = norm_bwd_blocks(p.T, p.d);
-  const int rows = blocks * norm_rows_per_block(p.d);
-  const int64_t stride = (int64_t)rows * p.d;
+  const int64_t stride = (int64_t)blocks * p.d;
   void* dg = p.gate == G_CHANNEL ? dgate : nullptr;
   const bool pre = dw_pre, post = dw_post || dg;
   if (p.T > 0) {
     const bool full = y && p.gate == G_FULL;
-#define MOE_NORM_RUN(W, NV, H, Y, P, F)                                                                              \
-  norm_backward_kernel<W, NV, H, Y, P, F><<<blocks, norm_threads(W), 0, st>>>(p, y, h_out, w_post, gate, w_pre, dh_out, \
+#define MOE_NORM_RUN(LR, NV, H, Y, P, F)                                                                              \
+  norm_backward_kernel<LR, NV, H, Y, P, F><<<blocks, norm_threads(LR), 0, st>>>(p, y, h_out, w_post, gate, w_pre, dh_out, \
                                                                               dx, dh, dy, dgate,                       \
                                                                               pre || post ? part : nullptr, stride)
-#define MOE_NORM_FORM(W, NV, H)                                 \
-  if (!y) MOE_NORM_RUN(W, NV, H, false, true, false);           \
-  else if (w_pre && full) MOE_NORM_RUN(W, NV, H, true, true, true); \
-  else if (w_pre) MOE_NORM_RUN(W, NV, H, true, true, false);    \
-  else if (full) MOE_NORM_RUN(W, NV, H, true, false, true);     \
-  else MOE_NORM_RUN(W, NV, H, true, false, false)
-#define MOE_NORM_CALL(W, NV)                   \
-  if (p.h_f32) { MOE_NORM_FORM(W, NV, true); } \
-  else { MOE_NORM_FORM(W, NV, false); }
+#define MOE_NORM_FORM(LR, NV, H)                                 \
+  if (!y) MOE_NORM_RUN(LR, NV, H, false, true, false);           \
+  else if (w_pre && full) MOE_NORM_RUN(LR, NV, H, true, true, true); \
+  else if (w_pre) MOE_NORM_RUN(LR, NV, H, true, true, false);    \
+  else if (full) MOE_NORM_RUN(LR, NV, H, true, false, true);     \
+  else MOE_NORM_RUN(LR, NV, H, true, false, false)
+#define MOE_NORM_CALL(LR, NV)                   \
+  if (p.h_f32) { MOE_NORM_FORM(LR, NV, true); } \
+  else { MOE_NORM_FORM(LR, NV, false); }
     MOE_NORM_DISPATCH(p.d, MOE_NORM_CALL);
 #undef MOE_NORM_CALL
 #undef MOE_NORM_FORM
@@ -469,7 +500,7 @@ hipError_t launch_norm_backward(const NormArgs& p, const uint16_t* y, const void
   }
   if (pre || post)
     norm_reduce_kernel<<<dim3((p.d + 63) / 64, pre && post ? 2 : 1), 1024, 0, st>>>(
-        p, part, stride, p.T > 0 ? rows : 0, pre ? 0 : 1, w_post, gate, dw_pre, dw_post, dg);
+        p, part, stride, p.T > 0 ? blocks : 0, pre ? 0 : 1, w_post, gate, dw_pre, dw_post, dg);
   return hipGetLastError();
 }
 
