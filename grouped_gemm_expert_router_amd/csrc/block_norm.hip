@@ -85,7 +85,7 @@ __device__ __forceinline__ void lds_barrier() {
 
 // Rows are spread over LR lanes of 8 values each, NV times: a part of a wave for short rows (heads), up
 // to 16 waves for long ones; a block of 256 threads or one row holds kRows rows.
-constexpr int norm_threads(int LR) { return LR <= 256 ? 256 : LR; }
+constexpr int norm_threads(int LR) { return LR <= 128 ? 256 : LR; }
 
 // Sums of K values over a row's LR lanes, the same in every lane.  sh: [K][LR / 64] of the row and of
 // this sum (the next one uses another, so one barrier is enough); the block's rows reach it together.
@@ -427,26 +427,42 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormArgs p, const flo
   if (dw_post) store1(dw_post, c, p.w_f32, by * a);
 }
 
-// lanes a row and 8-value vectors a lane for rows of d values
-#define MOE_NORM_DISPATCH(d, CALL)           \
-  do {                                       \
-    if ((d) <= 128) { CALL(16, 1); }         \
-    else if ((d) <= 256) { CALL(32, 1); }    \
-    else if ((d) <= 512) { CALL(64, 1); }    \
-    else if ((d) <= 1024) { CALL(128, 1); }  \
-    else if ((d) <= 2048) { CALL(256, 1); }  \
-    else if ((d) <= 4096) { CALL(512, 1); }  \
-    else if ((d) <= 8192) { CALL(1024, 1); } \
-    else { CALL(1024, 2); }                  \
+// Lanes of a row of d values, the fewest that hold it 8 values each
+int norm_lanes(int d) {
+  for (const int lanes : {16, 32, 64, 128, 192, 256, 384, 512, 768})
+    if (d <= 8 * lanes) return lanes;
+  return 1024;
+}
+
+#define MOE_NORM_DISPATCH(d, CALL)                 \
+  do {                                             \
+    switch (norm_lanes(d)) {                       \
+      case 16: { CALL(16, 1); } break;             \
+      case 32: { CALL(32, 1); } break;             \
+      case 64: { CALL(64, 1); } break;             \
+      case 128: { CALL(128, 1); } break;           \
+      case 192: { CALL(192, 1); } break;           \
+      case 256: { CALL(256, 1); } break;           \
+      case 384: { CALL(384, 1); } break;           \
+      case 512: { CALL(512, 1); } break;           \
+      case 768: { CALL(768, 1); } break;           \
+      default:                                     \
+        if ((d) <= 8 * 1024) { CALL(1024, 1); }    \
+        else { CALL(1024, 2); }                    \
+    }                                              \
   } while (0)
 
-int norm_rows_per_block(int d) { return d <= 128 ? 16 : d <= 256 ? 8 : d <= 512 ? 4 : d <= 1024 ? 2 : 1; }
+int norm_rows_per_block(int d) { return norm_threads(norm_lanes(d)) / norm_lanes(d); }
 
-// Blocks of the backward pass: two a compute unit of 4 waves, fewer of more waves
+// Blocks of the backward pass: 6 to 12 waves a compute unit, each with a row's loads ahead.  More of them
+// write more partial sums and read memory in smaller pieces (16384 rows of 2048: 2 a unit 78 us, 3 80, 4
+// 85; 4099 of 7168 in fp32: 1 a unit 105 us, 2 112); where over an eighth of the lanes idle, three
+// 256-thread blocks hold what two full ones would (46603 rows of 720: 2 a unit 85 us, 3 82).
 int norm_bwd_blocks(int64_t T, int d) {
+  const int lanes = norm_lanes(d);
+  const int per_cu = lanes >= 384 ? 1 : lanes == 256 ? 2 : lanes == 192 ? 3 : d >= 7 * lanes ? 2 : 3;
   const int64_t b = (T + norm_rows_per_block(d) - 1) / norm_rows_per_block(d);
-  const int64_t most = d <= 4096 ? 512 : 256;
-  return (int)(b < most ? b : most);
+  return (int)(b < 256 * per_cu ? b : 256 * per_cu);
 }
 
 }  // namespace

@@ -113,8 +113,9 @@ def check_backward(c, h_out, o, dh_out=True):
         assert_close(n, t, g[n], 2.0 ** -15 * s[n] + HALF[types[n]] * (np.abs(g[n]) + 2.0 ** -15 * s[n]))
 
 
-SHAPES = [(1, 8), (1, 2048), (3, 16), (5, 504), (7, 512), (130, 520), (4, 1024), (9, 1032), (33, 2048), (6, 2056),
-          (5, 4096), (3, 4104), (2, 7168), (2, 8192), (2, 8200), (1, 16384)]
+SHAPES = [(1, 8), (1, 2048), (3, 16), (40, 128), (33, 136), (9, 256), (19, 264), (5, 504), (7, 512), (130, 520), (4, 1024),
+          (9, 1032), (3, 1536), (4, 1544), (33, 2048), (6, 2056), (4, 3000), (3, 3600), (5, 4096), (3, 4104), (2, 6144),
+          (2, 6152), (2, 7168), (2, 8192), (2, 8200), (1, 16384)]
 
 
 @pytest.mark.parametrize("T,d", SHAPES)
@@ -128,12 +129,12 @@ def test_shapes(T, d):
         check_backward(c, h_out, backward(c, h_out))
 
 
-@pytest.mark.parametrize("gate", list(KINDS))
-@pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True), (False, False), (None, True)])
+FORMS = [(g, post, pre) for g in KINDS for post, pre in [(True, True), (True, False), (False, True), (False, False)]]
+
+
+@pytest.mark.parametrize("gate,post,pre", FORMS + [(None, None, True)])   # a gate needs the block's output
 @pytest.mark.parametrize("h,w", [(BF16, BF16), (F32, BF16), (BF16, F32), (F32, F32)])
 def test_forms(h, w, post, pre, gate):
-    if post is None and gate is not None:
-        pytest.skip("a gate needs the block's output")
     print(f"[case] norm form {h} {w} post={post} pre={pre} gate={gate}", flush=True)
     for d in (136, 1536):
         c = make(37, d, h, w, gate, post, pre, seed=7, res=0.75, out=1.5)
@@ -158,7 +159,7 @@ def test_forms(h, w, post, pre, gate):
 
 def test_many_rows_sum_in_a_fixed_order():
     """More rows than blocks walk at once; weights' gradients bitwise the same from run to run."""
-    for T, d in ((9001, 64), (2600, 1024), (2311, 2048)):
+    for T, d in ((20001, 64), (9001, 200), (2600, 1024), (2311, 2048), (700, 4096), (600, 8000)):
         print(f"[case] norm rows T={T} d={d}", flush=True)
         c = make(T, d, BF16, F32, "channel", seed=T)
         h_out, x = forward(c)
