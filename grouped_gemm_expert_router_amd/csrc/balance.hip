@@ -63,7 +63,7 @@ int balance_wide(int64_t T, int64_t E, int64_t S) {
   const int64_t rows = T > 0 ? (T + balance_tile(T) - 1) / balance_tile(T) / S + 1 : 1;
   int w = 1;
   while (w * 64 < E) w *= 2;
-  return rows * w <= 512 ? w : 1;
+  return rows * w <= 1100 ? w : 1;
 }
 
 // Last group whose first token is at or before t (-1: none).
@@ -95,6 +95,38 @@ __device__ __forceinline__ void load_row(const float* row, int E, int l, float f
   }
 }
 
+// Where a tile that is the whole batch, one group, puts its results (counts NULL: it is not)
+struct BalOut {
+  int32_t* counts;
+  int32_t* tokens;
+  float* losses;
+};
+
+// The losses of a batch that one block has seen whole.
+template <int kCols>
+__device__ __forceinline__ void whole_losses(const float (&shP)[4][kCols], const int32_t (&hist)[kCols],
+                                             const int32_t (&sh_n)[4], const float (&sh_z)[4], int E, int k,
+                                             const BalOut& o) {
+  __shared__ double sh[4];
+  double dot = 0.0;
+  for (int c = threadIdx.x; c < E; c += kBalThreads) {
+    o.counts[c] = hist[c];
+    dot += (double)((shP[0][c] + shP[1][c]) + (shP[2][c] + shP[3][c])) * (double)hist[c];
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) dot += __shfl_xor(dot, m, 64);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = dot;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  const int32_t n = sh_n[0] + sh_n[1] + sh_n[2] + sh_n[3];
+  dot = (sh[0] + sh[1]) + (sh[2] + sh[3]);
+  const double z = ((double)sh_z[0] + (double)sh_z[1]) + ((double)sh_z[2] + (double)sh_z[3]);
+  o.losses[0] = n > 0 ? (float)(dot * (double)E / ((double)k * (double)n * (double)n)) : 0.0f;
+  o.losses[1] = n > 0 ? (float)(z / n) : 0.0f;
+  o.tokens[0] = o.tokens[1] = n;
+  o.tokens[2] = n > 0;
+}
+
 // One block per tile of consecutive tokens, kL lanes per token, U tokens of a lane group in flight;
 // each lane keeps the sums of p of its own columns.  A tile is cut where a group ends; the piece of
 // tile b in group g has the slot b + g, which no other piece has (both grow along the tokens).
@@ -102,7 +134,7 @@ template <int V, int N>
 __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
     const int32_t* __restrict__ goff, int T, int E, int k, int S, int tile, float* __restrict__ lse_out,
-    float* __restrict__ Pp, int32_t* __restrict__ Cp, int32_t* __restrict__ np, float* __restrict__ zp) {
+    float* __restrict__ Pp, int32_t* __restrict__ Cp, int32_t* __restrict__ np, float* __restrict__ zp, BalOut whole) {
   constexpr int kCols = V * N * kL;
   constexpr int U = V * N <= 16 ? 2 : 1;
   __shared__ float shP[4][kCols];
@@ -198,6 +230,10 @@ __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
         if (l == 0) sh_n[wv] = cnt, sh_z[wv] = zs;
       }
       __syncthreads();
+      if (whole.counts) {
+        whole_losses(shP, hist, sh_n, sh_z, E, k, whole);
+        return;
+      }
       const int64_t slot = (int64_t)blockIdx.x + g;
       for (int c = tid; c < E; c += kBalThreads) {
         Pp[slot * E + c] = (shP[0][c] + shP[1][c]) + (shP[2][c] + shP[3][c]);
@@ -390,7 +426,8 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
       const int col = (n * kL + l) * V;
       if (col >= E) continue;
       if (V == 4)
-        *(float4*)(d_out + row + col) = make_float4(d[n * V], d[n * V + 1], d[n * V + 2], d[n * V + 3]);
+        __builtin_nontemporal_store(f32x4_t{d[n * V], d[n * V + 1], d[n * V + 2], d[n * V + 3]},
+                                    (f32x4_t*)(d_out + row + col));
       else
         d_out[row + col] = d[n];
     }
@@ -426,14 +463,18 @@ hipError_t launch_balance_forward(const float* logits, const int32_t* ids, const
   const BalWs w = bal_ws(T, E, S, (char*)ws);
   const int tile = balance_tile(T);
   const unsigned tiles = (unsigned)((T + (int64_t)tile - 1) / tile);
+  // one tile and one group of all tokens: the one block writes the results (64x8 tokens by experts: 4 us
+  // against 4 and 6 us for the reduction's launch)
+  const bool one = tiles == 1 && !goff;
+  const BalOut whole{one ? counts : nullptr, tokens, losses};
   if (tiles > 0) {
 #define MOE_BAL_CALL(V, N)                                                                                       \
   balance_stats_kernel<V, N><<<tiles, kBalThreads, 0, st>>>(logits, ids, mask, goff, T, E, k, S, tile, lse, w.P, \
-                                                            w.C, w.n, w.z)
+                                                            w.C, w.n, w.z, whole)
     MOE_BAL_DISPATCH(E, MOE_BAL_CALL);
 #undef MOE_BAL_CALL
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || one) return e;
   }
   const int wide = balance_wide(T, E, S);
   const int chunks = (E + 64 * wide - 1) / (64 * wide);
@@ -457,7 +498,7 @@ hipError_t launch_balance_backward(const float* logits, const float* lse, const 
                                    const int32_t* tokens, const float* d_losses, int T, int E, int k, int S,
                                    const float* d_in, float* d_out, hipStream_t st) {
   if (T == 0) return hipSuccess;
-  const int tile = 64;
+  const int tile = 32;
   const unsigned tiles = (unsigned)((T + (int64_t)tile - 1) / tile);
 #define MOE_BAL_CALL(V, N)                                                                                       \
   balance_grad_kernel<V, N><<<tiles, kBalThreads, 0, st>>>(logits, lse, goff, counts, tokens, d_losses, T, E, k, \
