@@ -10,6 +10,7 @@ rocprofv3 counter summaries when they match the current kernel sources) and the 
 oracle timed on a bounded sample of the same workload on the host cores.
 
     python bench.py [--gpus 1] [--steps 20] [--warmup 5] [--config qwen3] [--no-cpu-baseline]
+                    [--block-step]
 
 Helpers that read rocprofv3 CSV output (CPU only, print a text summary):
 
@@ -384,6 +385,95 @@ def summarize_memory(d, config, command):
 
 
 # ------------------------------------------------------------------ benchmark
+def block_step(moe, dm, b, x, W1, W2, Wg, dy, reps=10):
+    """The training step of a block around the layer, outside the timed region: norm, gate scores,
+    routing, balance loss, experts, norm and gated residual; the way back; gradient norm and AdamW on
+    every weight (fp32 master copies and states).  Returns ms of the whole step and of the calls that
+    are not the layer's own, with the GB/s of their algorithmic bytes."""
+    import torch
+    T, d, f, E, k = dm.T, dm.d, dm.f, dm.E, dm.k
+    dev, bf16, f32 = x.device, torch.bfloat16, torch.float32
+
+    def new(*shape, dtype=f32):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+    def ws(n):
+        return new(max(n, 256), dtype=torch.uint8)
+
+    ones = torch.ones(d, dtype=f32, device=dev)
+    p = {"W1": W1.clone(), "W2": W2.clone(), "Wg": Wg.clone(), "w_pre": ones.clone(), "w_post": ones.clone(),
+         "gate": ones.clone()}   # the step moves the weights: the layer's own stay as they are
+    g = {n: torch.empty_like(t) for n, t in p.items()}
+    rows, numel = [], 0
+    for n, t in p.items():
+        numel += t.numel()
+        rows.append(moe.adamw_tensor(g[n], t, torch.zeros(t.numel(), device=dev), torch.zeros(t.numel(), device=dev),
+                                     t.float() if t.dtype == bf16 else None, weight_decay=0.1 if t.dim() > 1 else 0.0))
+    tensors = moe.adamw_tensors(rows)
+    h, dh = x.float(), dy.float()
+    xn, h_out, dyn, dhn = new(T, d, dtype=bf16), new(T, d), new(T, d, dtype=bf16), new(T, d)
+    logits, lse, losses = new(T, E), new(T), new(2)
+    counts, tokens = new(1, E, dtype=torch.int32), new(3, dtype=torch.int32)
+    d_losses = torch.tensor([0.01, 0.001], device=dev)
+    norm, scale = new(1), new(1)
+    pre = moe.norm_desc(T, d, moe.MOE_F32, moe.MOE_F32)
+    post = moe.norm_desc(T, d, moe.MOE_F32, moe.MOE_F32, moe.MOE_GATE_CHANNEL)
+    wb, wn, wr, wg = (ws(moe.moe_balance_workspace_bytes(dm, 1)), ws(moe.moe_norm_workspace_bytes(post)),
+                      ws(moe.moe_workspace_bytes(dm, moe.MOE_WS_ROUTER)), ws(moe.moe_grad_norm_workspace_bytes(tensors)))
+    number = [0]
+
+    def adamw():
+        number[0] += 1
+        moe.moe_adamw_step(moe.adamw_hyper(1e-4, step=number[0], d_grad_scale=scale), tensors)
+
+    calls = [
+        ("norm_before", lambda: moe.moe_norm_forward(pre, None, h, None, None, p["w_pre"], None, xn), T * d * 6),
+        ("gate", lambda: moe.moe_router_logits(dm, xn, p["Wg"], logits), None),
+        ("route", lambda: moe.moe_route(dm, logits, b["topk_ids"], b["topk_w"], b["counts"], b["offsets"], b["perm"],
+                                        b["inv_perm"], b["ws_route"]), None),
+        ("balance", lambda: moe.moe_balance_forward(dm, logits, b["topk_ids"], None, None, 1, counts, tokens, losses, lse, wb),
+         T * E * 4 + T * k * 4 + T * 4),
+        ("experts", lambda: moe.moe_forward(dm, xn, None, p["W1"], None, p["W2"], None, b["topk_w"], b["offsets"], b["perm"],
+                                            b["inv_perm"], b["y"], b["saved"], b["ws_fwd"]), None),
+        ("norm_behind", lambda: moe.moe_norm_forward(post, b["y"], h, p["w_post"], p["gate"], None, h_out, None), T * d * 10),
+        ("norm_behind_backward", lambda: moe.moe_norm_backward(post, b["y"], None, p["w_post"], p["gate"], None, dh, None, dhn,
+                                                               dyn, g["w_post"], g["gate"], None, wn), T * d * 12),
+        ("experts_backward", lambda: moe.moe_backward(
+            dm, dyn, xn, None, p["W1"], None, p["W2"], None, b["topk_ids"], b["topk_w"], b["offsets"], b["perm"],
+            b["inv_perm"], b["saved"], b["dx"], g["W1"], g["W2"], b["d_topk_w"], b["d_logits"], b["ws_bwd"]), None),
+        ("balance_backward", lambda: moe.moe_balance_backward(dm, logits, lse, None, 1, counts, tokens, d_losses,
+                                                              b["d_logits"], b["d_logits"]), T * E * 12 + T * 4),
+        ("gate_backward", lambda: moe.moe_router_backward(dm, xn, p["Wg"], b["d_logits"], b["dx"], g["Wg"], wr), None),
+        ("norm_before_backward", lambda: moe.moe_norm_backward(pre, None, h, None, None, p["w_pre"], dhn, b["dx"], dhn, None,
+                                                               None, None, g["w_pre"], wn), T * d * 14),
+        ("grad_norm", lambda: moe.moe_grad_norm(tensors, 1.0, norm, scale, wg), numel * 2),
+        ("adamw", adamw, numel * 28),
+    ]
+    for _ in range(2):
+        for _, call, _ in calls:
+            call()
+    ev = [[torch.cuda.Event(enable_timing=True) for _ in range(len(calls) + 1)] for _ in range(reps)]
+    cur = torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    for r in range(reps):
+        ev[r][0].record(cur)
+        for i, (_, call, _) in enumerate(calls):
+            call()
+            ev[r][i + 1].record(cur)
+    torch.cuda.synchronize()
+    out = {"ms_per_step": sum(e[0].elapsed_time(e[-1]) for e in ev) / reps, "weights": numel, "calls": {},
+           "note": "norm, gate, routing, balance loss, experts, norm and gated residual, backward, gradient norm and "
+                   "AdamW (fp32 master copies and states); outside the timed step"}
+    for i, (n, _, by) in enumerate(calls):
+        ms = sorted(e[i].elapsed_time(e[i + 1]) for e in ev)[reps // 2]
+        out["calls"][n] = {"ms": ms}
+        if by:
+            out["calls"][n]["gbs"] = by / (ms * 1e-3) / 1e9
+    log(f"[bench] block step: {out['ms_per_step']:.3f} ms; " +
+        ", ".join(f"{n} {v['ms']:.3f}" for n, v in out["calls"].items()))
+    return out
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -394,6 +484,8 @@ def main():
     ap.add_argument("--config", default="qwen3", choices=sorted(WORKLOADS))
     ap.add_argument("--dtype", default="auto", choices=["auto", "mxfp8"],
                     help="auto: the workload's own format; mxfp8: run a bf16 workload as MXFP8 (quantised inside)")
+    ap.add_argument("--block-step", action="store_true",
+                    help="also time the training step of a block around the layer (bf16 workloads)")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--cpu-seconds", type=float, default=15.0, help="target duration of the CPU oracle sample")
     ap.add_argument("--calibrate-copy", action="store_true",
@@ -670,6 +762,11 @@ def main():
         log(f"[bench] router front end: logits {lms:.3f} ms, backward {bms:.3f} ms")
         del lg, dWg, rws, dxr
 
+    # the training step of a block around the layer (norms, balance loss, optimiser), on buffers of its own
+    block = None
+    if args.block_step and not fp8 and inp.Wg is not None:
+        block = block_step(moe, dm, b, x, W1, W2, bf16(inp.Wg), dy)
+
     # LLC-cold steps: a 512 MiB scratch write before each one (outside its timing) evicts the
     # step's operands from the 256 MB last-level cache and the L2s; the median step is reported
     cold = None
@@ -708,7 +805,7 @@ def main():
         "frac_of_mfma_peak": ideal_ms / ms,
         "useful_flop_per_step": useful, "ms_per_step_with_stage_events": ms_ev,
         "ms_per_step_graph_replay": ms_graph, "stages": stages,
-        "permute_standalone": permute, "router_front_end": router, "single_launch_forward": fused,
+        "permute_standalone": permute, "router_front_end": router, "block_step": block, "single_launch_forward": fused,
         "roofline": roof,
         "llc_cold": cold, "cpu_baseline": cpu,
     }
