@@ -866,7 +866,7 @@ int moe_adamw_step(const moe_adamw* hyper, const moe_tensor* tensors, int64_t n_
   // a beta that fp32 rounds to 1 would leave nothing of the gradient
   if (!(h.beta1 >= 0.0) || !((float)h.beta1 < 1.0f) || !(h.beta2 >= 0.0) || !((float)h.beta2 < 1.0f))
     return MOE_ERR_SHAPE;
-  if (!((float)h.eps > 0.0f) || !isfinite((float)h.eps)) return MOE_ERR_SHAPE;
+  if (!((float)h.eps >= 1.17549435e-38f) || !isfinite((float)h.eps)) return MOE_ERR_SHAPE;  // a normal fp32 value
   if (!h.d_step && h.step < 1) return MOE_ERR_SHAPE;
   const int rc = check_tensors(tensors, n_tensors, false);
   if (rc) return rc;

@@ -19,8 +19,12 @@ namespace {
 constexpr int kBalThreads = 256;
 constexpr int kBalRedThreads = 1024;
 
+// Tokens of a tile: at most 512 tiles, whose partial sums few blocks add, until a tile has 512 tokens (its
+// fp32 sums stay short); then up to 65536 tiles.
 int balance_tile(int64_t T) {
-  const int64_t t = (T + 511) / 512;  // at most 512 tiles, whose partial sums one block per 64 columns adds
+  int64_t t = (T + 511) / 512;
+  if (t > 512) t = 512;
+  if (t < (T + 65535) / 65536) t = (T + 65535) / 65536;
   return t < 64 ? 64 : (int)t;
 }
 
@@ -165,23 +169,23 @@ __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
     for (int i = 0; i < V * N; ++i) acc[i] = 0.0f;
     float zs = 0.0f;
     int cnt = 0;
-    for (int tb = a + r; tb < z; tb += kRows * U) {
+    for (int64_t tb = a + r; tb < z; tb += kRows * U) {
       float x[U][V * N];
       int first[U];
       bool on[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {  // every load before the first use
-        const int t = tb + u * kRows;
+        const int64_t t = tb + u * kRows;
         on[u] = t < z && in && (!mask || mask[t] != 0);
         first[u] = -1;
         if (on[u]) {
-          load_row<V, N>(logits + (int64_t)t * E, E, l, -INFINITY, x[u]);
-          if (l < k) first[u] = ids[(int64_t)t * k + l];
+          load_row<V, N>(logits + t * E, E, l, -INFINITY, x[u]);
+          if (l < k) first[u] = ids[t * k + l];
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = tb + u * kRows;
+        const int64_t t = tb + u * kRows;
         if (t >= z) break;
         float lse = -INFINITY;
         if (on[u]) {
@@ -205,7 +209,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
             ++cnt;
             if (first[u] >= 0 && first[u] < E) atomicAdd(&hist[first[u]], 1);  // integers: any order gives the same
             for (int j = l + kL; j < k; j += kL) {
-              const int e = ids[(int64_t)t * k + j];
+              const int e = ids[t * k + j];
               if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
             }
           }
@@ -381,8 +385,8 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
   float ca = 0.0f;
   const int32_t total = tokens[S];
   const float cb = total > 0 ? 2.0f * d_losses[1] / (float)total : 0.0f;
-  for (int t = t0 + r; t < t1; t += kRows) {
-    const int64_t row = (int64_t)t * E;
+  for (int64_t t = t0 + r; t < t1; t += kRows) {
+    const int64_t row = t * E;
     const float lse = lse_in[t];
     float p[V * N], d[V * N];
     load_row<V, N>(logits + row, E, l, -INFINITY, p);
@@ -394,7 +398,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
     }
     if (lse != -INFINITY) {  // else what was read of the logits is not used
       if (t < lo || t >= hi) {
-        int g = goff ? group_of(goff, S, t) : 0;
+        int g = goff ? group_of(goff, S, (int)t) : 0;
         g = g < 0 ? 0 : (g >= S ? S - 1 : g);  // a counted token lies in a group
         lo = goff ? goff[g] : 0;
         hi = goff ? goff[g + 1] : T;
@@ -498,7 +502,7 @@ hipError_t launch_balance_backward(const float* logits, const float* lse, const 
                                    const int32_t* tokens, const float* d_losses, int T, int E, int k, int S,
                                    const float* d_in, float* d_out, hipStream_t st) {
   if (T == 0) return hipSuccess;
-  const int tile = 32;
+  const int tile = T <= (1 << 27) ? 32 : 1024;  // a grid's threads fit 32 bits
   const unsigned tiles = (unsigned)((T + (int64_t)tile - 1) / tile);
 #define MOE_BAL_CALL(V, N)                                                                                       \
   balance_grad_kernel<V, N><<<tiles, kBalThreads, 0, st>>>(logits, lse, goff, counts, tokens, d_losses, T, E, k, \

@@ -15,6 +15,7 @@ namespace moe {
 
 namespace {
 
+constexpr int64_t kNormMaxBlocks = (int64_t)1 << 21;  // of up to 1024 threads: a grid has fewer than 2^32
 enum { G_NONE = 0, G_CHANNEL = 1, G_TOKEN = 2, G_FULL = 3 };
 
 // 8 consecutive values as they lie in memory, loaded once (non-temporal): a row's next loads are
@@ -88,7 +89,9 @@ __device__ __forceinline__ void lds_barrier() {
 constexpr int norm_threads(int LR) { return LR <= 128 ? 256 : LR; }
 
 // Sums of K values over a row's LR lanes, the same in every lane.  sh: [K][LR / 64] of the row and of
-// this sum (the next one uses another, so one barrier is enough); the block's rows reach it together.
+// this sum; the next sum takes another buffer, so that one barrier is enough (a wave that writes a
+// buffer again has passed the barrier of the sum between, which every wave reaches after its reads of
+// the first).  The block's rows reach it together.
 template <int LR, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
 #pragma unroll
@@ -123,79 +126,83 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
   constexpr int kRows = norm_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
   __shared__ float sh[kRows][2][W];
   const int slot = threadIdx.x / LR, lane = threadIdx.x % LR, wave = lane >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kRows + slot;
-  const bool on = t < p.T;
-  const int64_t base = on ? t * p.d : 0;
-  Raw8<false> yr[NV];
-  Raw8<HF32> hr[NV];
+  // one turn unless there are more rows than a grid's blocks take
+  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += (int64_t)gridDim.x * kRows) {
+    if (t0 >= (int64_t)gridDim.x * kRows) lds_barrier();  // the sums of the turn before have been read
+    const int64_t t = t0 + slot;
+    const bool on = t < p.T;
+    const int64_t base = on ? t * p.d : 0;
+    Raw8<false> yr[NV];
+    Raw8<HF32> hr[NV];
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int c = (n * LR + lane) * 8;
-    hr[n].zero();
-    yr[n].zero();
-    if (on && c < p.d) {
-      hr[n].load(h, base + c);
-      if (y) yr[n].load(y, base + c);
+    for (int n = 0; n < NV; ++n) {
+      const int c = (n * LR + lane) * 8;
+      hr[n].zero();
+      yr[n].zero();
+      if (on && c < p.d) {
+        hr[n].load(h, base + c);
+        if (y) yr[n].load(y, base + c);
+      }
     }
-  }
-  float hv[NV][8];
+    float hv[NV][8];
 #pragma unroll
-  for (int n = 0; n < NV; ++n) hr[n].get(hv[n]);
-  float s[1] = {0.0f};
-  if (y) {
-    float sq = p.out_scale;
-    if (p.gate == G_TOKEN && on) sq *= load1(gate, t, p.w_f32);
-    if (w_post) {
+    for (int n = 0; n < NV; ++n) hr[n].get(hv[n]);
+    float s[1] = {0.0f};
+    if (y) {
+      float sq = p.out_scale;
+      if (p.gate == G_TOKEN && on) sq *= load1(gate, t, p.w_f32);
+      if (w_post) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+          float yv[8];
+          yr[n].get(yv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[0] += yv[i] * yv[i];
+        }
+        row_sum<LR, 1>(s, sh[slot][0], wave);
+        sq *= rsqrtf(s[0] * p.inv_d + p.eps);
+      }
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        float yv[8];
+        const int c = (n * LR + lane) * 8;
+        if (!on || c >= p.d) continue;
+        float m[8], w[8], yv[8];
         yr[n].get(yv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += yv[i] * yv[i];
+        for (int i = 0; i < 8; ++i) m[i] = sq;
+        if (w_post) {
+          load_w8(w_post, c, p.w_f32, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m[i] *= w[i];
+        }
+        if (p.gate == G_CHANNEL || p.gate == G_FULL) {
+          load_w8(gate, p.gate == G_FULL ? base + c : c, p.w_f32, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m[i] *= w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hv[n][i] = p.res_scale * hv[n][i] + yv[i] * m[i];
+        store8<HF32>(h_out, base + c, hv[n]);
       }
-      row_sum<LR, 1>(s, sh[slot][0], wave);
-      sq *= rsqrtf(s[0] * p.inv_d + p.eps);
     }
+    if (!x) continue;
+    s[0] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += hv[n][i] * hv[n][i];
+    row_sum<LR, 1>(s, sh[slot][1], wave);
+    const float sp = rsqrtf(s[0] * p.inv_d + p.eps);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * LR + lane) * 8;
       if (!on || c >= p.d) continue;
-      float m[8], w[8], yv[8];
-      yr[n].get(yv);
+      float w[8];
+      load_w8(w_pre, c, p.w_f32, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m[i] = sq;
-      if (w_post) {
-        load_w8(w_post, c, p.w_f32, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] *= w[i];
-      }
-      if (p.gate == G_CHANNEL || p.gate == G_FULL) {
-        load_w8(gate, p.gate == G_FULL ? base + c : c, p.w_f32, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] *= w[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) hv[n][i] = p.res_scale * hv[n][i] + yv[i] * m[i];
-      store8<HF32>(h_out, base + c, hv[n]);
+      for (int i = 0; i < 8; ++i) w[i] *= hv[n][i] * sp;
+      store8<false>(x, base + c, w);
     }
-  }
-  if (!x) return;
-  s[0] = 0.0f;
-#pragma unroll
-  for (int n = 0; n < NV; ++n)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] += hv[n][i] * hv[n][i];
-  row_sum<LR, 1>(s, sh[slot][1], wave);
-  const float sp = rsqrtf(s[0] * p.inv_d + p.eps);
-#pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int c = (n * LR + lane) * 8;
-    if (!on || c >= p.d) continue;
-    float w[8];
-    load_w8(w_pre, c, p.w_f32, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] *= hv[n][i] * sp;
-    store8<false>(x, base + c, w);
   }
 }
 
@@ -261,10 +268,12 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
   };
   constexpr bool kAhead = NV == 1;  // two rows of 16 values a lane do not fit 1024 threads' registers
   if (kAhead) fetch((int64_t)blockIdx.x * kRows + slot);
+  int first = 0;  // the first sum's buffer: with one sum a row, two rows in turn
   for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += step) {
     const int64_t t = t0 + slot;
     const bool on = t < p.T;
     const int64_t base = on ? t * p.d : 0;
+    if (!Y) first ^= 1;
     if (!kAhead) fetch(t);
     const RowIn<NV, HF32, Y, P> in = cur;
     if (kAhead && t0 + step < p.T) fetch(t + step);
@@ -290,7 +299,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
         for (int i = 0; i < 8; ++i) s[kS - 1] += v[i] * v[i];
       }
     }
-    row_sum<LR, kS>(s, sh[slot][0], wave);
+    row_sum<LR, kS>(s, sh[slot][first], wave);
     const float sp = P ? rsqrtf(s[0] * p.inv_d + p.eps) : 0.0f, mp = P ? s[1] * p.inv_d * sp * sp * sp : 0.0f;
     const float sq = Y && w_post ? rsqrtf(s[kS - 1] * p.inv_d + p.eps) : 1.0f, sqg = sq * gt;
     float D[NV][8];
@@ -474,7 +483,8 @@ size_t norm_ws_bytes(int64_t T, int d) {
 hipError_t launch_norm_forward(const NormArgs& p, const uint16_t* y, const void* h, const void* w_post,
                                const void* gate, const void* w_pre, void* h_out, uint16_t* x, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  const unsigned blocks = (unsigned)((p.T + norm_rows_per_block(p.d) - 1) / norm_rows_per_block(p.d));
+  const int64_t all = (p.T + norm_rows_per_block(p.d) - 1) / norm_rows_per_block(p.d);
+  const unsigned blocks = (unsigned)(all < kNormMaxBlocks ? all : kNormMaxBlocks);  // a grid's threads fit 32 bits
 #define MOE_NORM_CALL(LR, NV)                                                                                       \
   if (p.h_f32)                                                                                                     \
     norm_forward_kernel<LR, NV, true><<<blocks, norm_threads(LR), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x);  \

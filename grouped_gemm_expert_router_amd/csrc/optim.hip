@@ -34,7 +34,7 @@ struct AdamTensor {
 
 struct AdamBatch {
   AdamTensor t[kAdamBatch];
-  int32_t first[kAdamBatch + 1];  // first chunk of each tensor
+  int32_t first[kAdamBatch + 1];  // first chunk of each tensor (below 0: earlier launches took some)
   int32_t n;
 };
 static_assert(kAdamBatch < 64, "a lane for each tensor");
@@ -400,33 +400,43 @@ __global__ __launch_bounds__(1024) void grad_norm_final_kernel(const double* __r
   }
 }
 
-// Calls fn(batch, chunks, index of the batch's first tensor) for runs of up to kAdamBatch tensors
-// that are not empty, each cut into chunks of `chunk` values.
+constexpr int64_t kMaxChunks = (int64_t)1 << 22;  // blocks a launch: a grid's threads fit 32 bits
+
+// Calls fn(batch, chunks, index of the batch's first tensor) for runs of up to kAdamBatch tensors and
+// kMaxChunks chunks of `chunk` values.  A tensor that a launch ends in goes on in the next: its first
+// chunk then lies before that launch's.
 template <class F>
 hipError_t for_batches(const moe_tensor* t, int64_t n, int64_t chunk, F fn) {
   AdamBatch b;
   b.n = 0;
   int64_t chunks = 0, first = 0;
+  const auto flush = [&]() {
+    b.first[b.n] = (int32_t)chunks;
+    const hipError_t e = chunks > 0 ? fn(b, chunks, first) : hipSuccess;
+    b.n = 0;
+    chunks = 0;
+    return e;
+  };
   for (int64_t i = 0; i < n; ++i) {
-    const int64_t c = (t[i].n + chunk - 1) / chunk;
-    if (b.n == kAdamBatch || (b.n > 0 && chunks + c >= ((int64_t)1 << 31))) {
-      b.first[b.n] = (int32_t)chunks;
-      const hipError_t e = fn(b, chunks, first);
-      if (e != hipSuccess) return e;
-      b.n = 0;
-      chunks = 0;
-    }
-    if (b.n == 0) first = i;
-    b.t[b.n] = AdamTensor{t[i].p, t[i].g, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale, t[i].master, t[i].n,
-                          t[i].weight_decay,
-                          (t[i].p_dtype == MOE_F32 ? kAdamP32 : 0) | (t[i].g_dtype == MOE_F32 ? kAdamG32 : 0) |
-                              (t[i].state == MOE_STATE_8BIT ? kAdam8bit : 0)};
-    b.first[b.n++] = (int32_t)chunks;
-    chunks += c;
+    const int64_t all = (t[i].n + chunk - 1) / chunk;
+    int64_t done = 0;
+    do {
+      if (b.n == kAdamBatch || chunks == kMaxChunks) {
+        const hipError_t e = flush();
+        if (e != hipSuccess) return e;
+      }
+      if (b.n == 0) first = i;
+      b.t[b.n] = AdamTensor{t[i].p, t[i].g, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale, t[i].master, t[i].n,
+                            t[i].weight_decay,
+                            (t[i].p_dtype == MOE_F32 ? kAdamP32 : 0) | (t[i].g_dtype == MOE_F32 ? kAdamG32 : 0) |
+                                (t[i].state == MOE_STATE_8BIT ? kAdam8bit : 0)};
+      b.first[b.n++] = (int32_t)(chunks - done);
+      const int64_t take = all - done < kMaxChunks - chunks ? all - done : kMaxChunks - chunks;
+      done += take;
+      chunks += take;
+    } while (done < all);
   }
-  if (b.n == 0 || chunks == 0) return hipSuccess;
-  b.first[b.n] = (int32_t)chunks;
-  return fn(b, chunks, first);
+  return flush();
 }
 
 int64_t norm_chunk(const moe_tensor* t, int64_t n) {

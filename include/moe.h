@@ -342,7 +342,7 @@ int moe_grad_norm(const moe_tensor* tensors, int64_t n_tensors, float max_norm, 
 typedef struct {
   double lr;              /* >= 0 and finite; unused with d_lr */
   double beta1, beta2;    /* in [0, 1) */
-  double eps;             /* > 0 and finite (in fp32 too) */
+  double eps;             /* at least 2^-126 and finite in fp32 */
   int64_t step;           /* 1 for the first step; unused with d_step */
   uint64_t seed;
   int32_t stochastic;     /* 0 or 1 */
