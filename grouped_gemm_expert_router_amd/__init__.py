@@ -301,24 +301,25 @@ def adamw_tensor(g, p=None, m=None, v=None, master=None, m_scale=None, v_scale=N
     """One row for adamw_tensors(): torch tensors of one parameter, its gradient and its states.  m and
     v with scales (float8_e4m3fn or uint8) are 8-bit states.  moe_grad_norm needs g alone."""
     import torch
-    types = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+    f32, types = torch.float32, {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
     n = g.numel()
     eight = m_scale is not None or v_scale is not None
-    codes = (torch.float8_e4m3fn, torch.uint8)
-    state = codes if eight else (torch.float32,)
-    blocks = (n + 255) // 256
-    for name, t, size, allowed in (("g", g, n, types), ("p", p, n, types), ("m", m, n, state), ("v", v, n, state),
-                                   ("master", master, n, (torch.float32,)),
-                                   ("m_scale", m_scale, blocks, (torch.float32,)),
-                                   ("v_scale", v_scale, blocks, (torch.float32,))):
+    state = (torch.float8_e4m3fn, torch.uint8) if eight else (f32,)
+    device = g.device
+
+    def check(name, t, size, allowed):
         if t is None:
-            continue
-        if t.numel() != size or not t.is_contiguous() or t.dtype not in allowed or t.device != g.device:
+            return None
+        if t.dtype not in allowed or t.numel() != size or not t.is_contiguous() or t.device != device:
             raise ValueError(f"adamw_tensor: {name} is {tuple(t.shape)} {t.dtype} on {t.device}, expected {size} "
-                             f"contiguous values on {g.device} of {sorted(map(str, allowed))}")
-    row = MoeTensor(_ptr(p), _ptr(g), _ptr(m), _ptr(v), _ptr(m_scale), _ptr(v_scale), _ptr(master), n,
-                    types[p.dtype] if p is not None else MOE_F32, types[g.dtype],
-                    MOE_STATE_8BIT if eight else MOE_STATE_F32, weight_decay)
+                             f"contiguous values on {device} of {sorted(map(str, allowed))}")
+        return t.data_ptr()
+
+    blocks = (n + 255) // 256
+    row = MoeTensor(check("p", p, n, types), check("g", g, n, types), check("m", m, n, state), check("v", v, n, state),
+                    check("m_scale", m_scale, blocks, (f32,)), check("v_scale", v_scale, blocks, (f32,)),
+                    check("master", master, n, (f32,)), n, types[p.dtype] if p is not None else MOE_F32,
+                    types[g.dtype], MOE_STATE_8BIT if eight else MOE_STATE_F32, weight_decay)
     return row, (g, p, m, v, master, m_scale, v_scale)
 
 

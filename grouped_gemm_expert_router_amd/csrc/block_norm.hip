@@ -118,6 +118,8 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
   }
 }
 
+}  // namespace
+
 // The row stays in registers between its passes.
 template <int LR, int NV, bool HF32>
 __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
@@ -206,12 +208,16 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
   }
 }
 
+namespace {
+
 // What one row of the backward pass reads, as it lies in memory
 template <int NV, bool HF32, bool Y, bool P>
 struct RowIn {
   Raw8<HF32> h[NV], D[NV];
   Raw8<false> g[NV], y[NV];
 };
+
+}  // namespace
 
 // A block walks rows a grid apart, each row's loads issued before the row before is worked on, and
 // keeps the weights and the sums for their gradients of its columns in registers; the sums leave
@@ -435,6 +441,8 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormArgs p, const flo
   if (p.gate == G_CHANNEL && rows) by *= load1(gate, c, p.w_f32);
   if (dw_post) store1(dw_post, c, p.w_f32, by * a);
 }
+
+namespace {
 
 // Lanes of a row of d values, the fewest that hold it 8 values each
 int norm_lanes(int d) {

@@ -278,6 +278,8 @@ __device__ __forceinline__ void adamw_tail(const AdamTensor& T, const Step& h, i
   }
 }
 
+}  // namespace
+
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamBatch batch, AdamScalars hp) {
   Step h;
   h.gs = 1.0f;
@@ -323,6 +325,8 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamBatch batch, Ad
 #undef MOE_ADAM_CASE
 }
 
+namespace {
+
 // Sum of g^2 of one chunk, in 64 bits (no square of an fp32 value overflows or vanishes there).
 // Each thread has U loads of 16 bytes in flight; the values behind the last of them go one by one.
 template <bool G32>
@@ -365,6 +369,8 @@ __device__ __forceinline__ double square_sum(const void* g, int64_t a, int64_t z
   return s;
 }
 
+}  // namespace
+
 __global__ __launch_bounds__(256) void grad_norm_kernel(AdamBatch batch, int chunk, double* __restrict__ part) {
   __shared__ double sh[4];
   const int which = tensor_of(batch, blockIdx.x);
@@ -399,6 +405,8 @@ __global__ __launch_bounds__(1024) void grad_norm_final_kernel(const double* __r
     *scale = !((float)r < INFINITY) ? NAN : f < 1.0 ? (float)f : 1.0f;  // NaN: a step to skip
   }
 }
+
+namespace {
 
 constexpr int64_t kMaxChunks = (int64_t)1 << 22;  // blocks a launch: a grid's threads fit 32 bits
 

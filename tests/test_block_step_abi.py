@@ -63,7 +63,7 @@ def test_balance_refusals(lib):
 
 def test_balance_workspace_is_bounded(lib):
     big = lambda T, S, E=256: size(lib.moe_balance_workspace_bytes, ctypes.byref(moe.dims(T, 128, 128, E, 1)), S)[1]  # noqa: E731
-    assert big(1 << 18, 1) == big(1 << 15, 1)                 # 512 tiles
+    assert big(1 << 19, 1) == big(1 << 16, 1)                 # 1024 tiles
     assert big(1 << 15, 64) > big(1 << 15, 1)
     assert big((1 << 31) - 1, 1, 8) <= (1 << 16) * (8 * 8 + 8) + 8192   # 65536 tiles at most
 

@@ -85,8 +85,8 @@ CASES = {
     "E509": dict(T=66, E=509, k=8), "E1023": dict(T=9, E=1023, k=3),
     "one_token": dict(T=1, E=128, k=8), "no_add": dict(T=100, E=64, k=4, add=False),
     "mask": dict(T=257, E=64, k=4, mask=True), "seqs": dict(T=400, E=96, k=4, S=9, mask=True),
-    # tiles of more than one row a lane group and more than 64 tokens: T > 512 * 64
-    "long": dict(T=40000, E=16, k=2, S=5, mask=True),
+    # tiles of more than 64 tokens: T > 1024 * 64
+    "long": dict(T=70001, E=16, k=2, S=5, mask=True),
     # groups that begin late, end early, are empty, are of one token, end on a tile's edge
     "ragged": dict(T=300, E=128, k=8, offsets=np.array([3, 3, 64, 65, 65, 128, 191, 256, 290], np.int32), mask=True),
     "all_outside": dict(T=100, E=16, k=2, offsets=np.array([100, 100], np.int32)),
