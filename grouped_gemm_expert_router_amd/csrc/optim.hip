@@ -32,20 +32,44 @@ struct AdamTensor {
   int32_t flags;
 };
 
+// Tensors of one launch, in its arguments; first: first chunk of each (below 0: earlier launches took some)
 struct AdamBatch {
-  AdamTensor t[kAdamBatch];
-  int32_t first[kAdamBatch + 1];  // first chunk of each tensor (below 0: earlier launches took some)
+  static constexpr int kMost = kAdamBatch;
+  AdamTensor t[kMost];
+  int32_t first[kMost];
   int32_t n;
+  void put(const moe_tensor& q) {
+    t[n] = AdamTensor{q.p, q.g, q.m, q.v, q.m_scale, q.v_scale, q.master, q.n, q.weight_decay,
+                      (q.p_dtype == MOE_F32 ? kAdamP32 : 0) | (q.g_dtype == MOE_F32 ? kAdamG32 : 0) |
+                          (q.state == MOE_STATE_8BIT ? kAdam8bit : 0)};
+  }
 };
-static_assert(kAdamBatch < 64, "a lane for each tensor");
 static_assert(sizeof(AdamBatch) + sizeof(AdamScalars) <= 4096 - 64, "kernel arguments");
 
-// The tensor of a chunk: each lane compares one entry (the arguments may lie in host memory, where a
-// search's dependent reads cost a round trip each).
-__device__ __forceinline__ int tensor_of(const AdamBatch& b, int chunk) {
-  const int lane = threadIdx.x & 63;
-  const bool at = lane < b.n && b.first[lane] <= chunk;
-  return __popcll(__ballot(at)) - 1;
+struct GradBatch {
+  static constexpr int kMost = 3 * 64;
+  const void* g[kMost];
+  int64_t n32[kMost];  // 2 n + 1 for fp32 gradients, 2 n for bf16
+  int32_t first[kMost];
+  int32_t n;
+  void put(const moe_tensor& q) {
+    g[n] = q.g;
+    n32[n] = 2 * q.n + (q.g_dtype == MOE_F32);
+  }
+};
+static_assert(sizeof(GradBatch) <= 4096 - 64, "kernel arguments");
+
+// The tensor of a chunk: each lane compares an entry or a few (the arguments may lie in host memory,
+// where a search's dependent reads cost a round trip each).
+template <class Batch>
+__device__ __forceinline__ int tensor_of(const Batch& b, int chunk) {
+  int at = -1;
+#pragma unroll
+  for (int q = 0; q < Batch::kMost; q += 64) {
+    const int i = q + (threadIdx.x & 63);
+    at += __popcll(__ballot(i < b.n && b.first[i < Batch::kMost ? i : 0] <= chunk));
+  }
+  return at;
 }
 
 // 1 - beta^step by squaring, in 64 bits
@@ -371,13 +395,13 @@ __device__ __forceinline__ double square_sum(const void* g, int64_t a, int64_t z
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void grad_norm_kernel(AdamBatch batch, int chunk, double* __restrict__ part) {
+__global__ __launch_bounds__(256) void grad_norm_kernel(GradBatch batch, int chunk, double* __restrict__ part) {
   __shared__ double sh[4];
   const int which = tensor_of(batch, blockIdx.x);
-  const AdamTensor& T = batch.t[which];
-  const int64_t a = (int64_t)(blockIdx.x - batch.first[which]) * chunk;
-  const int64_t z = T.n - a < chunk ? T.n : a + chunk;
-  double s = T.flags & kAdamG32 ? square_sum<true>(T.g, a, z) : square_sum<false>(T.g, a, z);
+  const void* g = batch.g[which];
+  const int64_t n = batch.n32[which] >> 1, a = (int64_t)(blockIdx.x - batch.first[which]) * chunk;
+  const int64_t z = n - a < chunk ? n : a + chunk;
+  double s = batch.n32[which] & 1 ? square_sum<true>(g, a, z) : square_sum<false>(g, a, z);
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m, 64);
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
@@ -410,16 +434,15 @@ namespace {
 
 constexpr int64_t kMaxChunks = (int64_t)1 << 22;  // blocks a launch: a grid's threads fit 32 bits
 
-// Calls fn(batch, chunks, index of the batch's first tensor) for runs of up to kAdamBatch tensors and
+// Calls fn(batch, chunks, index of the batch's first tensor) for runs of up to Batch::kMost tensors and
 // kMaxChunks chunks of `chunk` values.  A tensor that a launch ends in goes on in the next: its first
 // chunk then lies before that launch's.
-template <class F>
+template <class Batch, class F>
 hipError_t for_batches(const moe_tensor* t, int64_t n, int64_t chunk, F fn) {
-  AdamBatch b;
+  Batch b;
   b.n = 0;
   int64_t chunks = 0, first = 0;
   const auto flush = [&]() {
-    b.first[b.n] = (int32_t)chunks;
     const hipError_t e = chunks > 0 ? fn(b, chunks, first) : hipSuccess;
     b.n = 0;
     chunks = 0;
@@ -429,15 +452,12 @@ hipError_t for_batches(const moe_tensor* t, int64_t n, int64_t chunk, F fn) {
     const int64_t all = (t[i].n + chunk - 1) / chunk;
     int64_t done = 0;
     do {
-      if (b.n == kAdamBatch || chunks == kMaxChunks) {
+      if (b.n == Batch::kMost || chunks == kMaxChunks) {
         const hipError_t e = flush();
         if (e != hipSuccess) return e;
       }
       if (b.n == 0) first = i;
-      b.t[b.n] = AdamTensor{t[i].p, t[i].g, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale, t[i].master, t[i].n,
-                            t[i].weight_decay,
-                            (t[i].p_dtype == MOE_F32 ? kAdamP32 : 0) | (t[i].g_dtype == MOE_F32 ? kAdamG32 : 0) |
-                                (t[i].state == MOE_STATE_8BIT ? kAdam8bit : 0)};
+      b.put(t[i]);
       b.first[b.n++] = (int32_t)(chunks - done);
       const int64_t take = all - done < kMaxChunks - chunks ? all - done : kMaxChunks - chunks;
       done += take;
@@ -463,7 +483,7 @@ int64_t norm_chunks(const moe_tensor* t, int64_t n, int64_t chunk) {
 }  // namespace
 
 hipError_t launch_adamw(const moe_tensor* t, int64_t n, const AdamScalars& hp, hipStream_t st) {
-  return for_batches(t, n, kChunk, [&](const AdamBatch& b, int64_t chunks, int64_t first) {
+  return for_batches<AdamBatch>(t, n, kChunk, [&](const AdamBatch& b, int64_t chunks, int64_t first) {
     AdamScalars h = hp;
     h.first_tensor = first;
     adamw_kernel<<<(unsigned)chunks, kAdamThreads, 0, st>>>(b, h);
@@ -477,7 +497,7 @@ hipError_t launch_grad_norm(const moe_tensor* t, int64_t n, float max_norm, floa
                             hipStream_t st) {
   const int64_t chunk = norm_chunk(t, n);
   int64_t at = 0;
-  const hipError_t e = for_batches(t, n, chunk, [&](const AdamBatch& b, int64_t chunks, int64_t) {
+  const hipError_t e = for_batches<GradBatch>(t, n, chunk, [&](const GradBatch& b, int64_t chunks, int64_t) {
     grad_norm_kernel<<<(unsigned)chunks, 256, 0, st>>>(b, (int)chunk, part + at);
     at += chunks;
     return hipGetLastError();

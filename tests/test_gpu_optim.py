@@ -299,7 +299,7 @@ def test_extreme_gradients():
 
 
 @pytest.mark.parametrize("g", [F32, BF16])
-@pytest.mark.parametrize("sizes", [[1], [4, 255, 256, 0, 4097], [70001, 3], [1000] * 130, [9_000_001, 5]])
+@pytest.mark.parametrize("sizes", [[1], [4, 255, 256, 0, 4097], [70001, 3], [1000] * 400, [9_000_001, 5]])
 def test_grad_norm_parity(sizes, g):
     """Sums in 64 bits: the norm's own rounding to fp32, and the scale's."""
     print(f"[case] grad_norm {len(sizes)} {g}", flush=True)
