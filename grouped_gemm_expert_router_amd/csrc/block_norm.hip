@@ -306,7 +306,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
       }
     }
     row_sum<LR, kS>(s, sh[slot][first], wave);
-    const float sp = P ? rsqrtf(s[0] * p.inv_d + p.eps) : 0.0f, mp = P ? s[1] * p.inv_d * sp * sp * sp : 0.0f;
+    const float sp = P ? rsqrtf(s[0] * p.inv_d + p.eps) : 0.0f, mp = P ? s[1] * p.inv_d * sp * sp : 0.0f;
     const float sq = Y && w_post ? rsqrtf(s[kS - 1] * p.inv_d + p.eps) : 1.0f, sqg = sq * gt;
     float D[NV][8];
     float e[1] = {0.0f};  // D cwg y
@@ -320,7 +320,8 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
         in.g[n].get(g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          a_pre[n][i] += h[i] * g[i] * sp;
+          h[i] *= sp;
+          a_pre[n][i] += h[i] * g[i];
           D[n][i] += wp[n][i] * g[i] * sp;
           D[n][i] -= h[i] * mp;
         }
@@ -368,7 +369,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
     if (!FULL) e[0] *= sq;
     if (p.gate == G_TOKEN && dgate && on && lane == 0) store1(dgate, t, p.w_f32, e[0]);
     if (!dy) continue;
-    const float mq = w_post ? -e[0] * p.inv_d * sq * sqg : 0.0f;
+    const float mq = w_post ? e[0] * p.inv_d * sq : 0.0f;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * LR + lane) * 8;
@@ -376,7 +377,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
       float v[8], o[8];
       in.y[n].get(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = D[n][i] * cwg[n][i] * sqg + v[i] * mq;
+      for (int i = 0; i < 8; ++i) o[i] = sqg * (D[n][i] * cwg[n][i] - v[i] * mq);
       store8<false>(dy, base + c, o);
     }
   }
