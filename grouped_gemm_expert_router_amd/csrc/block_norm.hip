@@ -85,8 +85,18 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // Rows are spread over LR lanes of 8 values each, NV times: a part of a wave for short rows (heads), up
-// to 16 waves for long ones; a block of 256 threads or one row holds kRows rows.
+// to 16 waves for long ones.  A block holds kRows rows: forward one, or 256 threads of short ones;
+// backward the most that 1024 threads hold (a power of two), one block a compute unit.
 constexpr int norm_threads(int LR) { return LR <= 128 ? 256 : LR; }
+constexpr int norm_bwd_threads(int LR) { return 2 * LR > 1024 ? LR : LR % 192 == 0 ? 768 : 1024; }
+
+// The thread's row in its block; the same for a whole wave (and known to be, so that a row's addresses
+// stay in scalar registers) but for rows on a part of a wave.
+template <int LR>
+__device__ __forceinline__ int row_slot() {
+  const int s = threadIdx.x / LR;
+  return LR >= 64 ? __builtin_amdgcn_readfirstlane(s) : s;
+}
 
 // Sums of K values over a row's LR lanes, the same in every lane.  sh: [K][LR / 64] of the row and of
 // this sum; the next sum takes another buffer, so that one barrier is enough (a wave that writes a
@@ -127,7 +137,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
     const void* __restrict__ gate, const void* __restrict__ w_pre, void* h_out, uint16_t* __restrict__ x) {
   constexpr int kRows = norm_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
   __shared__ float sh[kRows][2][W];
-  const int slot = threadIdx.x / LR, lane = threadIdx.x % LR, wave = lane >> 6;
+  const int slot = row_slot<LR>(), lane = threadIdx.x % LR, wave = lane >> 6;
   // one turn unless there are more rows than a grid's blocks take
   for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += (int64_t)gridDim.x * kRows) {
     if (t0 >= (int64_t)gridDim.x * kRows) lds_barrier();  // the sums of the turn before have been read
@@ -213,6 +223,7 @@ namespace {
 // What one row of the backward pass reads, as it lies in memory
 template <int NV, bool HF32, bool Y, bool P>
 struct RowIn {
+  float gt;  // the token's gate
   Raw8<HF32> h[NV], D[NV];
   Raw8<false> g[NV], y[NV];
 };
@@ -227,37 +238,65 @@ struct RowIn {
 // behind the block and a channel's gate: A = sum_t gt D yh gives dw_post = out_scale gate A and
 // dgate = out_scale w_post A.
 template <int LR, int NV, bool HF32, bool Y, bool P, bool FULL>
-__global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
+__global__ __launch_bounds__(norm_bwd_threads(LR)) void norm_backward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* __restrict__ h_out, const void* __restrict__ w_post,
     const void* __restrict__ gate, const void* __restrict__ w_pre, const void* dh_out, const uint16_t* __restrict__ dx,
     void* dh, uint16_t* __restrict__ dy, void* __restrict__ dgate, float* __restrict__ part, int64_t part_stride) {
-  constexpr int kRows = norm_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
+  constexpr int kRows = norm_bwd_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
   __shared__ float sh[kRows][2][3 * W];
-  const int slot = threadIdx.x / LR, lane = threadIdx.x % LR, wave = lane >> 6;
-  float a_pre[NV][8], a_post[NV][8], wp[NV][8], cwg[NV][8];
+  const int slot = row_slot<LR>(), lane = threadIdx.x % LR, wave = lane >> 6;
+  // the weights of a lane's columns: in registers, or for the longest rows in LDS (16 values a lane of each
+  // would spill: 2048 rows of 16384 took 170 us)
+  constexpr bool kLds = NV > 1;
+  __shared__ float4 w_lds[kLds ? 4 * NV * LR : 1];
+  float a_pre[NV][8], a_post[NV][8], w_reg[NV][2][8];  // w_pre; out_scale gate w_post
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int c = (n * LR + lane) * 8;
+    float wp[8], cwg[8], w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a_pre[n][i] = a_post[n][i] = wp[n][i] = 0.0f, cwg[n][i] = FULL ? 1.0f : p.out_scale;
-    if (c >= p.d) continue;
-    if (P) load_w8(w_pre, c, p.w_f32, wp[n]);
-    if (Y && w_post) {
-      float w[8];
-      load_w8(w_post, c, p.w_f32, w);
+    for (int i = 0; i < 8; ++i) a_pre[n][i] = a_post[n][i] = wp[i] = 0.0f, cwg[i] = FULL ? 1.0f : p.out_scale;
+    if (c < p.d) {
+      if (P) load_w8(w_pre, c, p.w_f32, wp);
+      if (Y && w_post) {
+        load_w8(w_post, c, p.w_f32, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cwg[n][i] *= w[i];
+        for (int i = 0; i < 8; ++i) cwg[i] *= w[i];
+      }
+      if (Y && p.gate == G_CHANNEL) {
+        load_w8(gate, c, p.w_f32, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cwg[i] *= w[i];
+      }
     }
-    if (Y && p.gate == G_CHANNEL) {
-      float w[8];
-      load_w8(gate, c, p.w_f32, w);
+    if (kLds) {  // a lane reads what it wrote itself
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cwg[n][i] *= w[i];
+      for (int q = 0; q < 2; ++q) {
+        w_lds[(n * 4 + q) * LR + lane] = make_float4(wp[4 * q], wp[4 * q + 1], wp[4 * q + 2], wp[4 * q + 3]);
+        w_lds[(n * 4 + 2 + q) * LR + lane] = make_float4(cwg[4 * q], cwg[4 * q + 1], cwg[4 * q + 2], cwg[4 * q + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w_reg[n][0][i] = wp[i], w_reg[n][1][i] = cwg[i];
     }
   }
+  const auto weights = [&](int n, int which, float (&w)[8]) {
+    if (kLds) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 v = w_lds[(n * 4 + 2 * which + q) * LR + lane];
+        w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = w_reg[n][which][i];
+    }
+  };
   const int64_t step = (int64_t)gridDim.x * kRows;
   RowIn<NV, HF32, Y, P> cur;
   const auto fetch = [&](int64_t t) {
+    cur.gt = 1.0f;
+    if (Y && p.gate == G_TOKEN && t < p.T) cur.gt = load1(gate, t, p.w_f32);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * LR + lane) * 8;
@@ -272,7 +311,9 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
       }
     }
   };
-  constexpr bool kAhead = NV == 1;  // two rows of 16 values a lane do not fit 1024 threads' registers
+  // a second row's values fit 128 registers beside the first's, but for the longest rows and a gate of its
+  // own for each value beside the norm before a block (16384 x 2048: 93 us, with spills 139)
+  constexpr bool kAhead = NV == 1 && !(FULL && P);
   if (kAhead) fetch((int64_t)blockIdx.x * kRows + slot);
   int first = 0;  // the first sum's buffer: with one sum a row, two rows in turn
   for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += step) {
@@ -283,8 +324,6 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
     if (!kAhead) fetch(t);
     const RowIn<NV, HF32, Y, P> in = cur;
     if (kAhead && t0 + step < p.T) fetch(t + step);
-    float gt = 1.0f;
-    if (Y && p.gate == G_TOKEN && on) gt = load1(gate, t, p.w_f32);
     constexpr int kS = (P ? 2 : 0) + (Y ? 1 : 0);
     float s[kS];  // (h'^2, h' w_pre dx), (y^2)
 #pragma unroll
@@ -292,11 +331,12 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       if (P) {
-        float h[8], g[8];
+        float h[8], g[8], w[8];
         in.h[n].get(h);
         in.g[n].get(g);
+        weights(n, 0, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += h[i] * h[i], s[P ? 1 : 0] += h[i] * g[i] * wp[n][i];
+        for (int i = 0; i < 8; ++i) s[0] += h[i] * h[i], s[P ? 1 : 0] += h[i] * g[i] * w[i];
       }
       if (Y) {
         float v[8];
@@ -307,7 +347,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
     }
     row_sum<LR, kS>(s, sh[slot][first], wave);
     const float sp = P ? rsqrtf(s[0] * p.inv_d + p.eps) : 0.0f, mp = P ? s[1] * p.inv_d * sp * sp : 0.0f;
-    const float sq = Y && w_post ? rsqrtf(s[kS - 1] * p.inv_d + p.eps) : 1.0f, sqg = sq * gt;
+    const float sq = Y && w_post ? rsqrtf(s[kS - 1] * p.inv_d + p.eps) : 1.0f, sqg = sq * in.gt;
     float D[NV][8];
     float e[1] = {0.0f};  // D cwg y
 #pragma unroll
@@ -315,14 +355,15 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
       const int c = (n * LR + lane) * 8;
       in.D[n].get(D[n]);
       if (P) {
-        float h[8], g[8];
+        float h[8], g[8], w[8];
         in.h[n].get(h);
         in.g[n].get(g);
+        weights(n, 0, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           h[i] *= sp;
           a_pre[n][i] += h[i] * g[i];
-          D[n][i] += wp[n][i] * g[i] * sp;
+          D[n][i] += w[i] * g[i] * sp;
           D[n][i] -= h[i] * mp;
         }
       }
@@ -334,8 +375,9 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
         store8<HF32>(dh, base + c, o);
       }
       if (Y) {
-        float v[8];
+        float v[8], cwg[8];
         in.y[n].get(v);
+        weights(n, 1, cwg);
         if (FULL) {
           // D: w_post' dn with the channel's own gate; the gate's gradient has the value itself
           float gv[8], dg[8];
@@ -345,7 +387,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float q = p.out_scale * D[n][i] * (v[i] * sq);
-            dg[i] = q * cwg[n][i];
+            dg[i] = q * cwg[i];
             a_post[n][i] += q * gv[i];
             e[0] += dg[i] * gv[i];
             D[n][i] *= p.out_scale * gv[i];
@@ -359,7 +401,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
           for (int i = 0; i < 8; ++i) {
             const float q = D[n][i] * v[i];
             a_post[n][i] += q * sqg;
-            e[0] += q * cwg[n][i];
+            e[0] += q * cwg[i];
           }
         }
       }
@@ -374,10 +416,11 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
     for (int n = 0; n < NV; ++n) {
       const int c = (n * LR + lane) * 8;
       if (!on || c >= p.d) continue;
-      float v[8], o[8];
+      float v[8], cwg[8], o[8];
       in.y[n].get(v);
+      weights(n, 1, cwg);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = sqg * (D[n][i] * cwg[n][i] - v[i] * mq);
+      for (int i = 0; i < 8; ++i) o[i] = sqg * (D[n][i] * cwg[i] - v[i] * mq);
       store8<false>(dy, base + c, o);
     }
   }
@@ -393,19 +436,20 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
     return;
   }
   // the block's rows, in order (NV is 1 here)
-  __shared__ float red[kRows > 1 ? 2 * 2048 : 1];
+  constexpr int kCols = kRows * LR * 8;
+  __shared__ float red[kRows > 1 ? 2 * kCols : 1];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (P) red[slot * LR * 8 + lane * 8 + i] = a_pre[0][i];
-    if (Y) red[2048 + slot * LR * 8 + lane * 8 + i] = a_post[0][i];
+    if (Y) red[kCols + slot * LR * 8 + lane * 8 + i] = a_post[0][i];
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < p.d; c += norm_threads(LR)) {
+  for (int c = threadIdx.x; c < p.d; c += norm_bwd_threads(LR)) {
     float u = 0.0f, v = 0.0f;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       if (P) u += red[r * LR * 8 + c];
-      if (Y) v += red[2048 + r * LR * 8 + c];
+      if (Y) v += red[kCols + r * LR * 8 + c];
     }
     if (P) part[(int64_t)blockIdx.x * p.d + c] = u;
     if (Y) part[part_stride + (int64_t)blockIdx.x * p.d + c] = v;
@@ -472,15 +516,13 @@ int norm_lanes(int d) {
 
 int norm_rows_per_block(int d) { return norm_threads(norm_lanes(d)) / norm_lanes(d); }
 
-// Blocks of the backward pass: 6 to 12 waves a compute unit, each with a row's loads ahead.  More of them
-// write more partial sums and read memory in smaller pieces (16384 rows of 2048: 2 a unit 78 us, 3 80, 4
-// 85; 4099 of 7168 in fp32: 1 a unit 105 us, 2 112); where over an eighth of the lanes idle, three
-// 256-thread blocks hold what two full ones would (46603 rows of 720: 2 a unit 85 us, 3 82).
+// Blocks of the backward pass: one a compute unit, each with its rows' loads ahead.  Smaller blocks, more
+// of them, write more partial sums and read memory in smaller pieces (16384 rows of 2048 values: 2 blocks
+// of one row a unit 78.5 us, 4 of them 85, 1 block of two rows 75.2, of four rows 73.4).
 int norm_bwd_blocks(int64_t T, int d) {
-  const int lanes = norm_lanes(d);
-  const int per_cu = lanes >= 384 ? 1 : lanes == 256 ? 2 : lanes == 192 ? 3 : d >= 7 * lanes ? 2 : 3;
-  const int64_t b = (T + norm_rows_per_block(d) - 1) / norm_rows_per_block(d);
-  return (int)(b < 256 * per_cu ? b : 256 * per_cu);
+  const int rows = norm_bwd_threads(norm_lanes(d)) / norm_lanes(d);
+  const int64_t b = (T + rows - 1) / rows;
+  return (int)(b < 256 ? b : 256);
 }
 
 }  // namespace
@@ -514,7 +556,7 @@ hipError_t launch_norm_backward(const NormArgs& p, const uint16_t* y, const void
   if (p.T > 0) {
     const bool full = y && p.gate == G_FULL;
 #define MOE_NORM_RUN(LR, NV, H, Y, P, F)                                                                              \
-  norm_backward_kernel<LR, NV, H, Y, P, F><<<blocks, norm_threads(LR), 0, st>>>(p, y, h_out, w_post, gate, w_pre, dh_out, \
+  norm_backward_kernel<LR, NV, H, Y, P, F><<<blocks, norm_bwd_threads(LR), 0, st>>>(p, y, h_out, w_post, gate, w_pre, dh_out, \
                                                                               dx, dh, dy, dgate,                       \
                                                                               pre || post ? part : nullptr, stride)
 #define MOE_NORM_FORM(LR, NV, H)                                 \
