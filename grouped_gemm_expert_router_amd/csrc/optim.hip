@@ -203,7 +203,10 @@ __device__ __forceinline__ void random4(const float (&w)[4], const uint32_t (&u)
 }
 
 // The 256 whole values of a wave from b: every load is issued before the first use.  The streams are
-// read and written once (non-temporal).
+// read and written once (non-temporal).  Bound by HBM: 604M bf16 weights with fp32 master copies take
+// 2.95 ms with fp32 states (28 bytes a value, 5.7 TB/s) and 1.60 ms with 8-bit states (16, 6.1 TB/s).
+// One run a wave and no more: 4 runs of a wave in turn 3.08 and 1.72 ms, two of them in flight together
+// 3.02 and 1.66; cached stores 3.11 and 1.79.
 template <bool P32, bool MASTER, bool G32, bool EIGHT>
 __device__ __forceinline__ void adamw_run(const AdamTensor& T, const Step& h, int64_t b, int lane) {
   const int64_t i = b + lane * 4;
@@ -353,6 +356,7 @@ namespace {
 
 // Sum of g^2 of one chunk, in 64 bits (no square of an fp32 value overflows or vanishes there).
 // Each thread has U loads of 16 bytes in flight; the values behind the last of them go one by one.
+// Bound by HBM: 604M bf16 values in 176 us, 6.9 TB/s (4 or 16 loads: 179, 185), and 4 us for the final sum.
 template <bool G32>
 __device__ __forceinline__ double square_sum(const void* g, int64_t a, int64_t z) {
   constexpr int V = G32 ? 4 : 8, U = 8;

@@ -44,6 +44,8 @@
  *   - Shapes (MOE_ERR_SHAPE otherwise): T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 64),
  *     d and f positive multiples of 128 (MOE_FP8_E4M3, MOE_MXFP8: of 256) and at most 65536,
  *     T*k < 2^31 (MOE_MXFP8: T*k + 127*E rounded up to 128 < 2^31).
+ *     moe_norm_*, moe_grad_norm and moe_adamw_step take sizes of their own (see there); MOE_F32 is an
+ *     element type of theirs and no dtype of the layer.
  *   - fp8 (MOE_FP8_E4M3): codes are OCP e4m3 (bias 7, max 448, no infinities); a block's value
  *     is code * scale with its fp32 scale ([Prime] "Mit csinált a Prime Intellect?": blockwise
  *     FP8 is one of the kernel's data types).  Outputs and gradients stay bf16/fp32.

@@ -61,6 +61,12 @@ def test_balance_refusals(lib):
     assert bal_bwd(lib, moe.dims(0, 128, 128, 8, 2), dict(logits=None, d=None)) == moe.MOE_OK   # nothing to add
 
 
+def test_fp32_is_no_type_of_the_layer(lib):
+    dm = moe.dims(64, 256, 256, 8, 2, moe.MOE_F32)
+    assert size(lib.moe_workspace_bytes, ctypes.byref(dm), moe.MOE_WS_FORWARD)[0] == moe.MOE_ERR_DTYPE
+    assert size(lib.moe_balance_workspace_bytes, ctypes.byref(dm), 1)[0] == moe.MOE_ERR_DTYPE
+
+
 def test_balance_workspace_is_bounded(lib):
     big = lambda T, S, E=256: size(lib.moe_balance_workspace_bytes, ctypes.byref(moe.dims(T, 128, 128, E, 1)), S)[1]  # noqa: E731
     assert big(1 << 19, 1) == big(1 << 16, 1)                 # 1024 tiles
