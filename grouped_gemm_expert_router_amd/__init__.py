@@ -124,22 +124,36 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_raw_stream = None
+_torch = None  # (handle of a device's current stream, current device), once they are needed
+
+
+def _torch_calls():
+    global _torch
+    if _torch is None:
+        import torch
+        torch.cuda.current_device()  # sets up the runtime
+        _torch = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    return _torch
 
 
 def _stream(stream) -> Optional[int]:
     """A stream's handle; None is torch's current stream of the current device.  The handle is taken
     from torch directly: a torch.cuda.Stream object around it costs 2.8 us, most of a small call."""
-    global _raw_stream
     if stream is None:
-        if _raw_stream is None:
-            import torch
-            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch.cuda.current_device)
-        raw, device = _raw_stream
+        raw, device = _torch_calls()
         return raw(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _here(fn: str, t) -> None:
+    """Refuses a tensor that is not on the current device: the kernels go to a stream of that one."""
+    if t is None or isinstance(t, int):
+        return
+    index = t.get_device()
+    if index < 0 or index != _torch_calls()[1]():
+        raise ValueError(f"{fn}: tensors on {t.device}, not on the current GPU")
 
 
 def _check(fn: str, rc: int) -> None:
@@ -248,6 +262,7 @@ def moe_balance_workspace_bytes(dm: MoeDims, S: int) -> int:
 
 def moe_balance_forward(dm, logits, topk_ids, token_mask, group_offsets, S, counts, group_tokens, losses, lse, ws,
                         ws_bytes=None, stream=None):
+    _here("moe_balance_forward", logits)
     nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
     _check("moe_balance_forward", load_library().moe_balance_forward(
         ctypes.byref(dm), _ptr(logits), _ptr(topk_ids), _ptr(token_mask), _ptr(group_offsets), S, _ptr(counts),
@@ -256,6 +271,7 @@ def moe_balance_forward(dm, logits, topk_ids, token_mask, group_offsets, S, coun
 
 def moe_balance_backward(dm, logits, lse, group_offsets, S, counts, group_tokens, d_losses, d_logits_in, d_logits,
                          stream=None):
+    _here("moe_balance_backward", logits)
     _check("moe_balance_backward", load_library().moe_balance_backward(
         ctypes.byref(dm), _ptr(logits), _ptr(lse), _ptr(group_offsets), S, _ptr(counts), _ptr(group_tokens),
         _ptr(d_losses), _ptr(d_logits_in), _ptr(d_logits), _stream(stream)))
@@ -273,6 +289,7 @@ def moe_norm_workspace_bytes(nd: MoeNormDesc) -> int:
 
 
 def moe_norm_forward(nd, y, h, w_post, gate, w_pre, h_out, x, stream=None):
+    _here("moe_norm_forward", h)
     _check("moe_norm_forward", load_library().moe_norm_forward(
         ctypes.byref(nd), _ptr(y), _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(h_out), _ptr(x),
         _stream(stream)))
@@ -280,6 +297,7 @@ def moe_norm_forward(nd, y, h, w_post, gate, w_pre, h_out, x, stream=None):
 
 def moe_norm_backward(nd, y, h_out, w_post, gate, w_pre, dh_out, dx, dh, dy, dw_post, dgate, dw_pre, ws,
                       ws_bytes=None, stream=None):
+    _here("moe_norm_backward", h_out if h_out is not None else dh_out)
     nb = (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
     _check("moe_norm_backward", load_library().moe_norm_backward(
         ctypes.byref(nd), _ptr(y), _ptr(h_out), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(dh_out), _ptr(dx),
@@ -291,6 +309,9 @@ class TensorList:
 
     def __init__(self, rows):
         self.rows = list(rows)
+        self.first = self.rows[0][1][0] if self.rows else None
+        if any(keep[0].device != self.first.device for _, keep in self.rows):
+            raise ValueError("adamw_tensors: tensors on more than one device")
         self.array = (MoeTensor * max(len(self.rows), 1))(*(r for r, _ in self.rows))
 
     def __len__(self):
@@ -330,8 +351,10 @@ def adamw_tensors(rows) -> TensorList:
 
 def adamw_hyper(lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8, step: int = 1, seed: int = 0,
                 stochastic: bool = False, d_lr=None, d_step=None, d_grad_scale=None) -> MoeAdamW:
-    return MoeAdamW(lr, beta1, beta2, eps, step, seed, int(stochastic), 0, _ptr(d_lr), _ptr(d_step),
-                    _ptr(d_grad_scale))
+    hyper = MoeAdamW(lr, beta1, beta2, eps, step, seed, int(stochastic), 0, _ptr(d_lr), _ptr(d_step),
+                     _ptr(d_grad_scale))
+    hyper.keep = (d_lr, d_step, d_grad_scale)  # alive as long as their addresses are
+    return hyper
 
 
 def moe_grad_norm_workspace_bytes(tensors: TensorList) -> int:
@@ -342,12 +365,14 @@ def moe_grad_norm_workspace_bytes(tensors: TensorList) -> int:
 
 
 def moe_grad_norm(tensors: TensorList, max_norm, norm, scale, ws, ws_bytes=None, stream=None):
+    _here("moe_grad_norm", tensors.first)
     nb = (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
     _check("moe_grad_norm", load_library().moe_grad_norm(tensors.array, len(tensors), max_norm, _ptr(norm),
                                                          _ptr(scale), _ptr(ws), nb, _stream(stream)))
 
 
 def moe_adamw_step(hyper: MoeAdamW, tensors: TensorList, stream=None):
+    _here("moe_adamw_step", tensors.first)
     _check("moe_adamw_step", load_library().moe_adamw_step(ctypes.byref(hyper), tensors.array, len(tensors),
                                                            _stream(stream)))
 

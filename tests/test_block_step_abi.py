@@ -222,3 +222,18 @@ def test_adamw_tensor_checks_torch_tensors():
             moe.adamw_tensor(z(10), **kw)
     with pytest.raises(ValueError):
         moe.adamw_tensor(z(10, torch.float16))
+
+
+def test_tensors_of_another_device_are_refused():
+    z = torch.zeros(64)
+    nd, dm = moe.norm_desc(1, 64, moe.MOE_F32, moe.MOE_F32), moe.dims(8, 128, 128, 8, 2)
+    tl = moe.adamw_tensors([moe.adamw_tensor(z, z, z, z)])
+    for call in (lambda: moe.moe_norm_forward(nd, None, z, None, None, z, None, z),
+                 lambda: moe.moe_norm_backward(nd, None, z, None, None, z, z, z, z, None, None, None, z, z),
+                 lambda: moe.moe_balance_forward(dm, z, z, None, None, 1, z, z, z, z, z),
+                 lambda: moe.moe_balance_backward(dm, z, z, None, 1, z, z, z, None, z),
+                 lambda: moe.moe_grad_norm(tl, 1.0, z, None, z), lambda: moe.moe_adamw_step(moe.adamw_hyper(1e-3), tl)):
+        with pytest.raises(ValueError, match="not on the current GPU"):
+            call()
+    with pytest.raises(ValueError, match="more than one device"):
+        moe.adamw_tensors([moe.adamw_tensor(z), moe.adamw_tensor(torch.zeros(3, device="meta"))])
