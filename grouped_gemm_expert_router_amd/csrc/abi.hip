@@ -876,7 +876,7 @@ int moe_adamw_step(const moe_adamw* hyper, const moe_tensor* tensors, int64_t n_
   a.b1 = (float)h.beta1, a.b2 = (float)h.beta2;
   a.a1 = (float)(1.0 - h.beta1), a.a2 = (float)(1.0 - h.beta2);
   a.lr = (float)h.lr, a.eps = (float)h.eps;
-  a.b1d = h.beta1, a.b2d = h.beta2;
+  a.ln_b1 = log(h.beta1), a.ln_b2 = log(h.beta2);  // -inf for 0
   a.step = (uint64_t)h.step, a.seed = h.seed, a.stochastic = h.stochastic;
   a.d_lr = h.d_lr, a.d_step = h.d_step, a.d_grad_scale = h.d_grad_scale;
   if (!h.d_step) {

@@ -196,7 +196,7 @@ hipError_t launch_norm_backward(const NormArgs& p, const uint16_t* y, const void
 constexpr int kAdamBatch = 48;
 struct AdamScalars {
   float b1, b2, a1, a2, lr, eps, inv_c1, inv_rc2;  // a = 1 - b; 1 / (1 - b1^step), 1 / sqrt(1 - b2^step)
-  double b1d, b2d;
+  double ln_b1, ln_b2;  // for a step on the device
   uint64_t step, seed;
   int64_t first_tensor;
   const float* d_lr;

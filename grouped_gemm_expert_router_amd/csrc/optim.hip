@@ -72,14 +72,6 @@ __device__ __forceinline__ int tensor_of(const Batch& b, int chunk) {
   return at;
 }
 
-// 1 - beta^step by squaring, in 64 bits
-__device__ __forceinline__ double one_less_power(double beta, uint64_t step) {
-  double p = 1.0, q = beta;
-  for (; step; step >>= 1, q *= q)
-    if (step & 1) p *= q;
-  return 1.0 - p;
-}
-
 // Random words of the element: the step's keys are splitmix64's finaliser (Steele, Lea, Flood 2014)
 // of the seed, the step and the tensor's place in the list; each value's words come from them and
 // its index by two and three rounds of multiply and shift (the constants: of 400 random odd pairs
@@ -103,12 +95,25 @@ __device__ __forceinline__ uint32_t noise2(uint32_t u, uint32_t k0) {
   return w ^ (w >> 15);
 }
 
-// e4m3 code of y in [0, 448], rounded up with the probability of the remainder (16 random bits).
-// Below 2^-6 the codes are even steps of 2^-9: 2^-6 added makes them those of one binade.
-__device__ __forceinline__ uint32_t code_of(float y, uint32_t r16) {
-  const bool low = y < 0.015625f;
-  const uint32_t b = __float_as_uint(low ? y + 0.015625f : y) + (r16 << 4);
-  return (b >> 20) - (low ? 968u : 960u);
+// e4m3 code of y in [0, 448], rounded up with the probability of the remainder: rs holds 16 random bits
+// in place (bits 4 to 19 of the 20 that the code leaves out).  A code is an fp32 value's exponent less
+// 120 and its upper three mantissa bits; below 2^-6 the codes are even steps of 2^-9, those of one
+// binade once 2^-6 is added, and half of that has the exponent one lower that they start from.
+__device__ __forceinline__ uint32_t code_of(float y, uint32_t rs) {
+  const uint32_t b = __float_as_uint(y < 0.015625f ? __builtin_fmaf(y, 0.5f, 0.0078125f) : y);
+  return (b + rs - (960u << 20)) >> 20;
+}
+
+// Square root: the hardware's reciprocal root (1 ulp) and one correction of the product.  The same bits
+// as the rounded root for every mantissa in two binades, normal and denormal (checked on the GPU); 0 and
+// infinity are their own roots.
+__device__ __forceinline__ float root_of(float v) {
+  const bool tiny = v < 0x1p-96f;  // keeps the reciprocal's argument normal
+  const float x = tiny ? v * 0x1p64f : v;
+  const float y = __builtin_amdgcn_rsqf(x), r = x * y;
+  float q = __builtin_fmaf(__builtin_fmaf(-r, r, x), 0.5f * y, r);
+  if (tiny) q *= 0x1p-32f;
+  return __builtin_amdgcn_classf(v, 0x260) ? v : q;
 }
 
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
@@ -158,9 +163,9 @@ struct Step {
   bool random_p;
 };
 
-// Four values' update; `w` holds the master copy or the parameter.  Products and sums round one by
-// one (no fused multiply-add): a state's code then follows from single fp32 operations, and the same
-// step written out in them gives the same bits.
+// Four values' update; `w` holds the master copy or the parameter.  The moments' products and sums
+// round one by one (no fused multiply-add): a state's code then follows from single fp32 operations,
+// and the same step written out in them gives the same bits.
 __device__ __forceinline__ void update4(const Step& h, float (&g)[4], float (&m)[4], float (&v)[4], float (&w)[4],
                                         float (&root)[4]) {
 #pragma clang fp contract(off)
@@ -169,8 +174,8 @@ __device__ __forceinline__ void update4(const Step& h, float (&g)[4], float (&m)
     g[j] *= h.gs;
     m[j] = h.b1 * m[j] + h.a1 * g[j];
     v[j] = h.b2 * v[j] + (h.a2 * g[j]) * g[j];
-    root[j] = sqrtf(v[j]);
-    w[j] = w[j] * h.keep - (h.rate * m[j]) * __builtin_amdgcn_rcpf(root[j] * h.inv_rc2 + h.eps);
+    root[j] = root_of(v[j]);
+    w[j] = __builtin_fmaf(w[j], h.keep, -(h.rate * m[j]) * __builtin_amdgcn_rcpf(__builtin_fmaf(root[j], h.inv_rc2, h.eps)));
   }
 }
 
@@ -184,12 +189,12 @@ __device__ __forceinline__ void encode4(const float (&m)[4], const float (&root)
   cm = cr = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t a = code_of(fminf(fabsf(m[j]) * im, 448.0f), u[j] & 0xFFFFu);
-    cm |= (a | (m[j] < 0.0f ? 0x80u : 0u)) << (8 * j);
+    const uint32_t a = code_of(fminf(fabsf(m[j]) * im, 448.0f), (u[j] << 4) & 0xFFFF0u);
+    cm |= (a | (__float_as_uint(m[j]) >> 24 & 0x80u)) << (8 * j);
     const float y = fminf(root[j] * ir, 448.0f);
-    uint32_t b = code_of(y, u[j] >> 16);
-    if (b == 0 && y > 0.0f) b = 1;  // a root above 0 stays above 0: it divides the next step
-    cr |= b << (8 * j);
+    // a root above 0 stays above 0: it divides the next step
+    const uint32_t least = __float_as_uint(y) < 1u ? 0u : 1u, b = code_of(y, (u[j] >> 12) & 0xFFFF0u);
+    cr |= (b > least ? b : least) << (8 * j);
   }
 }
 
@@ -206,7 +211,8 @@ __device__ __forceinline__ void random4(const float (&w)[4], const uint32_t (&u)
 // read and written once (non-temporal).  Bound by HBM: 604M bf16 weights with fp32 master copies take
 // 2.95 ms with fp32 states (28 bytes a value, 5.7 TB/s) and 1.60 ms with 8-bit states (16, 6.1 TB/s).
 // One run a wave and no more: 4 runs of a wave in turn 3.08 and 1.72 ms, two of them in flight together
-// 3.02 and 1.66; cached stores 3.11 and 1.79.
+// 3.02 and 1.66; cached stores 3.11 and 1.79.  The step's number on the device costs a wave an expm1: 8-bit
+// states 1.73 ms (by powers in 64 bits in every lane: 2.15 to 2.39).
 template <bool P32, bool MASTER, bool G32, bool EIGHT>
 __device__ __forceinline__ void adamw_run(const AdamTensor& T, const Step& h, int64_t b, int lane) {
   const int64_t i = b + lane * 4;
@@ -321,9 +327,12 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamBatch batch, Ad
   h.inv_rc2 = hp.inv_rc2;
   uint64_t step = hp.step;
   if (hp.d_step) {
+    // 1 - beta^step = -expm1(step ln beta): beta1 in the even lanes, beta2 in the odd ones
     step = (uint64_t)*hp.d_step;
-    inv_c1 = (float)(1.0 / one_less_power(hp.b1d, step));
-    h.inv_rc2 = (float)(1.0 / sqrt(one_less_power(hp.b2d, step)));
+    const float c = -expm1f((float)((double)step * (threadIdx.x & 1 ? hp.ln_b2 : hp.ln_b1)));
+    const float inv = inverse(c);
+    inv_c1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), 0));
+    h.inv_rc2 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(__builtin_amdgcn_sqrtf(inv)), 1));
   }
   const uint64_t key = step_key(hp.seed, step, (uint64_t)(hp.first_tensor + which));
   h.k0 = (uint32_t)key, h.k1 = (uint32_t)(key >> 32);
