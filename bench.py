@@ -57,7 +57,8 @@ STAGE_KERNEL_BF16 = {"gemm_up": "moe::grouped_gemm_kernel<0,", "gemm_down": "moe
                      "plan": "moe::plan_", "tile_map": "moe::tile_map_kernel", "wg_split": "moe::wg_split_kernel",
                      "tokrow": "moe::tokrow_kernel", "permute": "moe::permute_kernel",
                      "gemm_fused": "moe::fused_forward_kernel", "fwd_queue": "moe::fwd_queue_kernel",
-                     "ksort": "moe::kstep_sort_kernel"}
+                     "ksort": "moe::kstep_sort_kernel", "balance": "moe::balance_", "norm": "moe::norm_",
+                     "grad_norm": "moe::grad_norm_", "adamw": "moe::adamw_kernel"}
 # blockwise fp8: the four data GEMMs in e4m3, the weight gradients in bf16 on x dequantised to bf16
 STAGE_KERNEL_FP8 = dict(STAGE_KERNEL_BF16, gemm_up="moe::grouped_gemm_fp8_kernel<0>",
                         gemm_down="moe::grouped_gemm_fp8_kernel<1>", gemm_dact="moe::grouped_gemm_fp8_kernel<2>",

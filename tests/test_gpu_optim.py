@@ -280,6 +280,9 @@ def test_step_and_rate_on_the_device():
         for p in params:
             p.guards()
             check(p, lr=float(np.float32(1e-2)), t=t)
+    p = Param(300, rng)                  # betas of 0 have no bias
+    step([p], b1=0.0, b2=0.0, t=0, d_step=torch.tensor([9], dtype=torch.int64, device="cuda"))
+    check(p, b1=0.0, b2=0.0, t=9)
 
 
 def test_extreme_gradients():
