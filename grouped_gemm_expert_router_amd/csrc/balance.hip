@@ -21,12 +21,16 @@ constexpr int kBalRedThreads = 1024;
 
 // Tokens of a tile: at most 1024 tiles, whose partial sums few blocks add, until a tile has 512 tokens (its
 // fp32 sums stay short); then up to 65536 tiles.  Both directions of 131071 tokens, 256 experts in 37
-// groups: 512 tiles 119 us, 1024 tiles 113, 2048 tiles 116.
+// groups: 512 tiles 119 us, 1024 tiles 113, 2048 tiles 116.  Short batches: one tile, and so one launch, up
+// to 128 tokens (100 x 128: 13.1 us, as two tiles 16.4); then tiles of 32 tokens up to 8192 (5000 x 119:
+// 17.5 us, tiles of 64 18.0), of 64 behind (16384 x 128: 20.8, of 128 22.0).
 int balance_tile(int64_t T) {
+  if (T <= 128) return 128;
   int64_t t = (T + 1023) / 1024;
   if (t > 512) t = 512;
   if (t < (T + 65535) / 65536) t = (T + 65535) / 65536;
-  return t < 64 ? 64 : (int)t;
+  const int least = T <= 8192 ? 32 : 64;
+  return t < least ? least : (int)t;
 }
 
 int64_t al256i(int64_t x) { return (x + 255) & ~(int64_t)255; }
@@ -261,48 +265,11 @@ __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
   }
 }
 
-namespace {
-
-// The losses from the groups' terms, by one block in a fixed order; sh: 64 doubles.
-__device__ __forceinline__ void write_losses(const double* part, const double* zpart, int32_t* tokens, int S, int chunks,
-                                             float* losses, double* sh) {
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  double bal = 0.0, zs = 0.0;
-  int32_t groups = 0, total = 0;
-  for (int64_t i = tid; i < (int64_t)S * chunks; i += kBalRedThreads) bal += part[i];
-  for (int i = tid; i < S; i += kBalRedThreads) {
-    const int32_t m = tokens[i];
-    total += m;
-    groups += m > 0;
-    zs += zpart[i];
-  }
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    bal += __shfl_xor(bal, m, 64);
-    zs += __shfl_xor(zs, m, 64);
-    total += __shfl_xor(total, m, 64);
-    groups += __shfl_xor(groups, m, 64);
-  }
-  __syncthreads();
-  if (lane == 0) sh[wv] = bal, sh[16 + wv] = zs, sh[32 + wv] = total, sh[48 + wv] = groups;
-  __syncthreads();
-  if (tid != 0) return;
-  bal = 0.0, zs = 0.0;
-  double n = 0.0, g = 0.0;
-  for (int w = 0; w < kBalRedThreads / 64; ++w) bal += sh[w], zs += sh[16 + w], n += sh[32 + w], g += sh[48 + w];
-  losses[0] = g > 0.0 ? (float)(bal / g) : 0.0f;
-  losses[1] = n > 0.0 ? (float)(zs / n) : 0.0f;
-  tokens[S] = (int32_t)n;
-  tokens[S + 1] = (int32_t)g;
-}
-
-}  // namespace
-
 // One block per (chunk of 64 * W columns, group): its 16 waves are W columns of 64 by 16 / W rows; adds
 // the pieces of the group's tiles in a fixed order (64-bit sums) and writes the counts.  A grid of one
 // block writes the losses too; else balance_final_kernel does (a last block found by a counter needs a
-// fence that writes the L2s back: 14 us for 2 blocks, against 4 and 4 for the two launches or 8 for one
-// block).  Latency: 16384 x 128, 256 pieces: 8 us; 131071 x 256, 37 groups: 7 us and 4.
+// fence that writes the L2s back: 14 us for 2 blocks, against 4 and 4 for the two launches or 6 for one
+// block).  Latency: 16384 x 128, 256 pieces: 6 us; 131071 x 256, 37 groups: 7 us and 4.
 template <int W>
 __global__ __launch_bounds__(kBalRedThreads) void balance_reduce_kernel(
     const float* __restrict__ Pp, const int32_t* __restrict__ Cp, const int32_t* __restrict__ np,
@@ -323,6 +290,12 @@ __global__ __launch_bounds__(kBalRedThreads) void balance_reduce_kernel(
     z = goff[g + 1] > T ? T : goff[g + 1];
   }
   const int b0 = z > a ? a / tile : 0, b1 = z > a ? (z - 1) / tile + 1 : 0;
+  int32_t n = 0;
+  double zs = 0.0;
+  for (int b = b0 + tid; b < b1; b += kBalRedThreads) {
+    n += np[b + g];
+    zs += (double)zp[b + g];
+  }
   double P = 0.0;
   int32_t C = 0;
   if (c < E) {
@@ -332,12 +305,6 @@ __global__ __launch_bounds__(kBalRedThreads) void balance_reduce_kernel(
       P += (double)Pp[at];
       C += Cp[at];
     }
-  }
-  int32_t n = 0;
-  double zs = 0.0;
-  for (int b = b0 + tid; b < b1; b += kBalRedThreads) {
-    n += np[b + g];
-    zs += (double)zp[b + g];
   }
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) {
@@ -365,21 +332,55 @@ __global__ __launch_bounds__(kBalRedThreads) void balance_reduce_kernel(
     if (lane == 0) sh[wv] = dot;
   }
   __syncthreads();
-  if (tid == 0) {
-    dot = 0.0;
-    for (int w = 0; w < W; ++w) dot += sh[w];
-    part[(int64_t)g * chunks + blockIdx.x] = n > 0 ? dot * (double)E / ((double)k * (double)n * (double)n) : 0.0;
-    if (blockIdx.x == 0) tokens[g] = n, zpart[g] = zs;
+  if (tid != 0) return;
+  dot = 0.0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) dot += sh[w];
+  const double term = n > 0 ? dot * (double)E / ((double)k * (double)n * (double)n) : 0.0;
+  if (gridDim.x * gridDim.y == 1) {  // one group, seen whole
+    losses[0] = (float)term;
+    losses[1] = n > 0 ? (float)(zs / n) : 0.0f;
+    tokens[0] = tokens[1] = n;
+    tokens[2] = n > 0;
+    return;
   }
-  if (gridDim.x * gridDim.y > 1) return;
-  __syncthreads();
-  write_losses(part, zpart, tokens, S, chunks, losses, sh);
+  part[(int64_t)g * chunks + blockIdx.x] = term;
+  if (blockIdx.x == 0) tokens[g] = n, zpart[g] = zs;
 }
 
-__global__ __launch_bounds__(kBalRedThreads) void balance_final_kernel(const double* part, const double* zpart, int S,
+// The losses from the groups' terms, in a fixed order, by one wave for few of them.
+template <int NT>
+__global__ __launch_bounds__(NT) void balance_final_kernel(const double* part, const double* zpart, int S,
                                                                        int chunks, int32_t* tokens, float* losses) {
-  __shared__ double sh[64];
-  write_losses(part, zpart, tokens, S, chunks, losses, sh);
+  __shared__ double sh[4][NT / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  double bal = 0.0, zs = 0.0;
+  int32_t groups = 0, total = 0;
+  for (int64_t i = tid; i < (int64_t)S * chunks; i += NT) bal += part[i];
+  for (int i = tid; i < S; i += NT) {
+    const int32_t m = tokens[i];
+    total += m;
+    groups += m > 0;
+    zs += zpart[i];
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    bal += __shfl_xor(bal, m, 64);
+    zs += __shfl_xor(zs, m, 64);
+    total += __shfl_xor(total, m, 64);
+    groups += __shfl_xor(groups, m, 64);
+  }
+  if (lane == 0) sh[0][wv] = bal, sh[1][wv] = zs, sh[2][wv] = total, sh[3][wv] = groups;
+  __syncthreads();
+  if (tid != 0) return;
+  bal = 0.0, zs = 0.0;
+  double n = 0.0, g = 0.0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) bal += sh[0][w], zs += sh[1][w], n += sh[2][w], g += sh[3][w];
+  losses[0] = g > 0.0 ? (float)(bal / g) : 0.0f;
+  losses[1] = n > 0.0 ? (float)(zs / n) : 0.0f;
+  tokens[S] = (int32_t)n;
+  tokens[S + 1] = (int32_t)g;
 }
 
 // The gradient: kL lanes per token.  Since sum_e p = 1, an integer near their mean is taken off the
@@ -483,8 +484,7 @@ hipError_t launch_balance_forward(const float* logits, const int32_t* ids, const
   const BalWs w = bal_ws(T, E, S, (char*)ws);
   const int tile = balance_tile(T);
   const unsigned tiles = (unsigned)((T + (int64_t)tile - 1) / tile);
-  // one tile and one group of all tokens: the one block writes the results (64x8 tokens by experts: 4 us
-  // against 4 and 6 us for the reduction's launch)
+  // one tile and one group of all tokens: the one block writes the results
   const bool one = tiles == 1 && !goff;
   const BalOut whole{one ? counts : nullptr, tokens, losses};
   if (tiles > 0) {
@@ -510,7 +510,10 @@ hipError_t launch_balance_forward(const float* logits, const int32_t* ids, const
 #undef MOE_BAL_CALL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || chunks * S == 1) return e;
-  balance_final_kernel<<<1, kBalRedThreads, 0, st>>>(w.part, w.zpart, S, chunks, tokens, losses);
+  if ((int64_t)chunks * S <= 512)
+    balance_final_kernel<64><<<1, 64, 0, st>>>(w.part, w.zpart, S, chunks, tokens, losses);
+  else
+    balance_final_kernel<kBalRedThreads><<<1, kBalRedThreads, 0, st>>>(w.part, w.zpart, S, chunks, tokens, losses);
   return hipGetLastError();
 }
 

@@ -83,7 +83,8 @@ CASES = {
     "E256": dict(T=65, E=256, k=8), "E500": dict(T=40, E=500, k=8), "E1024_k64": dict(T=33, E=1024, k=64),
     "E7": dict(T=200, E=7, k=2), "E65": dict(T=64, E=65, k=5), "E129": dict(T=130, E=129, k=8),
     "E509": dict(T=66, E=509, k=8), "E1023": dict(T=9, E=1023, k=3),
-    "one_token": dict(T=1, E=128, k=8), "no_add": dict(T=100, E=64, k=4, add=False),
+    "one_token": dict(T=1, E=128, k=8), "one_tile": dict(T=128, E=33, k=3), "two_tiles": dict(T=129, E=48, k=4),
+    "tiles_of_64": dict(T=8193, E=24, k=2, S=3), "no_add": dict(T=100, E=64, k=4, add=False),
     "mask": dict(T=257, E=64, k=4, mask=True), "seqs": dict(T=400, E=96, k=4, S=9, mask=True),
     # tiles of more than 64 tokens: T > 1024 * 64
     "long": dict(T=70001, E=16, k=2, S=5, mask=True),

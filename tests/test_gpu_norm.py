@@ -159,9 +159,10 @@ def test_forms(h, w, post, pre, gate):
 
 def test_many_rows_sum_in_a_fixed_order():
     """More rows than blocks walk at once; weights' gradients bitwise the same from run to run."""
-    for T, d in ((20001, 64), (9001, 200), (2600, 1024), (2311, 2048), (700, 4096), (600, 8000)):
-        print(f"[case] norm rows T={T} d={d}", flush=True)
-        c = make(T, d, BF16, F32, "channel", seed=T)
+    for T, d, gate in ((20001, 64, "channel"), (9001, 200, "token"), (2600, 1024, "channel"), (2311, 2048, "full"),
+                       (1100, 1536, "token"), (700, 4096, "channel"), (600, 8000, "full"), (520, 16384, "channel")):
+        print(f"[case] norm rows T={T} d={d} {gate}", flush=True)
+        c = make(T, d, BF16, F32, gate, seed=T)
         h_out, x = forward(c)
         check_forward(c, h_out, x)
         o = backward(c, h_out)
