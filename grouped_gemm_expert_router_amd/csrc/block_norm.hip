@@ -15,7 +15,6 @@ namespace moe {
 
 namespace {
 
-constexpr int64_t kNormMaxBlocks = (int64_t)1 << 21;  // of up to 1024 threads: a grid has fewer than 2^32
 enum { G_NONE = 0, G_CHANNEL = 1, G_TOKEN = 2, G_FULL = 3 };
 
 // 8 consecutive values as they lie in memory, loaded once (non-temporal): a row's next loads are
@@ -85,10 +84,9 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // Rows are spread over LR lanes of 8 values each, NV times: a part of a wave for short rows (heads), up
-// to 16 waves for long ones.  A block holds kRows rows: forward one, or 256 threads of short ones;
-// backward the most that 1024 threads hold (a power of two), one block a compute unit.
-constexpr int norm_threads(int LR) { return LR <= 128 ? 256 : LR; }
-constexpr int norm_bwd_threads(int LR) { return 2 * LR > 1024 ? LR : LR % 192 == 0 ? 768 : 1024; }
+// to 16 waves for long ones.  A block holds the most rows that 1024 threads do (a power of two), and
+// there is one block a compute unit.
+constexpr int norm_threads(int LR) { return 2 * LR > 1024 ? LR : LR % 192 == 0 ? 768 : 1024; }
 
 // The thread's row in its block; the same for a whole wave (and known to be, so that a row's addresses
 // stay in scalar registers) but for rows on a part of a wave.
@@ -130,8 +128,11 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
 
 }  // namespace
 
-// The row stays in registers between its passes.  Bound by HBM: 16384 rows of 2048 in bf16, both norms: 47
-// us, 5.7 TB/s (non-temporal both ways; cached 51 us); lanes without values cost it (1032 of 1536: 4.7 TB/s).
+// A block walks rows a grid apart, each row's loads issued before the row before is worked on; a row
+// stays in registers between its passes, and so do the weights (cw = out_scale w_post and a channel's
+// gate).  Bound by HBM: 16384 rows of 2048 in bf16, both norms: 45 us, 5.9 TB/s (a block for each row: 48;
+// cached loads and stores 51); 64527 rows of 520: 50 us (a block for two rows: 62); 3728 of 9000: 49 us
+// (without the loads ahead 55).
 template <int LR, int NV, bool HF32>
 __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* h, const void* __restrict__ w_post,
@@ -139,62 +140,78 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
   constexpr int kRows = norm_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
   __shared__ float sh[kRows][2][W];
   const int slot = row_slot<LR>(), lane = threadIdx.x % LR, wave = lane >> 6;
-  // one turn unless there are more rows than a grid's blocks take
-  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += (int64_t)gridDim.x * kRows) {
-    if (t0 >= (int64_t)gridDim.x * kRows) lds_barrier();  // the sums of the turn before have been read
-    const int64_t t = t0 + slot;
-    const bool on = t < p.T;
-    const int64_t base = on ? t * p.d : 0;
-    Raw8<false> yr[NV];
-    Raw8<HF32> hr[NV];
+  float wp[NV][8], cw[NV][8];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int c = (n * LR + lane) * 8;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wp[n][i] = 0.0f, cw[n][i] = p.out_scale;
+    if (c < p.d) {
+      if (x) load_w8(w_pre, c, p.w_f32, wp[n]);
+      if (w_post) {
+        load_w8(w_post, c, p.w_f32, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cw[n][i] *= w[i];
+      }
+      if (p.gate == G_CHANNEL) {
+        load_w8(gate, c, p.w_f32, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cw[n][i] *= w[i];
+      }
+    }
+  }
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  Raw8<false> yr[NV];
+  Raw8<HF32> hr[NV];
+  float gt = 1.0f;
+  const auto fetch = [&](int64_t t) {  // a row as it lies in memory
+    gt = 1.0f;
+    if (p.gate == G_TOKEN && t < p.T) gt = load1(gate, t, p.w_f32);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * LR + lane) * 8;
       hr[n].zero();
       yr[n].zero();
-      if (on && c < p.d) {
-        hr[n].load(h, base + c);
-        if (y) yr[n].load(y, base + c);
+      if (t < p.T && c < p.d) {
+        hr[n].load(h, t * p.d + c);
+        if (y) yr[n].load(y, t * p.d + c);
       }
     }
-    float hv[NV][8];
+  };
+  fetch((int64_t)blockIdx.x * kRows + slot);
+  int par = 0;  // the sums' two buffers in turn
+  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += step) {
+    const int64_t t = t0 + slot;
+    const bool on = t < p.T;
+    const int64_t base = on ? t * p.d : 0;
+    float hv[NV][8], yv[NV][8];
 #pragma unroll
-    for (int n = 0; n < NV; ++n) hr[n].get(hv[n]);
-    float s[1] = {0.0f};
+    for (int n = 0; n < NV; ++n) hr[n].get(hv[n]), yr[n].get(yv[n]);
+    float s[1] = {0.0f}, sq = gt;
+    if (t0 + step < p.T) fetch(t + step);
     if (y) {
-      float sq = p.out_scale;
-      if (p.gate == G_TOKEN && on) sq *= load1(gate, t, p.w_f32);
       if (w_post) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-          float yv[8];
-          yr[n].get(yv);
+        for (int n = 0; n < NV; ++n)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] += yv[i] * yv[i];
-        }
-        row_sum<LR, 1>(s, sh[slot][0], wave);
+          for (int i = 0; i < 8; ++i) s[0] += yv[n][i] * yv[n][i];
+        row_sum<LR, 1>(s, sh[slot][par], wave);
+        par ^= 1;
         sq *= rsqrtf(s[0] * p.inv_d + p.eps);
       }
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
         const int c = (n * LR + lane) * 8;
         if (!on || c >= p.d) continue;
-        float m[8], w[8], yv[8];
-        yr[n].get(yv);
+        if (p.gate == G_FULL) {
+          float w[8];
+          load_w8(gate, base + c, p.w_f32, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = sq;
-        if (w_post) {
-          load_w8(w_post, c, p.w_f32, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m[i] *= w[i];
-        }
-        if (p.gate == G_CHANNEL || p.gate == G_FULL) {
-          load_w8(gate, p.gate == G_FULL ? base + c : c, p.w_f32, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m[i] *= w[i];
+          for (int i = 0; i < 8; ++i) yv[n][i] *= w[i];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) hv[n][i] = p.res_scale * hv[n][i] + yv[i] * m[i];
+        for (int i = 0; i < 8; ++i) hv[n][i] = p.res_scale * hv[n][i] + yv[n][i] * (cw[n][i] * sq);
         store8<HF32>(h_out, base + c, hv[n]);
       }
     }
@@ -204,16 +221,16 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
     for (int n = 0; n < NV; ++n)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[0] += hv[n][i] * hv[n][i];
-    row_sum<LR, 1>(s, sh[slot][1], wave);
+    row_sum<LR, 1>(s, sh[slot][par], wave);
+    par ^= 1;
     const float sp = rsqrtf(s[0] * p.inv_d + p.eps);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * LR + lane) * 8;
       if (!on || c >= p.d) continue;
       float w[8];
-      load_w8(w_pre, c, p.w_f32, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] *= hv[n][i] * sp;
+      for (int i = 0; i < 8; ++i) w[i] = wp[n][i] * hv[n][i] * sp;
       store8<false>(x, base + c, w);
     }
   }
@@ -243,11 +260,11 @@ struct RowIn {
 // sums, and 5 for norm_reduce_kernel; 4099 of 7168 with an fp32 stream: 100 us, 5.3 TB/s (17 turns of
 // 256 blocks for 16.01 rows each).
 template <int LR, int NV, bool HF32, bool Y, bool P, bool FULL>
-__global__ __launch_bounds__(norm_bwd_threads(LR)) void norm_backward_kernel(
+__global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* __restrict__ h_out, const void* __restrict__ w_post,
     const void* __restrict__ gate, const void* __restrict__ w_pre, const void* dh_out, const uint16_t* __restrict__ dx,
     void* dh, uint16_t* __restrict__ dy, void* __restrict__ dgate, float* __restrict__ part, int64_t part_stride) {
-  constexpr int kRows = norm_bwd_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
+  constexpr int kRows = norm_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
   __shared__ float sh[kRows][2][3 * W];
   const int slot = row_slot<LR>(), lane = threadIdx.x % LR, wave = lane >> 6;
   // the weights of a lane's columns: in registers, or for the longest rows in LDS (16 values a lane of each
@@ -449,7 +466,7 @@ __global__ __launch_bounds__(norm_bwd_threads(LR)) void norm_backward_kernel(
     if (Y) red[kCols + slot * LR * 8 + lane * 8 + i] = a_post[0][i];
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < p.d; c += norm_bwd_threads(LR)) {
+  for (int c = threadIdx.x; c < p.d; c += norm_threads(LR)) {
     float u = 0.0f, v = 0.0f;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -519,13 +536,11 @@ int norm_lanes(int d) {
     }                                              \
   } while (0)
 
-int norm_rows_per_block(int d) { return norm_threads(norm_lanes(d)) / norm_lanes(d); }
-
-// Blocks of the backward pass: one a compute unit, each with its rows' loads ahead.  Smaller blocks, more
-// of them, write more partial sums and read memory in smaller pieces (16384 rows of 2048 values: 2 blocks
-// of one row a unit 78.5 us, 4 of them 85, 1 block of two rows 75.2, of four rows 73.4).
-int norm_bwd_blocks(int64_t T, int d) {
-  const int rows = norm_bwd_threads(norm_lanes(d)) / norm_lanes(d);
+// One block a compute unit, each with its rows' loads ahead.  Smaller blocks, more of them, write more
+// partial sums and read memory in smaller pieces (backward, 16384 rows of 2048 values: 2 blocks of one row
+// a unit 78.5 us, 4 of them 85, 1 block of two rows 75.2, of four rows 73.4).
+int norm_blocks(int64_t T, int d) {
+  const int rows = norm_threads(norm_lanes(d)) / norm_lanes(d);
   const int64_t b = (T + rows - 1) / rows;
   return (int)(b < 256 ? b : 256);
 }
@@ -533,14 +548,13 @@ int norm_bwd_blocks(int64_t T, int d) {
 }  // namespace
 
 size_t norm_ws_bytes(int64_t T, int d) {
-  return (size_t)(2 * (int64_t)norm_bwd_blocks(T, d) * d * 4);
+  return (size_t)(2 * (int64_t)norm_blocks(T, d) * d * 4);
 }
 
 hipError_t launch_norm_forward(const NormArgs& p, const uint16_t* y, const void* h, const void* w_post,
                                const void* gate, const void* w_pre, void* h_out, uint16_t* x, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  const int64_t all = (p.T + norm_rows_per_block(p.d) - 1) / norm_rows_per_block(p.d);
-  const unsigned blocks = (unsigned)(all < kNormMaxBlocks ? all : kNormMaxBlocks);  // a grid's threads fit 32 bits
+  const int blocks = norm_blocks(p.T, p.d);
 #define MOE_NORM_CALL(LR, NV)                                                                                       \
   if (p.h_f32)                                                                                                     \
     norm_forward_kernel<LR, NV, true><<<blocks, norm_threads(LR), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x);  \
@@ -554,14 +568,14 @@ hipError_t launch_norm_forward(const NormArgs& p, const uint16_t* y, const void*
 hipError_t launch_norm_backward(const NormArgs& p, const uint16_t* y, const void* h_out, const void* w_post,
                                 const void* gate, const void* w_pre, const void* dh_out, const uint16_t* dx, void* dh,
                                 uint16_t* dy, void* dw_post, void* dgate, void* dw_pre, float* part, hipStream_t st) {
-  const int blocks = norm_bwd_blocks(p.T, p.d);
+  const int blocks = norm_blocks(p.T, p.d);
   const int64_t stride = (int64_t)blocks * p.d;
   void* dg = p.gate == G_CHANNEL ? dgate : nullptr;
   const bool pre = dw_pre, post = dw_post || dg;
   if (p.T > 0) {
     const bool full = y && p.gate == G_FULL;
 #define MOE_NORM_RUN(LR, NV, H, Y, P, F)                                                                              \
-  norm_backward_kernel<LR, NV, H, Y, P, F><<<blocks, norm_bwd_threads(LR), 0, st>>>(p, y, h_out, w_post, gate, w_pre, dh_out, \
+  norm_backward_kernel<LR, NV, H, Y, P, F><<<blocks, norm_threads(LR), 0, st>>>(p, y, h_out, w_post, gate, w_pre, dh_out, \
                                                                               dx, dh, dy, dgate,                       \
                                                                               pre || post ? part : nullptr, stride)
 #define MOE_NORM_FORM(LR, NV, H)                                 \
