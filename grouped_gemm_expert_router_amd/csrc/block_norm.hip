@@ -85,8 +85,10 @@ __device__ __forceinline__ void lds_barrier() {
 
 // Rows are spread over LR lanes of 8 values each, NV times: a part of a wave for short rows (heads), up
 // to 16 waves for long ones.  A block holds the most rows that 1024 threads do (a power of two), and
-// there is one block a compute unit.
+// there is one block a compute unit.  Forward, while all rows fit the card at once: blocks of 256 threads
+// or of one row, as many as hold them.
 constexpr int norm_threads(int LR) { return 2 * LR > 1024 ? LR : LR % 192 == 0 ? 768 : 1024; }
+constexpr int norm_few_threads(int LR) { return LR <= 128 ? 256 : LR; }
 
 // The thread's row in its block; the same for a whole wave (and known to be, so that a row's addresses
 // stay in scalar registers) but for rows on a part of a wave.
@@ -129,37 +131,44 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
 }  // namespace
 
 // A block walks rows a grid apart, each row's loads issued before the row before is worked on; a row
-// stays in registers between its passes, and so do the weights (cw = out_scale w_post and a channel's
-// gate).  Bound by HBM: 16384 rows of 2048 in bf16, both norms: 45 us, 5.9 TB/s (a block for each row: 48;
+// stays in registers between its passes, and so do the weights.  FEW: each block has its rows once, and
+// loads the weights where it needs them, so that 64 registers do and a compute unit holds 2048 threads
+// (rows of 2048 values: 1: 2.4 us, one block a unit 2.9; 512: 3.2 and 4.0; 2048: 6.3 and 7.3; 4096, where
+// the rows no longer fit: 14.5 and 13.9).  Bound by HBM: 16384 rows of 2048 in bf16, both norms: 45 us, 5.9 TB/s (a block for each row: 48;
 // cached loads and stores 51); 64527 rows of 520: 50 us (a block for two rows: 62); 3728 of 9000: 49 us
 // (without the loads ahead 55).
-template <int LR, int NV, bool HF32>
-__global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
+template <int LR, int NV, bool HF32, bool FEW>
+__global__ __launch_bounds__(FEW ? norm_few_threads(LR) : norm_threads(LR), FEW && NV == 1 ? 8 : 1) void norm_forward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* h, const void* __restrict__ w_post,
     const void* __restrict__ gate, const void* __restrict__ w_pre, void* h_out, uint16_t* __restrict__ x) {
-  constexpr int kRows = norm_threads(LR) / LR, W = LR < 64 ? 1 : LR / 64;
+  constexpr int kRows = (FEW ? norm_few_threads(LR) : norm_threads(LR)) / LR, W = LR < 64 ? 1 : LR / 64;
   __shared__ float sh[kRows][2][W];
   const int slot = row_slot<LR>(), lane = threadIdx.x % LR, wave = lane >> 6;
-  float wp[NV][8], cw[NV][8];
-#pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int c = (n * LR + lane) * 8;
+  // the weights of a lane's columns: w_pre, and out_scale w_post with a channel's gate
+  const auto load_pre = [&](int c, float (&v)[8]) { load_w8(w_pre, c, p.w_f32, v); };
+  const auto load_post = [&](int c, float (&v)[8]) {
     float w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wp[n][i] = 0.0f, cw[n][i] = p.out_scale;
-    if (c < p.d) {
-      if (x) load_w8(w_pre, c, p.w_f32, wp[n]);
-      if (w_post) {
-        load_w8(w_post, c, p.w_f32, w);
+    for (int i = 0; i < 8; ++i) v[i] = p.out_scale;
+    if (w_post) {
+      load_w8(w_post, c, p.w_f32, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cw[n][i] *= w[i];
-      }
-      if (p.gate == G_CHANNEL) {
-        load_w8(gate, c, p.w_f32, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cw[n][i] *= w[i];
-      }
+      for (int i = 0; i < 8; ++i) v[i] *= w[i];
     }
+    if (p.gate == G_CHANNEL) {
+      load_w8(gate, c, p.w_f32, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= w[i];
+    }
+  };
+  float wp[NV][8], cw[NV][8];
+#pragma unroll
+  for (int n = 0; n < NV && !FEW; ++n) {
+    const int c = (n * LR + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wp[n][i] = cw[n][i] = 0.0f;
+    if (c < p.d && x) load_pre(c, wp[n]);
+    if (c < p.d && y) load_post(c, cw[n]);
   }
   const int64_t step = (int64_t)gridDim.x * kRows;
   Raw8<false> yr[NV];
@@ -181,7 +190,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
   };
   fetch((int64_t)blockIdx.x * kRows + slot);
   int par = 0;  // the sums' two buffers in turn
-  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += step) {
+  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 = FEW ? p.T : t0 + step) {
     const int64_t t = t0 + slot;
     const bool on = t < p.T;
     const int64_t base = on ? t * p.d : 0;
@@ -189,7 +198,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
 #pragma unroll
     for (int n = 0; n < NV; ++n) hr[n].get(hv[n]), yr[n].get(yv[n]);
     float s[1] = {0.0f}, sq = gt;
-    if (t0 + step < p.T) fetch(t + step);
+    if (!FEW && t0 + step < p.T) fetch(t + step);
     if (y) {
       if (w_post) {
 #pragma unroll
@@ -204,6 +213,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
       for (int n = 0; n < NV; ++n) {
         const int c = (n * LR + lane) * 8;
         if (!on || c >= p.d) continue;
+        if (FEW) load_post(c, cw[n]);
         if (p.gate == G_FULL) {
           float w[8];
           load_w8(gate, base + c, p.w_f32, w);
@@ -228,6 +238,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_forward_kernel(
     for (int n = 0; n < NV; ++n) {
       const int c = (n * LR + lane) * 8;
       if (!on || c >= p.d) continue;
+      if (FEW) load_pre(c, wp[n]);
       float w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = wp[n][i] * hv[n][i] * sp;
@@ -554,14 +565,20 @@ size_t norm_ws_bytes(int64_t T, int d) {
 hipError_t launch_norm_forward(const NormArgs& p, const uint16_t* y, const void* h, const void* w_post,
                                const void* gate, const void* w_pre, void* h_out, uint16_t* x, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  const int blocks = norm_blocks(p.T, p.d);
-#define MOE_NORM_CALL(LR, NV)                                                                                       \
-  if (p.h_f32)                                                                                                     \
-    norm_forward_kernel<LR, NV, true><<<blocks, norm_threads(LR), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x);  \
-  else                                                                                                             \
-    norm_forward_kernel<LR, NV, false><<<blocks, norm_threads(LR), 0, st>>>(p, y, h, w_post, gate, w_pre, h_out, x)
+  const int lanes = norm_lanes(p.d), few_rows = norm_few_threads(lanes) / lanes;
+  const bool few = p.T <= 256 * 2048 / lanes;  // lanes that the card holds
+  const int blocks = few ? (int)((p.T + few_rows - 1) / few_rows) : norm_blocks(p.T, p.d);
+#define MOE_NORM_LAUNCH(LR, NV, F, FEW)                                                                \
+  norm_forward_kernel<LR, NV, F, FEW><<<blocks, FEW ? norm_few_threads(LR) : norm_threads(LR), 0, st>>>( \
+      p, y, h, w_post, gate, w_pre, h_out, x)
+#define MOE_NORM_CALL(LR, NV)                             \
+  if (few && p.h_f32) MOE_NORM_LAUNCH(LR, NV, true, true); \
+  else if (few) MOE_NORM_LAUNCH(LR, NV, false, true);      \
+  else if (p.h_f32) MOE_NORM_LAUNCH(LR, NV, true, false);  \
+  else MOE_NORM_LAUNCH(LR, NV, false, false)
   MOE_NORM_DISPATCH(p.d, MOE_NORM_CALL);
 #undef MOE_NORM_CALL
+#undef MOE_NORM_LAUNCH
   return hipGetLastError();
 }
 

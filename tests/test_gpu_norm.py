@@ -233,3 +233,17 @@ def test_gradient_against_differences():
         down, _ = value()
         t[i] += step
         assert abs((up - down) / (2 * step) - float(o[grad][i])) <= 2.0 ** -16 * size
+
+
+@pytest.mark.parametrize("d", [64, 200, 512, 1000, 1536, 2048, 2056, 4096, 5000, 8192, 8200])
+def test_forward_many_rows(d):
+    """More rows than the card holds at once, the last turn of the blocks ragged; the last size that fits."""
+    lanes = next((n for n in (16, 32, 64, 128, 192, 256, 384, 512, 768) if d <= 8 * n), 1024)
+    T = 256 * 2048 // lanes
+    for i, (rows, h, w, gate) in enumerate([(T + 3, BF16, F32, "channel"), (T + 257, F32, BF16, "token"), (T, BF16, BF16, "full")]):
+        print(f"[case] norm T={rows} d={d} {h} {gate}", flush=True)
+        c = make(rows, d, h, w, gate, seed=500 + d + i, res=0.75, out=1.5)
+        h_out, x = forward(c)
+        check_forward(c, h_out, x)
+        same = forward(c, inplace=True)
+        assert torch.equal(same[0], h_out) and torch.equal(same[1], x)
