@@ -198,11 +198,13 @@ __device__ __forceinline__ void encode4(const float (&m)[4], const float (&root)
   }
 }
 
-// Two bf16 pairs of w, stochastically rounded with the second words of u
+// Two bf16 pairs of w, stochastically rounded with the second words of u (a NaN's bits could carry into
+// its sign)
 __device__ __forceinline__ void random4(const float (&w)[4], const uint32_t (&u)[4], uint32_t k0, uint32_t& a, uint32_t& b) {
   uint32_t q[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) q[j] = (__float_as_uint(w[j]) + (noise2(u[j], k0) & 0xFFFFu)) >> 16;
+  for (int j = 0; j < 4; ++j)
+    q[j] = w[j] == w[j] ? (__float_as_uint(w[j]) + (noise2(u[j], k0) & 0xFFFFu)) >> 16 : 0x7FC0u;
   a = q[0] | q[1] << 16;
   b = q[2] | q[3] << 16;
 }

@@ -338,9 +338,10 @@ int moe_grad_norm(const moe_tensor* tensors, int64_t n_tensors, float max_norm, 
  * rounded stochastically (a code up with the probability of the remainder; a nonzero sqrt(v) never
  * becomes zero), and so is a bf16 parameter without a master copy if `stochastic` is 1 (to nearest
  * if 0); the random bits are a function of seed, step, the tensor's place in the list and the
- * value's index, so a step is bitwise reproducible.  lr and step may live on the device (d_lr,
- * d_step) for a captured graph whose replays move on; they are read when the step runs.  The
- * tensors overlap nowhere. */
+ * value's index, so a step is bitwise reproducible.  A gradient that is not finite makes its weight
+ * NaN and leaves nothing of the 8-bit states of its 256 values; the scale of moe_grad_norm skips such
+ * a step.  lr and step may live on the device (d_lr, d_step) for a captured graph whose replays move
+ * on; they are read when the step runs.  The tensors overlap nowhere. */
 typedef struct {
   double lr;              /* >= 0 and finite; unused with d_lr */
   double beta1, beta2;    /* in [0, 1) */

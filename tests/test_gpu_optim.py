@@ -323,6 +323,24 @@ def test_grad_norm_parity(sizes, g):
         assert_close("scale", out[GUARD + 1:GUARD + 2], [scale], 2.0 ** -23 * scale)
 
 
+def test_not_a_number_stays_one():
+    """A NaN of any payload in a gradient or a parameter gives a NaN: the random bits that round a bf16
+    parameter do not carry over its exponent and sign."""
+    print("[case] adamw NaN", flush=True)
+    rng = np.random.default_rng(33)
+    for eight in (False, True):
+        p = Param(300, rng, p=BF16, g=F32, eight=eight)     # a whole run and a tail
+        at = torch.tensor([0, 5, 130, 255, 256, 299], device="cuda")
+        p.g.view(torch.int32)[at] = torch.tensor([0x7FFFFFFF, -1, 0x7F800001, 0x7FC00000, 0x7FFFFFFF, -1],
+                                                 dtype=torch.int32, device="cuda")
+        p.t["p"].view(torch.int16)[[9, 290]] = torch.tensor([0x7FFF, -1], dtype=torch.int16, device="cuda")
+        for seed in range(8):
+            step([p], seed=seed, stochastic=True)
+            nan = torch.isnan(p.t["p"])
+            assert nan[at].all() and nan[[9, 290]].all() and (eight or int(nan.sum()) == 8)
+        p.guards()
+
+
 def test_grad_norm_far_sizes_and_bad_values():
     """Squares beyond fp32's range both ways are fine in 64 bits; a NaN, an infinity and a norm beyond
     fp32 give a scale that skips the step."""
