@@ -192,8 +192,7 @@ hipError_t launch_norm_backward(const NormArgs& p, const uint16_t* y, const void
                                 const void* gate, const void* w_pre, const void* dh_out, const uint16_t* dx, void* dh,
                                 uint16_t* dy, void* dw_post, void* dgate, void* dw_pre, float* part, hipStream_t st);
 
-// gradient norm and AdamW over a list of tensors, kAdamBatch of them in a launch's arguments
-constexpr int kAdamBatch = 48;
+// gradient norm and AdamW over a list of tensors
 struct AdamScalars {
   float b1, b2, a1, a2, lr, eps, inv_c1, inv_rc2;  // a = 1 - b; 1 / (1 - b1^step), 1 / sqrt(1 - b2^step)
   double ln_b1, ln_b2;  // for a step on the device

@@ -330,7 +330,8 @@ int moe_grad_norm_workspace_bytes(const moe_tensor* tensors, int64_t n_tensors, 
 int moe_grad_norm(const moe_tensor* tensors, int64_t n_tensors, float max_norm, float* norm, float* scale,
                   void* ws, size_t ws_bytes, void* stream);
 
-/* One AdamW step on n_tensors tensors (a host array; one launch for each 48 of them):
+/* One AdamW step on n_tensors tensors (a host array; one launch for each 64 of them, or for each 54
+ * if some have 8-bit states):
  *   g' = s g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
  *   w  = (1 - lr weight_decay) w - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
  * in fp32 on the master copy where there is one, else on p.  s = *d_grad_scale, or 1.  If
