@@ -85,6 +85,17 @@ __device__ __forceinline__ int group_of(const int32_t* off, int S, int t) {
   return lo - 1;
 }
 
+// The same for a whole wave: a few offsets a lane, all loaded at once, where few loads cover them.
+__device__ __forceinline__ int wave_group_of(const int32_t* off, int S, int t) {
+  if (S >= 256) return group_of(off, S, t);
+  const int lane = threadIdx.x & 63;
+  int n = -1;
+#pragma unroll
+  for (int q = 0; q < 256; q += 64)
+    if (q <= S) n += __popcll(__ballot(q + lane <= S && off[q + lane <= S ? q + lane : 0] <= t));
+  return n;
+}
+
 constexpr int kL = 16;                      // lanes a token: a DPP row, so its sums need no LDS
 constexpr int kRows = kBalThreads / kL;     // tokens a block takes at a time
 
@@ -140,8 +151,10 @@ __device__ __forceinline__ void whole_losses(const float (&shP)[4][kCols], const
 
 // One block per tile of consecutive tokens, kL lanes per token, U tokens of a lane group in flight;
 // each lane keeps the sums of p of its own columns.  A tile is cut where a group ends; the piece of
-// tile b in group g has the slot b + g, which no other piece has (both grow along the tokens).
-// 131071 x 256 in 37 groups: 31 us, 4.5 TB/s of logits and slots, bound by the loads that four waves a
+// tile b in group g has the slot b + g, which no other piece has (both grow along the tokens).  Where
+// tiles are few, a tile's pieces are shared by blocks (gridDim.y of them: 42 tokens of 385 in 43 groups,
+// both ways: 33 us, by one block 116).
+// 131071 x 256 in 37 groups: 30 us, 4.6 TB/s of logits and slots, bound by the loads that four waves a
 // SIMD keep in flight around each token's two dependent sums (a whole wave for each token, with shuffles
 // through LDS: 117 us; four tokens in flight: 2 % less in one group, 7 % more in 37).  16384 x 128: 6 us,
 // of which the memory needs 1.5.
@@ -158,21 +171,18 @@ __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
   __shared__ float sh_z[4];
   const int tid = threadIdx.x, wv = tid >> 6, l = tid % kL, r = tid / kL;
   const int t0 = blockIdx.x * tile, t1 = T - t0 < tile ? T : t0 + tile;
-  int g = goff ? group_of(goff, S, t0) : 0;
-  int a = t0;
-  while (a < t1) {
-    // the piece [a, z) of the tile: one group, or tokens of none (before the first, behind the last)
-    int z = t1;
+  // the pieces of the tile: its part of each group, of the tokens before the first (-1) and behind the last
+  for (int g = (goff ? wave_group_of(goff, S, t0) : 0) + blockIdx.y; g <= S; g += gridDim.y) {
+    int a = t0, z = t1;
     if (goff) {
-      const int e = g < 0 ? goff[0] : (g < S ? goff[g + 1] : t1);
-      if (g < S && e < z) z = e;
-      if (z <= a) {  // an empty group
-        if (g >= S) break;
-        ++g;
-        continue;
-      }
+      if (g >= 0 && goff[g] > a) a = goff[g];
+      if (a >= t1) break;
+      if (g < S && goff[g + 1] < z) z = goff[g + 1];
+      if (z <= a) continue;  // an empty group
+    } else if (g > 0) {
+      break;
     }
-    const bool in = !goff || (g >= 0 && g < S);
+    const bool in = g >= 0 && g < S;
     for (int c = tid; c < kCols; c += kBalThreads) hist[c] = 0;
     __syncthreads();
     float acc[V * N];
@@ -260,8 +270,6 @@ __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
       }
     }
     __syncthreads();
-    a = z;
-    ++g;
   }
 }
 
@@ -393,6 +401,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
     int E, int k, int S, int tile, const float* d_in, float* d_out) {
   const int tid = threadIdx.x, l = tid % kL, r = tid / kL;
   const int t0 = blockIdx.x * tile, t1 = T - t0 < tile ? T : t0 + tile;
+  const int g0 = goff ? wave_group_of(goff, S, t0) : 0, end0 = goff ? (g0 < S ? goff[g0 + 1] : t1) : T;
   int lo = 0, hi = -1;  // the group's tokens: no group yet
   float c[V * N];
 #pragma unroll
@@ -413,7 +422,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
     }
     if (lse != -INFINITY) {  // else what was read of the logits is not used
       if (t < lo || t >= hi) {
-        int g = goff ? group_of(goff, S, (int)t) : 0;
+        int g = t < end0 ? g0 : group_of(goff, S, (int)t);
         g = g < 0 ? 0 : (g >= S ? S - 1 : g);  // a counted token lies in a group
         lo = goff ? goff[g] : 0;
         hi = goff ? goff[g + 1] : T;
@@ -488,8 +497,9 @@ hipError_t launch_balance_forward(const float* logits, const int32_t* ids, const
   const bool one = tiles == 1 && !goff;
   const BalOut whole{one ? counts : nullptr, tokens, losses};
   if (tiles > 0) {
+    const dim3 grid(tiles, tiles >= 512 ? 1 : 512 / tiles < (unsigned)S ? 512 / tiles : S);
 #define MOE_BAL_CALL(V, N)                                                                                       \
-  balance_stats_kernel<V, N><<<tiles, kBalThreads, 0, st>>>(logits, ids, mask, goff, T, E, k, S, tile, lse, w.P, \
+  balance_stats_kernel<V, N><<<grid, kBalThreads, 0, st>>>(logits, ids, mask, goff, T, E, k, S, tile, lse, w.P, \
                                                             w.C, w.n, w.z, whole)
     MOE_BAL_DISPATCH(E, MOE_BAL_CALL);
 #undef MOE_BAL_CALL

@@ -92,6 +92,10 @@ CASES = {
     "ragged": dict(T=300, E=128, k=8, offsets=np.array([3, 3, 64, 65, 65, 128, 191, 256, 290], np.int32), mask=True),
     "all_outside": dict(T=100, E=16, k=2, offsets=np.array([100, 100], np.int32)),
     "one_each": dict(T=70, E=12, k=2, offsets=np.arange(71, dtype=np.int32)),
+    # as many groups as offsets that a wave loads at a time, one less and one more, and far more
+    **{f"groups_{S}": dict(T=3 * S // 2, E=20, k=2, S=S, mask=S % 2 == 0) for S in (62, 63, 64, 127, 128, 255, 256, 1000)},
+    "more_groups_than_tokens": dict(T=42, E=385, k=3, S=43), "groups_in_few_tiles": dict(T=900, E=200, k=6, S=400, mask=True),
+    "most_groups": dict(T=3000, E=9, k=2, S=65535), "groups_in_long": dict(T=40000, E=12, k=2, S=300, mask=True),
     "local_slots": dict(T=150, E=32, k=8, ids_cut=True), "wide_logits": dict(T=90, E=40, k=4, spread=6.0),
 }
 
