@@ -67,12 +67,13 @@ BalWs bal_ws(int64_t T, int64_t E, int64_t S, char* ws) {
 }
 
 // Columns of 64 a block of the reduction takes: all of them while its 16 waves then read few rows each
-// (one block, and no launch for the losses, if there is one group), else one.
+// (one block, and no launch for the losses, if there is one group), else one.  Both directions: 16384 x 128
+// (2 x 257 rows) by one block 19.2 us, by two 20.1; 8192 x 256 (4 x 257) by one 23.2, by four 21.0.
 int balance_wide(int64_t T, int64_t E, int64_t S) {
   const int64_t rows = T > 0 ? (T + balance_tile(T) - 1) / balance_tile(T) / S + 1 : 1;
   int w = 1;
   while (w * 64 < E) w *= 2;
-  return rows * w <= 1100 ? w : 1;
+  return rows * w <= 600 ? w : 1;
 }
 
 // Last group whose first token is at or before t (-1: none).
@@ -154,7 +155,7 @@ __device__ __forceinline__ void whole_losses(const float (&shP)[4][kCols], const
 // tile b in group g has the slot b + g, which no other piece has (both grow along the tokens).  Where
 // tiles are few, a tile's pieces are shared by blocks (gridDim.y of them: 42 tokens of 385 in 43 groups,
 // both ways: 33 us, by one block 116).
-// 131071 x 256 in 37 groups: 30 us, 4.6 TB/s of logits and slots, bound by the loads that four waves a
+// 131071 x 256 in 37 groups: 31 us, 4.5 TB/s of logits and slots, bound by the loads that four waves a
 // SIMD keep in flight around each token's two dependent sums (a whole wave for each token, with shuffles
 // through LDS: 117 us; four tokens in flight: 2 % less in one group, 7 % more in 37).  16384 x 128: 6 us,
 // of which the memory needs 1.5.
@@ -531,7 +532,10 @@ hipError_t launch_balance_backward(const float* logits, const float* lse, const 
                                    const int32_t* tokens, const float* d_losses, int T, int E, int k, int S,
                                    const float* d_in, float* d_out, hipStream_t st) {
   if (T == 0) return hipSuccess;
-  const int tile = T <= (1 << 27) ? 32 : 1024;  // a grid's threads fit 32 bits
+  // tokens of a block (both directions, 128 experts: 2048 tokens by 16 11.5 us, by 32 12.0; 8192 by 32
+  // 15.3, by 16 16.3, by 64 17.6; 32768 by 64 25.8, by 32 27.4; 131071 x 256 by 64 107, by 32 111); a
+  // grid's threads fit 32 bits
+  const int tile = T <= 4096 ? 16 : T <= 12288 ? 32 : T <= (1 << 27) ? 64 : 1024;
   const unsigned tiles = (unsigned)((T + (int64_t)tile - 1) / tile);
 #define MOE_BAL_CALL(V, N)                                                                                       \
   balance_grad_kernel<V, N><<<tiles, kBalThreads, 0, st>>>(logits, lse, goff, counts, tokens, d_losses, T, E, k, \
