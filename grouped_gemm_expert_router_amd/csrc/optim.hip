@@ -10,6 +10,8 @@
 // each 256 values.  They are rounded stochastically: an average moves by (1 - b) of its distance
 // in a step, far less than half of e4m3's step of 1/8, so rounding to nearest would hold it where
 // it is; rounded up with the probability of the remainder its expectation moves as it should.
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -17,8 +19,13 @@ namespace moe {
 
 namespace {
 
-constexpr int kAdamThreads = 256;
-constexpr int kChunk = kAdamThreads * 4;  // values a block updates: 256 a wave
+// A block of the update: a wave takes 256 values.  fp32 states move 26 to 32 bytes a value in seven to nine
+// streams, and DRAM serves them best from few waves in small blocks: with one wave a block and three a SIMD,
+// 604M weights with master copies take 2.62 ms; four a SIMD 2.65, eight in blocks of four 3.02 (bf16
+// weights without master copies: 200M in 0.81 ms, 0.76, 0.84).  8-bit states are nearer the vector ALU's
+// bound and want every wave: 1.55 ms, one wave a block 1.6, five a SIMD 1.69.
+constexpr int adam_threads(bool eight) { return eight ? 256 : 64; }
+constexpr int adam_chunk(bool eight) { return adam_threads(eight) * 4; }
 
 enum { kAdamP32 = 1, kAdamG32 = 2, kAdam8bit = 4 };
 
@@ -32,11 +39,12 @@ struct AdamTensor {
   int32_t flags;
 };
 
-// Tensors of one launch, in its arguments; first: first chunk of each (below 0: earlier launches took
-// some).  Lists without 8-bit states leave the scales out and fit more tensors in a launch (60 tensors of
+// Tensors of one launch, in its arguments; first: first chunk of each, modulo 2^32 (the first tensor's
+// lies before the launch if earlier ones took some of it).  Lists without 8-bit states leave the scales out and fit more tensors in a launch (60 tensors of
 // 3333 values: 6.6 us, in two launches 10.0).
 template <bool EIGHT>
 struct AdamBatch {
+  static constexpr bool kEight = EIGHT;
   static constexpr int kMost = EIGHT ? 54 : 64;
   void* ptr[EIGHT ? 7 : 5][kMost];  // p, g, m, v, master, scales
   int64_t n8[kMost];                // 8 n + flags
@@ -81,7 +89,7 @@ __device__ __forceinline__ int tensor_of(const Batch& b, int chunk) {
 #pragma unroll
   for (int q = 0; q < Batch::kMost; q += 64) {
     const int i = q + (threadIdx.x & 63);
-    at += __popcll(__ballot(i < b.n && b.first[i < Batch::kMost ? i : 0] <= chunk));
+    at += __popcll(__ballot(i < b.n && (i == 0 || b.first[i < Batch::kMost ? i : 0] <= chunk)));
   }
   return at;
 }
@@ -225,10 +233,11 @@ __device__ __forceinline__ void random4(const float (&w)[4], const uint32_t (&u)
 
 // The 256 whole values of a wave from b: every load is issued before the first use.  The streams are
 // read and written once (non-temporal).  Bound by HBM: 604M bf16 weights with fp32 master copies take
-// 2.95 ms with fp32 states (28 bytes a value, 5.7 TB/s) and 1.60 ms with 8-bit states (16, 6.1 TB/s).
-// One run a wave and no more: 4 runs of a wave in turn 3.08 and 1.72 ms, two of them in flight together
-// 3.02 and 1.66; cached stores 3.11 and 1.79.  The step's number on the device costs a wave an expm1: 8-bit
-// states 1.73 ms (by powers in 64 bits in every lane: 2.15 to 2.39).
+// 2.62 ms with fp32 states (28 bytes a value, 6.5 TB/s) and 1.55 ms with 8-bit states (16, 6.2 TB/s).
+// One run a wave and no more (in blocks of four waves, as many as fit: 2.95 and 1.60 ms; 4 runs of a wave in
+// turn 3.08 and 1.72, two of them in flight together 3.02 and 1.66; cached stores 3.11 and 1.79).  The
+// step's number on the device costs a wave an expm1: 8-bit states 1.73 ms (by powers in 64 bits in every
+// lane: 2.15 to 2.39).
 template <bool P32, bool MASTER, bool G32, bool EIGHT>
 __device__ __forceinline__ void adamw_run(const AdamTensor& T, const Step& h, int64_t b, int lane) {
   const int64_t i = b + lane * 4;
@@ -331,7 +340,8 @@ __device__ __forceinline__ void adamw_tail(const AdamTensor& T, const Step& h, i
 }  // namespace
 
 template <bool EIGHT>
-__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamBatch<EIGHT> batch, AdamScalars hp) {
+__global__ __launch_bounds__(adam_threads(EIGHT)) __attribute__((amdgpu_waves_per_eu(EIGHT ? 1 : 3, EIGHT ? 8 : 3)))
+void adamw_kernel(AdamBatch<EIGHT> batch, AdamScalars hp) {
   Step h;
   h.gs = 1.0f;
   if (hp.d_grad_scale) {
@@ -359,7 +369,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamBatch<EIGHT> ba
   h.rate = lr * inv_c1;
   h.random_p = !(T.flags & kAdamP32) && !T.master && hp.stochastic;
   const int lane = threadIdx.x & 63;
-  const int64_t b = (int64_t)(blockIdx.x - batch.first[which]) * kChunk + (threadIdx.x >> 6) * 256;
+  const int64_t b = (int64_t)(blockIdx.x - batch.first[which]) * adam_chunk(EIGHT) + (threadIdx.x >> 6) * 256;
   if (b >= T.n) return;
   if (T.n - b < 256) {
     adamw_tail<EIGHT>(T, h, b, lane);
@@ -515,14 +525,16 @@ int64_t norm_chunks(const moe_tensor* t, int64_t n, int64_t chunk) {
 
 hipError_t launch_adamw(const moe_tensor* t, int64_t n, const AdamScalars& hp, hipStream_t st) {
   const auto run = [&](const auto& b, int64_t chunks, int64_t first) {
+    constexpr bool EIGHT = std::decay_t<decltype(b)>::kEight;
     AdamScalars h = hp;
     h.first_tensor = first;
-    adamw_kernel<<<(unsigned)chunks, kAdamThreads, 0, st>>>(b, h);
+    adamw_kernel<EIGHT><<<(unsigned)chunks, adam_threads(EIGHT), 0, st>>>(b, h);
     return hipGetLastError();
   };
   bool eight = false;
   for (int64_t i = 0; i < n; ++i) eight |= t[i].n > 0 && t[i].state == MOE_STATE_8BIT;
-  return eight ? for_batches<AdamBatch<true>>(t, n, kChunk, run) : for_batches<AdamBatch<false>>(t, n, kChunk, run);
+  return eight ? for_batches<AdamBatch<true>>(t, n, adam_chunk(true), run)
+               : for_batches<AdamBatch<false>>(t, n, adam_chunk(false), run);
 }
 
 size_t grad_norm_ws_bytes(const moe_tensor* t, int64_t n) { return (size_t)norm_chunks(t, n, norm_chunk(t, n)) * 8; }
