@@ -58,6 +58,35 @@ def test_adamw_and_norm_of_a_tensor_past_32_bits():
     assert torch.isfinite(p[-4096:].float()).all()
 
 
+def test_adamw_with_fp32_states_past_a_launch():
+    """A tensor that three launches share, between small ones: around the launches' borders and in the tail
+    the same bits as a small tensor of these values, and the tensors behind it have their own step."""
+    n, head = (1 << 31) + 3 * 256 + 9, 1001
+    print(f"[case] adamw fp32 states n={n}", flush=True)
+    sizes = [head, n, 0, 777]
+    ps = [fill(k, BF16, 10 + i, 0.1) for i, k in enumerate(sizes)]
+    gs = [fill(k, BF16, 20 + i, 1e-2) for i, k in enumerate(sizes)]
+    ms = [torch.zeros(k, device="cuda") for k in sizes]
+    vs = [torch.zeros(k, device="cuda") for k in sizes]
+    row = lambda p, g, m, v: moe.adamw_tensor(g, p, m, v, weight_decay=0.1)  # noqa: E731
+    first = (1 << 30) - 4 * 256   # the first launch holds `head` in 4 blocks of 256 values
+    spots = [(1, a) for a in (0, first - 512, (1 << 30) - 256, first + (1 << 30) - 512, 1 << 31, n - 9 - 256)]
+    spots += [(0, 0), (3, 0)]
+    size = 768
+    before = [(ps[i][a:a + size].clone(), gs[i][a:a + size].clone()) for i, a in spots]
+    hp = moe.adamw_hyper(1e-2, step=1)
+    moe.moe_adamw_step(hp, moe.adamw_tensors([row(*q) for q in zip(ps, gs, ms, vs)]))
+    torch.cuda.synchronize()
+    for (i, a), (p0, g0) in zip(spots, before):
+        k = p0.numel()
+        m0, v0 = torch.zeros(k, device="cuda"), torch.zeros(k, device="cuda")
+        moe.moe_adamw_step(hp, moe.adamw_tensors([row(p0, g0, m0, v0)]))
+        assert torch.equal(p0, ps[i][a:a + k]), (i, a)
+        assert torch.equal(m0, ms[i][a:a + k]) and torch.equal(v0, vs[i][a:a + k]), (i, a)
+    for a in range(0, n, 1 << 28):    # no value left out
+        assert int((vs[1][a:a + (1 << 28)] == 0).sum()) == int((gs[1][a:a + (1 << 28)] == 0).sum())
+
+
 @pytest.mark.parametrize("T,d", [(40_000_003, 8), (2_200_001, 1032)])
 def test_norm_rows_past_a_grid(T, d):
     """More rows than a grid's blocks, offsets past 32 bits: sampled rows, and the weight's gradient whole."""
