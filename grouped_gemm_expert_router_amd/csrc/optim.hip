@@ -19,7 +19,7 @@ namespace moe {
 
 namespace {
 
-// A block of the update: a wave takes 256 values.  fp32 states move 26 to 32 bytes a value in seven to nine
+// A block of the update: a wave takes 256 values.  fp32 states move 22 to 30 bytes a value in seven or eight
 // streams, and DRAM serves them best from few waves in small blocks: with one wave a block and three a SIMD,
 // 604M weights with master copies take 2.62 ms; four a SIMD 2.65, eight in blocks of four 3.02 (bf16
 // weights without master copies: 200M in 0.81 ms, 0.76, 0.84).  8-bit states are nearer the vector ALU's

@@ -166,6 +166,23 @@ def test_many_tensors_in_one_list():
             check(p)
 
 
+@pytest.mark.parametrize("n", [1, 54, 55, 64, 65, 129])
+@pytest.mark.parametrize("eight", [False, True])
+def test_lists_around_a_launch(n, eight):
+    """As many tensors as a launch holds and one more, without and with 8-bit states; the last one empty."""
+    print(f"[case] adamw list of {n}, 8-bit {eight}", flush=True)
+    rng = np.random.default_rng(40 + n)
+    kinds = [k for k in TYPES.values() if not k.get("eight")]
+    params = [Param(int(rng.integers(1, 1200)), rng, **kinds[i % len(kinds)]) for i in range(n)]
+    if eight:
+        params[n // 2] = Param(700, rng, eight=True)
+    params.append(Param(0, rng))
+    step(params)
+    for p in params[:-1]:
+        p.guards()
+        check(p)
+
+
 def test_repeated_steps_are_bitwise_reproducible():
     print("[case] adamw repeat", flush=True)
     out = []
