@@ -98,6 +98,15 @@ __device__ __forceinline__ int row_slot() {
   return LR >= 64 ? __builtin_amdgcn_readfirstlane(s) : s;
 }
 
+// First row of the block in a turn that starts at row `turn`.  Blocks go to the 8 XCDs one by one; in long
+// batches' full turns each XCD takes rows side by side (backward, 16384 rows of 2048 in bf16: 71 us, in the
+// blocks' order 73; 2048 rows: 16.2 and 15.3.  Forward both are the same within 1 %).
+__device__ __forceinline__ int64_t turn_row(int64_t turn, int64_t step, int64_t T, int rows) {
+  const unsigned b = blockIdx.x, n = gridDim.x;
+  const bool side = n % 8 == 0 && T >= 8 * step && turn + step <= T;
+  return turn + (int64_t)(side ? b % 8 * (n / 8) + b / 8 : b) * rows;
+}
+
 // Sums of K values over a row's LR lanes, the same in every lane.  sh: [K][LR / 64] of the row and of
 // this sum; the next sum takes another buffer, so that one barrier is enough (a wave that writes a
 // buffer again has passed the barrier of the sum between, which every wave reaches after its reads of
@@ -267,7 +276,7 @@ struct RowIn {
 // behind the block and a channel's gate: A = sum_t gt D yh gives dw_post = out_scale gate A and
 // dgate = out_scale w_post A.
 //
-// Bound by HBM, 21 vector operations a value: 16384 rows of 2048 in bf16: 69 us, 5.9 TB/s with the partial
+// Bound by HBM, 21 vector operations a value: 16384 rows of 2048 in bf16: 67 us, 6.1 TB/s with the partial
 // sums, and 5 for norm_reduce_kernel; 4099 of 7168 with an fp32 stream: 100 us, 5.3 TB/s (17 turns of
 // 256 blocks for 16.01 rows each).
 template <int LR, int NV, bool HF32, bool Y, bool P, bool FULL>
@@ -347,16 +356,19 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
   // a second row's values fit 128 registers beside the first's, but for the longest rows and a gate of its
   // own for each value beside the norm before a block (16384 x 2048: 93 us, with spills 139)
   constexpr bool kAhead = NV == 1 && !(FULL && P);
-  if (kAhead) fetch((int64_t)blockIdx.x * kRows + slot);
+  int64_t turn = 0, t0 = turn_row(0, step, p.T, kRows);
+  if (kAhead) fetch(t0 + slot);
   int first = 0;  // the first sum's buffer: with one sum a row, two rows in turn
-  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += step) {
+  while (t0 < p.T) {
     const int64_t t = t0 + slot;
     const bool on = t < p.T;
+    turn += step;
+    t0 = turn_row(turn, step, p.T, kRows);  // the next row
     const int64_t base = on ? t * p.d : 0;
     if (!Y) first ^= 1;
     if (!kAhead) fetch(t);
     const RowIn<NV, HF32, Y, P> in = cur;
-    if (kAhead && t0 + step < p.T) fetch(t + step);
+    if (kAhead && t0 < p.T) fetch(t0 + slot);
     constexpr int kS = (P ? 2 : 0) + (Y ? 1 : 0);
     float s[kS];  // (h'^2, h' w_pre dx), (y^2)
 #pragma unroll

@@ -247,3 +247,18 @@ def test_forward_many_rows(d):
         check_forward(c, h_out, x)
         same = forward(c, inplace=True)
         assert torch.equal(same[0], h_out) and torch.equal(same[1], x)
+
+
+@pytest.mark.parametrize("d,step", [(64, 32768), (520, 2048), (1536, 1024), (2048, 1024), (8192, 256), (8200, 256)])
+def test_backward_many_rows(d, step):
+    """Eight and more turns of 256 blocks, the last one ragged: every row once, in whatever order."""
+    for i, (T, h, gate) in enumerate([(8 * step + 5, BF16, "channel"), (9 * step - 1, F32, "token")]):
+        if T * d > 1 << 24:
+            T = 8 * step + 1 if i == 0 else 8 * step
+        print(f"[case] norm backward T={T} d={d} {h} {gate}", flush=True)
+        c = make(T, d, h, BF16, gate, seed=700 + d + i)
+        h_out, _ = forward(c)
+        o = backward(c, h_out)
+        check_backward(c, h_out, o)
+        same = backward(c, h_out, inplace=True)
+        assert all(torch.equal(o[n], same[n]) for n in o)
