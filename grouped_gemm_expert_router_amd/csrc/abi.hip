@@ -793,6 +793,7 @@ int moe_norm_backward(const moe_norm_desc* desc, const void* y, const void* h_ou
   if (rows && !y && (w_post || gate || dy || dw_post || dgate || desc->gate != MOE_GATE_NONE)) return MOE_ERR_SHAPE;
   if (rows && !w_pre && (h_out || dx || dw_pre)) return MOE_ERR_SHAPE;
   if (rows && w_pre && (!h_out || !dx)) return MOE_ERR_NULL;
+  if (rows && !y && !w_pre) return MOE_ERR_NULL;       // no part of the block to go back through
   if (rows && !w_pre && !dh_out) return MOE_ERR_NULL;  // no gradient comes in
   if (rows && !w_post && dw_post) return MOE_ERR_NULL;
   if (rows && (gate != nullptr) != (desc->gate != MOE_GATE_NONE)) return MOE_ERR_NULL;

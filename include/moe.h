@@ -292,8 +292,9 @@ int moe_norm_forward(const moe_norm_desc* desc, const void* y, const void* h, co
  *   dw_pre, dw_post [d], dgate (the gate's shape): summed over what the weight or gate is shared by
  * Any output may be NULL (not wanted).  dh may be dh_out itself; otherwise outputs overlap no input.
  * The sums over tokens are fp32 in a fixed order (bitwise reproducible).  h_out and dx go with w_pre: all three or
- * none (MOE_ERR_NULL; MOE_ERR_SHAPE if dx or h_out come without w_pre).  T = 0 writes zeros to
- * dw_pre, dw_post and a channel gate's dgate.  ws: moe_norm_workspace_bytes. */
+ * none (MOE_ERR_NULL; MOE_ERR_SHAPE if dx or h_out come without w_pre), and one of y and w_pre is
+ * needed (MOE_ERR_NULL).  T = 0 writes zeros to dw_pre, dw_post and a channel gate's dgate.
+ * ws: moe_norm_workspace_bytes. */
 int moe_norm_backward(const moe_norm_desc* desc, const void* y, const void* h_out, const void* w_post,
                       const void* gate, const void* w_pre, const void* dh_out, const void* dx, void* dh,
                       void* dy, void* dw_post, void* dgate, void* dw_pre, void* ws, size_t ws_bytes,
