@@ -1,7 +1,7 @@
 // Load-balancing loss of the gate: balance loss, z-loss, per-expert counts, and their gradient.
 //
 // With l = logits, a token counts if its mask is set, it lies in a group (a run of tokens: a
-// sequence, or the whole batch) and it has a logit above -inf:
+// sequence, or the whole batch) and it has a logit that is not -inf (a NaN counts):
 //   lse_t = log sum_e exp(l_te)        p_te = exp(l_te - lse_t)
 //   c_ge  = routed slots of g's counted tokens at expert e,   P_ge = sum of their p_te,   N_g
 //   balance = 1/G sum_{N_g > 0} E / (k N_g^2) sum_e c_ge P_ge      z = 1/N sum_t lse_t^2
@@ -215,6 +215,14 @@ __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
 #pragma unroll
           for (int i = 1; i < V * N; ++i) mx = fmaxf(mx, x[u][i]);
           mx = row16_max(mx);
+          if (mx == -INFINITY) {
+            // a maximum drops NaN beside -inf (another expert's, or behind the row): a token has no choice only
+            // if all its logits are -inf
+            bool other = false;
+#pragma unroll
+            for (int i = 0; i < V * N; ++i) other |= x[u][i] != -INFINITY;
+            if (__ballot(other) >> (tid & 48) & 0xffff) mx = NAN;
+          }
           if (mx != -INFINITY) {  // the same for the token's lanes
             float s = 0.0f;
 #pragma unroll

@@ -224,7 +224,7 @@ int moe_combine(const moe_dims* dims, const void* op, const int32_t* inv_perm, v
  * for the whole batch): group g holds tokens group_offsets[g] .. group_offsets[g+1]-1 (int32
  * [S+1], never decreasing, within [0, T]; NULL with S = 1: all T tokens); tokens before the first
  * or behind the last group belong to none.  A token counts if it lies in a group, its token_mask
- * byte is not 0 (uint8 [T]; NULL: every token) and it has a logit above -inf.  With
+ * byte is not 0 (uint8 [T]; NULL: every token) and it has a logit that is not -inf.  With
  * p = softmax(logits) over all E, over the counted tokens:
  *   counts[g, e] = slots of g's tokens with topk_ids = e,  P[g, e] = sum of p[t, e],  N_g = tokens
  *   losses[0] = 1/G sum_{g: N_g > 0} E / (k N_g^2) sum_e counts[g, e] P[g, e],  G = such groups
@@ -233,8 +233,8 @@ int moe_combine(const moe_dims* dims, const void* op, const int32_t* inv_perm, v
  * Outputs: counts int32 [S, E]; group_tokens int32 [S+2]: N_g, then N, then G; losses fp32 [2];
  * lse fp32 [T], -inf for a token that does not count.  Nothing is read of the logits and ids of a
  * token that is masked or lies in no group.  A logit of -inf is an expert that cannot be chosen (p = 0);
- * NaN or +inf in a counted token makes the losses NaN.  Sums run in a fixed order (bitwise
- * reproducible), across tokens in 64 bits.  dims: T, E and k are used.  S: 1 .. 65535
+ * a token with a NaN or +inf counts, whatever its other logits are, and makes its lse and the losses
+ * NaN.  Sums run in a fixed order (bitwise reproducible), across tokens in 64 bits.  dims: T, E and k are used.  S: 1 .. 65535
  * (MOE_ERR_SHAPE).  ws: moe_balance_workspace_bytes.  logits, topk_ids, counts and lse 16-byte
  * aligned, the other arrays to their type. */
 int moe_balance_workspace_bytes(const moe_dims* dims, int64_t S, size_t* out);

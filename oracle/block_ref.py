@@ -21,7 +21,8 @@ def _counted(logits, mask, offsets):
     for g, (a, z) in enumerate(zip(offsets[:-1], offsets[1:])):
         group[a:z] = g
     for t in range(T):
-        if (mask is not None and mask[t] == 0) or not np.any(logits[t] > -np.inf):
+        # a NaN is not -inf: its token counts
+        if (mask is not None and mask[t] == 0) or np.all(logits[t] == -np.inf):
             group[t] = -1
     return group
 
