@@ -40,8 +40,9 @@ def balance(logits, ids, mask=None, offsets=None):
     for t in np.flatnonzero(group >= 0):
         x = logits[t].astype(np.float64)
         top = x.max()
-        lse[t] = top + np.log(np.exp(x - top).sum())
-        p[t] = np.exp(x - lse[t])
+        e = np.exp(x - top)
+        lse[t] = top + np.log(e.sum())
+        p[t] = e / e.sum()
         g = group[t]
         n[g] += 1
         P[g] += p[t]
