@@ -140,25 +140,43 @@ def _stream(stream) -> Optional[int]:
     """A stream's handle; None is torch's current stream of the current device.  The handle is taken
     from torch directly: a torch.cuda.Stream object around it costs 2.8 us, most of a small call."""
     if stream is None:
-        raw, device = _torch_calls()
+        raw, device = _torch or _torch_calls()
         return raw(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
-def _here(fn: str, t) -> None:
-    """Refuses a tensor that is not on the current device: the kernels go to a stream of that one."""
-    if t is None or isinstance(t, int):
-        return
-    index = t.get_device()
-    if index < 0 or index != _torch_calls()[1]():
-        raise ValueError(f"{fn}: tensors on {t.device}, not on the current GPU")
-
-
 def _check(fn: str, rc: int) -> None:
     if rc != MOE_OK:
         raise MoEError(fn, rc, load_library().moe_status_string(rc).decode())
+
+
+def _elsewhere(fn: str, t):
+    raise ValueError(f"{fn}: tensors on {t.device}, not on the current GPU")
+
+
+def _device() -> Optional[int]:
+    """torch's current device, None without a GPU."""
+    if _torch is None:
+        import torch
+        if not torch.cuda.is_available():
+            return None
+    return _torch_calls()[1]()
+
+
+def _arguments(fn: str, stream, tensors: tuple) -> list:
+    """Addresses of a call's tensors (None and plain addresses stay) and the stream's handle.  Refuses a tensor
+    that is not on the current device: the kernels go to a stream of that one, and would fault on the host's
+    memory.  A small call's time is the host's, so no step here is more than that needs."""
+    here = _torch[1]() if _torch is not None else _device()
+    try:
+        a = [None if t is None else t.data_ptr() if t.get_device() == here else _elsewhere(fn, t) for t in tensors]
+    except AttributeError:   # a plain address among them
+        a = [t if t is None or isinstance(t, int) else t.data_ptr() if t.get_device() == here else _elsewhere(fn, t)
+             for t in tensors]
+    a.append(_stream(stream) if stream is not None or here is None else _torch[0](here))
+    return a
 
 
 def status_string(status: int) -> str:
@@ -262,19 +280,20 @@ def moe_balance_workspace_bytes(dm: MoeDims, S: int) -> int:
 
 def moe_balance_forward(dm, logits, topk_ids, token_mask, group_offsets, S, counts, group_tokens, losses, lse, ws,
                         ws_bytes=None, stream=None):
-    _here("moe_balance_forward", logits)
     nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
-    _check("moe_balance_forward", load_library().moe_balance_forward(
-        ctypes.byref(dm), _ptr(logits), _ptr(topk_ids), _ptr(token_mask), _ptr(group_offsets), S, _ptr(counts),
-        _ptr(group_tokens), _ptr(losses), _ptr(lse), _ptr(ws), nb, _stream(stream)))
+    a = _arguments("moe_balance_forward", stream, (logits, topk_ids, token_mask, group_offsets, counts, group_tokens,
+                                                   losses, lse, ws))
+    a.insert(4, S)
+    a.insert(-1, nb)
+    _check("moe_balance_forward", load_library().moe_balance_forward(dm, *a))
 
 
 def moe_balance_backward(dm, logits, lse, group_offsets, S, counts, group_tokens, d_losses, d_logits_in, d_logits,
                          stream=None):
-    _here("moe_balance_backward", logits)
-    _check("moe_balance_backward", load_library().moe_balance_backward(
-        ctypes.byref(dm), _ptr(logits), _ptr(lse), _ptr(group_offsets), S, _ptr(counts), _ptr(group_tokens),
-        _ptr(d_losses), _ptr(d_logits_in), _ptr(d_logits), _stream(stream)))
+    a = _arguments("moe_balance_backward", stream, (logits, lse, group_offsets, counts, group_tokens, d_losses,
+                                                    d_logits_in, d_logits))
+    a.insert(3, S)
+    _check("moe_balance_backward", load_library().moe_balance_backward(dm, *a))
 
 
 def norm_desc(T: int, d: int, h_dtype: int = MOE_BF16, w_dtype: int = MOE_BF16, gate: int = MOE_GATE_NONE,
@@ -289,19 +308,16 @@ def moe_norm_workspace_bytes(nd: MoeNormDesc) -> int:
 
 
 def moe_norm_forward(nd, y, h, w_post, gate, w_pre, h_out, x, stream=None):
-    _here("moe_norm_forward", h)
-    _check("moe_norm_forward", load_library().moe_norm_forward(
-        ctypes.byref(nd), _ptr(y), _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(h_out), _ptr(x),
-        _stream(stream)))
+    a = _arguments("moe_norm_forward", stream, (y, h, w_post, gate, w_pre, h_out, x))
+    _check("moe_norm_forward", load_library().moe_norm_forward(nd, *a))
 
 
 def moe_norm_backward(nd, y, h_out, w_post, gate, w_pre, dh_out, dx, dh, dy, dw_post, dgate, dw_pre, ws,
                       ws_bytes=None, stream=None):
-    _here("moe_norm_backward", h_out if h_out is not None else dh_out)
     nb = (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
-    _check("moe_norm_backward", load_library().moe_norm_backward(
-        ctypes.byref(nd), _ptr(y), _ptr(h_out), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(dh_out), _ptr(dx),
-        _ptr(dh), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), _ptr(ws), nb, _stream(stream)))
+    a = _arguments("moe_norm_backward", stream, (y, h_out, w_post, gate, w_pre, dh_out, dx, dh, dy, dw_post, dgate, dw_pre, ws))
+    a.insert(-1, nb)
+    _check("moe_norm_backward", load_library().moe_norm_backward(nd, *a))
 
 
 class TensorList:
@@ -365,16 +381,18 @@ def moe_grad_norm_workspace_bytes(tensors: TensorList) -> int:
 
 
 def moe_grad_norm(tensors: TensorList, max_norm, norm, scale, ws, ws_bytes=None, stream=None):
-    _here("moe_grad_norm", tensors.first)
     nb = (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
-    _check("moe_grad_norm", load_library().moe_grad_norm(tensors.array, len(tensors), max_norm, _ptr(norm),
-                                                         _ptr(scale), _ptr(ws), nb, _stream(stream)))
+    _, *a = _arguments("moe_grad_norm", stream, (tensors.first, norm, scale, ws))   # the list is on its first's device
+    a.insert(-1, nb)
+    _check("moe_grad_norm", load_library().moe_grad_norm(tensors.array, len(tensors), max_norm, *a))
 
 
 def moe_adamw_step(hyper: MoeAdamW, tensors: TensorList, stream=None):
-    _here("moe_adamw_step", tensors.first)
-    _check("moe_adamw_step", load_library().moe_adamw_step(ctypes.byref(hyper), tensors.array, len(tensors),
-                                                           _stream(stream)))
+    here = _device()
+    for t in (tensors.first, *getattr(hyper, "keep", ())):
+        if t is not None and not isinstance(t, int) and t.get_device() != here:
+            _elsewhere("moe_adamw_step", t)
+    _check("moe_adamw_step", load_library().moe_adamw_step(hyper, tensors.array, len(tensors), _stream(stream)))
 
 
 _hook_ref = None
