@@ -132,7 +132,10 @@ def _torch_calls():
     if _torch is None:
         import torch
         torch.cuda.current_device()  # sets up the runtime
-        _torch = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+        # not public: where they are missing, the public calls behind them
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        _torch = (raw or (lambda index: torch.cuda.current_stream(index).cuda_stream), device or torch.cuda.current_device)
     return _torch
 
 

@@ -118,3 +118,21 @@ def test_every_tensor_of_a_call_is_on_the_current_device(fn, monkeypatch):
     with pytest.raises(ValueError, match="not on the current GPU"):
         call(here)
     assert lib.calls == [fn]
+
+
+def test_stream_handles_come_from_the_public_call_where_there_is_no_raw_one(monkeypatch):
+    """torch's raw handle and device functions are not public: without them the same come from
+    torch.cuda's own calls."""
+    import torch
+
+    class Stream:
+        def __init__(self, device):
+            self.cuda_stream = 4096 + device
+
+    monkeypatch.setattr(moe, "_torch", None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(3 if device is None else device))
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    assert moe._stream(None) == 4099
+    assert moe._device() in (None, 3)   # None: no GPU here
