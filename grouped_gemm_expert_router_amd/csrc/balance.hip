@@ -21,9 +21,10 @@ constexpr int kBalRedThreads = 1024;
 
 // Tokens of a tile: at most 1024 tiles, whose partial sums few blocks add, until a tile has 512 tokens (its
 // fp32 sums stay short); then up to 65536 tiles.  Both directions of 131071 tokens, 256 experts in 37
-// groups: 512 tiles 119 us, 1024 tiles 113, 2048 tiles 116.  Short batches: one tile, and so one launch, up
-// to 128 tokens (100 x 128: 13.1 us, as two tiles 16.4); then tiles of 32 tokens up to 8192 (5000 x 119:
-// 17.5 us, tiles of 64 18.0), of 64 behind (16384 x 128: 20.8, of 128 22.0).
+// groups: with 512 tiles 5 % more, with 2048 tiles 3 %.  Short batches: one tile, and so one launch, up
+// to 128 tokens (100 x 128 as two tiles: 25 % more); then tiles of 32 tokens up to 8192 (5000 x 119 by 64:
+// 3 % more), of 64 behind (16384 x 128 by 128: 6 % more).  Measured at 119 to 256 experts; the number of
+// experts is not looked at.  What the kernels take by this rule stands at each of them.
 int balance_tile(int64_t T) {
   if (T <= 128) return 128;
   int64_t t = (T + 1023) / 1024;
@@ -67,8 +68,8 @@ BalWs bal_ws(int64_t T, int64_t E, int64_t S, char* ws) {
 }
 
 // Columns of 64 a block of the reduction takes: all of them while its 16 waves then read few rows each
-// (one block, and no launch for the losses, if there is one group), else one.  Both directions: 16384 x 128
-// (2 x 257 rows) by one block 19.2 us, by two 20.1; 8192 x 256 (4 x 257) by one 23.2, by four 21.0.
+// (one block, and no launch for the losses, if there is one group), else one.  16384 x 128 (2 x 257 rows):
+// by two blocks 0.9 us more; 8192 x 256 (4 x 257): by one block 2.2 us more.
 int balance_wide(int64_t T, int64_t E, int64_t S) {
   const int64_t rows = T > 0 ? (T + balance_tile(T) - 1) / balance_tile(T) / S + 1 : 1;
   int w = 1;
@@ -153,12 +154,13 @@ __device__ __forceinline__ void whole_losses(const float (&shP)[4][kCols], const
 // One block per tile of consecutive tokens, kL lanes per token, U tokens of a lane group in flight;
 // each lane keeps the sums of p of its own columns.  A tile is cut where a group ends; the piece of
 // tile b in group g has the slot b + g, which no other piece has (both grow along the tokens).  Where
-// tiles are few, a tile's pieces are shared by blocks (gridDim.y of them: 42 tokens of 385 in 43 groups,
-// both ways: 33 us, by one block 116).
-// 131071 x 256 in 37 groups: 31 us, 4.5 TB/s of logits and slots, bound by the loads that four waves a
-// SIMD keep in flight around each token's two dependent sums (a whole wave for each token, with shuffles
-// through LDS: 117 us; four tokens in flight: 2 % less in one group, 7 % more in 37).  16384 x 128: 6 us,
-// of which the memory needs 1.5.
+// tiles are few, a tile's pieces are shared by blocks (gridDim.y of them: 42 tokens of 385 in 43 groups
+// 6 us, by one block 83 us more).
+// 131071 x 256, in one group and in 37: 31 us, 4.5 TB/s of logits and slots, bound by the loads that four
+// waves a SIMD keep in flight around each token's two dependent sums (a whole wave for each token, with
+// shuffles through LDS: 86 us more; four tokens in flight: 2 % less in one group, 7 % more in 37).  More
+// experts leave three and two waves a SIMD and one token in flight: 65536 x 384 28 us, 65536 x 512 33,
+// 32768 x 1024 31 (3.6, 4.1 and 4.4 TB/s).  16384 x 128: 7 us, of which the memory needs 1.4.
 template <int V, int N>
 __global__ __launch_bounds__(kBalThreads) void balance_stats_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
@@ -402,7 +404,8 @@ __global__ __launch_bounds__(NT) void balance_final_kernel(const double* part, c
 
 // The gradient: kL lanes per token.  Since sum_e p = 1, an integer near their mean is taken off the
 // counts first, which loses nothing and keeps the difference from cancelling.  Bound by HBM: 131071 x 256
-// with another gradient added: 70 us, 5.7 TB/s; written past the caches (cached stores: 75 us).
+// in 37 groups with another gradient added: 69 us, 5.8 TB/s; written past the caches (cached stores: 5 us
+// more).  16384 x 128: 7 us.
 template <int V, int N>
 __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
     const float* __restrict__ logits, const float* __restrict__ lse_in, const int32_t* __restrict__ goff,
@@ -448,7 +451,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_grad_kernel(
         ca = n > 0 ? (float)((double)d_losses[0] * (double)E / ((double)k * n * (double)n * (double)tokens[S + 1])) : 0.0f;
       }
       // p = e / sum e: lse is rounded to its own size, and exp(l - lse) alone would be off by as much (of logits
-      // past 2^27 the log E is lost: by a factor of E).  One sum more: 16384 x 128 19.7 us, without it 19.5
+      // past 2^27 the log E is lost: by a factor of E).  One sum more: 16384 x 128 0.2 us
       float dot = 0.0f, sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < V * N; ++i) {
@@ -544,9 +547,8 @@ hipError_t launch_balance_backward(const float* logits, const float* lse, const 
                                    const int32_t* tokens, const float* d_losses, int T, int E, int k, int S,
                                    const float* d_in, float* d_out, hipStream_t st) {
   if (T == 0) return hipSuccess;
-  // tokens of a block (both directions, 128 experts: 2048 tokens by 16 11.5 us, by 32 12.0; 8192 by 32
-  // 15.3, by 16 16.3, by 64 17.6; 32768 by 64 25.8, by 32 27.4; 131071 x 256 by 64 107, by 32 111); a
-  // grid's threads fit 32 bits
+  // tokens of a block (128 experts: 2048 tokens by 32 0.5 us more; 8192 by 16 1.0 more, by 64 2.3; 32768 by
+  // 32 1.6 more; 131071 x 256 by 32 4 more); a grid's threads fit 32 bits
   const int tile = T <= 4096 ? 16 : T <= 12288 ? 32 : T <= (1 << 27) ? 64 : 1024;
   const unsigned tiles = (unsigned)((T + (int64_t)tile - 1) / tile);
 #define MOE_BAL_CALL(V, N)                                                                                       \

@@ -99,8 +99,8 @@ __device__ __forceinline__ int row_slot() {
 }
 
 // First row of the block in a turn that starts at row `turn`.  Blocks go to the 8 XCDs one by one; in long
-// batches' full turns each XCD takes rows side by side (backward, 16384 rows of 2048 in bf16: 71 us, in the
-// blocks' order 73; 2048 rows: 16.2 and 15.3.  Forward both are the same within 1 %).
+// batches' full turns each XCD takes rows side by side (backward, 16384 rows of 2048 in bf16: in the blocks'
+// order 2 us more; 2048 rows, where it is kept: 0.9 us less.  Forward both are the same within 1 %).
 __device__ __forceinline__ int64_t turn_row(int64_t turn, int64_t step, int64_t T, int rows) {
   const unsigned b = blockIdx.x, n = gridDim.x;
   const bool side = n % 8 == 0 && T >= 8 * step && turn + step <= T;
@@ -142,10 +142,11 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float* sh, int wave) {
 // A block walks rows a grid apart, each row's loads issued before the row before is worked on; a row
 // stays in registers between its passes, and so do the weights.  FEW: each block has its rows once, and
 // loads the weights where it needs them, so that 64 registers do and a compute unit holds 2048 threads
-// (rows of 2048 values: 1: 2.4 us, one block a unit 2.9; 512: 3.2 and 4.0; 2048: 6.3 and 7.3; 4096, where
-// the rows no longer fit: 14.5 and 13.9).  Bound by HBM: 16384 rows of 2048 in bf16, both norms: 45 us, 5.9 TB/s (a block for each row: 48;
-// cached loads and stores 51); 64527 rows of 520: 50 us (a block for two rows: 62); 3728 of 9000: 49 us
-// (without the loads ahead 55).
+// (rows of 2048 values, by one block a unit: 1 row 0.5 us more, 512 rows 0.8, 2048 rows 1.0; 4096 rows, which
+// no longer fit, 0.6 less).  One row: 2.4 us.  Bound by HBM: 16384 rows of 2048 in bf16, both norms: 45 us,
+// 5.9 TB/s (a block for each row 3 us more; cached loads and stores 6), with an fp32 stream 71 us, 5.7 TB/s;
+// 64527 rows of 520: 50 us (a block for two rows 12 more); 3728 of 9000: 49 us (without the loads ahead 6
+// more).
 template <int LR, int NV, bool HF32, bool FEW>
 __global__ __launch_bounds__(FEW ? norm_few_threads(LR) : norm_threads(LR), FEW && NV == 1 ? 8 : 1) void norm_forward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* h, const void* __restrict__ w_post,
@@ -277,8 +278,11 @@ struct RowIn {
 // dgate = out_scale w_post A.
 //
 // Bound by HBM, 21 vector operations a value: 16384 rows of 2048 in bf16: 67 us, 6.1 TB/s with the partial
-// sums, and 5 for norm_reduce_kernel; 4099 of 7168 with an fp32 stream: 100 us, 5.3 TB/s (17 turns of
-// 256 blocks for 16.01 rows each).
+// sums, and 5 for norm_reduce_kernel; 4099 of 7168 with an fp32 stream: 101 us, 5.3 TB/s (17 turns of
+// 256 blocks for 16.01 rows each).  Rows of more than 8192 values: a lane has 16, nothing is loaded ahead,
+// and with both norms 28 of its 128 registers are spilled (41 to 45 with a gate for each value): 2048 rows
+// of 16384 in bf16 127 us, 3.2 TB/s, 3728 of 9000 165 us; with one of the norms, which spills nothing, 54
+// and 57 us, 5.0 and 4.7 TB/s.
 template <int LR, int NV, bool HF32, bool Y, bool P, bool FULL>
 __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
     NormArgs p, const uint16_t* __restrict__ y, const void* __restrict__ h_out, const void* __restrict__ w_post,
@@ -288,7 +292,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
   __shared__ float sh[kRows][2][3 * W];
   const int slot = row_slot<LR>(), lane = threadIdx.x % LR, wave = lane >> 6;
   // the weights of a lane's columns: in registers, or for the longest rows in LDS (16 values a lane of each
-  // would spill: 2048 rows of 16384 took 170 us)
+  // would spill still more: 2048 rows of 16384 half as long again)
   constexpr bool kLds = NV > 1;
   __shared__ float4 w_lds[kLds ? 4 * NV * LR : 1];
   float a_pre[NV][8], a_post[NV][8], w_reg[NV][2][8];  // w_pre; out_scale gate w_post
@@ -354,7 +358,7 @@ __global__ __launch_bounds__(norm_threads(LR)) void norm_backward_kernel(
     }
   };
   // a second row's values fit 128 registers beside the first's, but for the longest rows and a gate of its
-  // own for each value beside the norm before a block (16384 x 2048: 93 us, with spills 139)
+  // own for each value beside the norm before a block (16384 x 2048: 95 us, loaded ahead and spilled 46 more)
   constexpr bool kAhead = NV == 1 && !(FULL && P);
   int64_t turn = 0, t0 = turn_row(0, step, p.T, kRows);
   if (kAhead) fetch(t0 + slot);
@@ -560,8 +564,8 @@ int norm_lanes(int d) {
   } while (0)
 
 // One block a compute unit, each with its rows' loads ahead.  Smaller blocks, more of them, write more
-// partial sums and read memory in smaller pieces (backward, 16384 rows of 2048 values: 2 blocks of one row
-// a unit 78.5 us, 4 of them 85, 1 block of two rows 75.2, of four rows 73.4).
+// partial sums and read memory in smaller pieces (backward, 16384 rows of 2048 values, beside one block of four
+// rows a unit: 2 blocks of one row 5 us more, 4 of them 12, 1 block of two rows 2).
 int norm_blocks(int64_t T, int d) {
   const int rows = norm_threads(norm_lanes(d)) / norm_lanes(d);
   const int64_t b = (T + rows - 1) / rows;

@@ -237,7 +237,9 @@ __device__ __forceinline__ void random4(const float (&w)[4], const uint32_t (&u)
 // One run a wave and no more (in blocks of four waves, as many as fit: 2.95 and 1.60 ms; 4 runs of a wave in
 // turn 3.08 and 1.72, two of them in flight together 3.02 and 1.66; cached stores 3.11 and 1.79).  The
 // step's number on the device costs a wave an expm1: 8-bit states 1.73 ms (by powers in 64 bits in every
-// lane: 2.15 to 2.39).
+// lane: 2.15 to 2.39).  200M weights without master copies: fp32 0.89 ms (6.3 TB/s) and with 8-bit states
+// 0.53 (6.1); bf16, rounded with random bits, 0.81 (5.4) and with 8-bit states 0.49 (4.1: nearer the vector
+// ALU's bound, two random words a value).
 template <bool P32, bool MASTER, bool G32, bool EIGHT>
 __device__ __forceinline__ void adamw_run(const AdamTensor& T, const Step& h, int64_t b, int lane) {
   const int64_t i = b + lane * 4;
@@ -393,7 +395,8 @@ namespace {
 
 // Sum of g^2 of one chunk, in 64 bits (no square of an fp32 value overflows or vanishes there).
 // Each thread has U loads of 16 bytes in flight; the values behind the last of them go one by one.
-// Bound by HBM: 604M bf16 values in 176 us, 6.9 TB/s (4 or 16 loads: 179, 185), and 4 us for the final sum.
+// Bound by HBM: 604M bf16 values in 176 us, 6.9 TB/s (4 or 16 loads: 179, 185), and 4 us for the final sum;
+// 300M fp32 values in 182 us.
 template <bool G32>
 __device__ __forceinline__ double square_sum(const void* g, int64_t a, int64_t z) {
   constexpr int V = G32 ? 4 : 8, U = 8;

@@ -234,9 +234,10 @@ int moe_combine(const moe_dims* dims, const void* op, const int32_t* inv_perm, v
  * lse fp32 [T], -inf for a token that does not count.  Nothing is read of the logits and ids of a
  * token that is masked or lies in no group.  A logit of -inf is an expert that cannot be chosen (p = 0);
  * a token with a NaN or +inf counts, whatever its other logits are, and makes its lse and the losses
- * NaN.  Sums run in a fixed order (bitwise reproducible), across tokens in 64 bits.  dims: T, E and k are used.  S: 1 .. 65535
- * (MOE_ERR_SHAPE).  ws: moe_balance_workspace_bytes.  logits, topk_ids, counts and lse 16-byte
- * aligned, the other arrays to their type. */
+ * NaN.  Sums run in a fixed order (bitwise reproducible): in fp32 over up to 512 tokens of a group that
+ * follow each other (T / 65536 where T is above 2^25), in 64 bits over those sums.  dims: T, E
+ * and k are used.  S: 1 .. 65535 (MOE_ERR_SHAPE).  ws: moe_balance_workspace_bytes.  logits, topk_ids,
+ * counts and lse 16-byte aligned, the other arrays to their type. */
 int moe_balance_workspace_bytes(const moe_dims* dims, int64_t S, size_t* out);
 int moe_balance_forward(const moe_dims* dims, const float* logits, const int32_t* topk_ids,
                         const uint8_t* token_mask, const int32_t* group_offsets, int64_t S, int32_t* counts,
@@ -248,7 +249,8 @@ int moe_balance_forward(const moe_dims* dims, const float* logits, const int32_t
  * d_logits, which may be d_logits_in itself (pass moe_backward's d_logits as both):
  *   d_logits = d_logits_in + p (d_losses[0] E / (k N_g^2 G) (counts[g, e] - sum_i counts[g, i] p_i)
  *                               + 2 d_losses[1] lse / N)
- * The counts carry no gradient.  Rows of tokens that do not count are those of d_logits_in.
+ * The counts carry no gradient.  Rows of tokens that do not count are those of d_logits_in (their logits are
+ * read and not used).  p is a row's exponentials over their sum, so it keeps its bits at any size of lse.
  * logits, topk routing and groups as in the forward call, with its lse, counts and group_tokens
  * (counts and group_tokens may have been summed over other GPUs' tokens in between, for the loss of
  * the joint batch: N_g, N and the counts summed, G the number of joint groups). */
@@ -341,9 +343,10 @@ int moe_grad_norm(const moe_tensor* tensors, int64_t n_tensors, float max_norm, 
  * becomes zero), and so is a bf16 parameter without a master copy if `stochastic` is 1 (to nearest
  * if 0); the random bits are a function of seed, step, the tensor's place in the list and the
  * value's index, so a step is bitwise reproducible.  A gradient that is not finite makes its weight
- * NaN and leaves nothing of the 8-bit states of its 256 values; the scale of moe_grad_norm skips such
- * a step.  lr and step may live on the device (d_lr, d_step) for a captured graph whose replays move
- * on; they are read when the step runs.  The tensors overlap nowhere. */
+ * NaN and leaves nothing of the 8-bit states of its 256 values (one whose square passes fp32's range
+ * leaves nothing of their sqrt(v)); the scale of moe_grad_norm skips such a step, or brings it into range.
+ * lr and step may live on the device (d_lr, d_step) for a captured graph whose replays move on; they are
+ * read when the step runs.  The tensors overlap nowhere. */
 typedef struct {
   double lr;              /* >= 0 and finite; unused with d_lr */
   double beta1, beta2;    /* in [0, 1) */
