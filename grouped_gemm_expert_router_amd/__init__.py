@@ -16,6 +16,9 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 MOE_BF16, MOE_FP8_E4M3, MOE_MXFP8, MOE_F32 = 0, 1, 2, 3
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
 MOE_STATE_F32, MOE_STATE_8BIT = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_BLOCK_ROWS, MOE_BLOCK_TOKENS, MOE_BLOCK_TILES = 0, 1, 2
+MOE_B_KN, MOE_B_NK, MOE_B_NK_ROWS = 0, 1, 2
 MOE_WS_ROUTE, MOE_WS_FORWARD, MOE_WS_BACKWARD, MOE_WS_ROUTER = 0, 1, 2, 3
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_WORKSPACE, MOE_ERR_HIP, MOE_ERR_ALIGN = 0, -1, -2, -3, -4, -5, -6
 
@@ -24,7 +27,9 @@ ENTRY_POINTS = ("moe_workspace_bytes", "moe_saved_bytes", "moe_route", "moe_rout
                 "moe_permute", "moe_combine", "moe_mxfp8_quantize", "moe_mxfp8_quantize_weights",
                 "moe_balance_workspace_bytes", "moe_balance_forward", "moe_balance_backward",
                 "moe_norm_workspace_bytes", "moe_norm_forward", "moe_norm_backward",
-                "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_adamw_step", "moe_set_stage_hook",
+                "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_adamw_step", "moe_score_workspace_bytes",
+                "moe_score_route", "moe_score_backward", "moe_bias_update", "moe_fp8_quantize",
+                "moe_fp8_matmul_workspace_bytes", "moe_fp8_matmul", "moe_set_stage_hook",
                 "moe_status_string")
 
 
@@ -53,6 +58,17 @@ class MoeAdamW(ctypes.Structure):
         ("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("stochastic", ctypes.c_int32),
         ("reserved", ctypes.c_int32), ("d_lr", ctypes.c_void_p), ("d_step", ctypes.c_void_p),
         ("d_grad_scale", ctypes.c_void_p)]
+
+
+class MoeScoreDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "E", "k")] + [
+        (n, ctypes.c_int32) for n in ("score", "renormalise", "groups", "group_topk", "group_best")] + [
+        ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class MoeMatmulDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("M", "N", "K", "lda", "ldb", "ldc")] + [
+        (n, ctypes.c_int32) for n in ("b_form", "c_dtype", "reserved")]
 
 
 # void hook(const char* stage, int begin, void* stream, void* user)
@@ -104,6 +120,14 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_grad_norm_workspace_bytes.argtypes = [tp, i64, szp]
     lib.moe_grad_norm.argtypes = [tp, i64, ctypes.c_float, vp, vp, vp, sz, vp]
     lib.moe_adamw_step.argtypes = [ap, tp, i64, vp]
+    sp, mp = ctypes.POINTER(MoeScoreDesc), ctypes.POINTER(MoeMatmulDesc)
+    lib.moe_score_workspace_bytes.argtypes = [sp, szp]
+    lib.moe_score_route.argtypes = [sp] + [vp] * 10 + [sz, vp]
+    lib.moe_score_backward.argtypes = [sp] + [vp] * 4 + [vp]
+    lib.moe_bias_update.argtypes = [i64, vp, ctypes.c_float, vp, vp, vp]
+    lib.moe_fp8_quantize.argtypes = [vp, ctypes.c_int32, i64, i64, i64, ctypes.c_int32, vp, vp, vp]
+    lib.moe_fp8_matmul_workspace_bytes.argtypes = [mp, szp]
+    lib.moe_fp8_matmul.argtypes = [mp] + [vp] * 7 + [sz, vp]
     lib.moe_set_stage_hook.argtypes = [STAGE_HOOK, vp]
     lib.moe_status_string.argtypes = [i32]
     lib.moe_status_string.restype = ctypes.c_char_p
@@ -398,6 +422,66 @@ def moe_adamw_step(hyper: MoeAdamW, tensors: TensorList, stream=None):
     _check("moe_adamw_step", load_library().moe_adamw_step(hyper, tensors.array, len(tensors), _stream(stream)))
 
 
+def score_desc(T: int, E: int, k: int, score: int = MOE_SCORE_SIGMOID, renormalise: bool = True, scale: float = 1.0,
+               groups: int = 1, group_topk: int = 1, group_best: int = 1) -> MoeScoreDesc:
+    return MoeScoreDesc(T, E, k, score, int(renormalise), groups, group_topk, group_best, scale, 0)
+
+
+def moe_score_workspace_bytes(sd: MoeScoreDesc) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_score_workspace_bytes", load_library().moe_score_workspace_bytes(ctypes.byref(sd), ctypes.byref(out)))
+    return out.value
+
+
+def moe_score_route(sd, logits, bias, token_mask, topk_ids, topk_w, counts, offsets, perm, inv_perm, ws, ws_bytes=None,
+                    stream=None):
+    nb = (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
+    a = _arguments("moe_score_route", stream, (logits, bias, token_mask, topk_ids, topk_w, counts, offsets, perm,
+                                               inv_perm, ws))
+    a.insert(-1, nb)
+    _check("moe_score_route", load_library().moe_score_route(sd, *a))
+
+
+def moe_score_backward(sd, logits, topk_ids, d_topk_w, d_logits, stream=None):
+    a = _arguments("moe_score_backward", stream, (logits, topk_ids, d_topk_w, d_logits))
+    _check("moe_score_backward", load_library().moe_score_backward(sd, *a))
+
+
+def moe_bias_update(counts, rate, bias, bias_out, E=None, stream=None):
+    a = _arguments("moe_bias_update", stream, (counts, bias, bias_out))
+    a.insert(1, rate)
+    _check("moe_bias_update", load_library().moe_bias_update(counts.numel() if E is None else E, *a))
+
+
+def moe_fp8_quantize(src, rows, cols, form, codes, scales, ld=None, src_dtype=None, stream=None):
+    """src_dtype: MOE_BF16 or MOE_F32, taken from src where it is None; ld: cols where it is None."""
+    if src_dtype is None:
+        src_dtype = {"torch.bfloat16": MOE_BF16, "torch.float32": MOE_F32}.get(str(src.dtype), -1)
+    src, codes, scales, st = _arguments("moe_fp8_quantize", stream, (src, codes, scales))
+    _check("moe_fp8_quantize", load_library().moe_fp8_quantize(src, src_dtype, rows, cols, cols if ld is None else ld,
+                                                               form, codes, scales, st))
+
+
+def matmul_desc(M: int, N: int, K: int, b_form: int = MOE_B_KN, c_dtype: int = MOE_BF16, lda: Optional[int] = None,
+                ldb: Optional[int] = None, ldc: Optional[int] = None) -> MoeMatmulDesc:
+    return MoeMatmulDesc(M, N, K, K if lda is None else lda, (N if b_form == MOE_B_KN else K) if ldb is None else ldb,
+                         N if ldc is None else ldc, b_form, c_dtype, 0)
+
+
+def moe_fp8_matmul_workspace_bytes(md: MoeMatmulDesc) -> int:
+    out = ctypes.c_size_t(0)
+    _check("moe_fp8_matmul_workspace_bytes",
+           load_library().moe_fp8_matmul_workspace_bytes(ctypes.byref(md), ctypes.byref(out)))
+    return out.value
+
+
+def moe_fp8_matmul(md, A, A_scale, B, B_scale, C_in, C, ws, ws_bytes=None, stream=None):
+    nb = (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
+    a = _arguments("moe_fp8_matmul", stream, (A, A_scale, B, B_scale, C_in, C, ws))
+    a.insert(-1, nb)
+    _check("moe_fp8_matmul", load_library().moe_fp8_matmul(md, *a))
+
+
 _hook_ref = None
 
 
@@ -459,6 +543,10 @@ __all__ = ["MoeDims", "MoEError", "dims", "load_library", "status_string", "moe_
            "adamw_tensor", "adamw_tensors", "adamw_hyper", "moe_grad_norm_workspace_bytes", "moe_grad_norm",
            "moe_adamw_step", "MOE_F32", "MOE_GATE_NONE", "MOE_GATE_CHANNEL", "MOE_GATE_TOKEN", "MOE_GATE_FULL",
            "MOE_STATE_F32", "MOE_STATE_8BIT",
+           "MoeScoreDesc", "score_desc", "moe_score_workspace_bytes", "moe_score_route", "moe_score_backward",
+           "moe_bias_update", "moe_fp8_quantize", "MoeMatmulDesc", "matmul_desc", "moe_fp8_matmul_workspace_bytes",
+           "moe_fp8_matmul", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_BLOCK_ROWS", "MOE_BLOCK_TOKENS",
+           "MOE_BLOCK_TILES", "MOE_B_KN", "MOE_B_NK", "MOE_B_NK_ROWS",
            "ENTRY_POINTS", "MOE_BF16",
            "MOE_FP8_E4M3", "MOE_MXFP8", "MOE_WS_ROUTE", "MOE_WS_FORWARD",
            "MOE_WS_BACKWARD", "MOE_WS_ROUTER", "MOE_OK", "MOE_ERR_NULL", "MOE_ERR_SHAPE", "MOE_ERR_DTYPE", "MOE_ERR_WORKSPACE",

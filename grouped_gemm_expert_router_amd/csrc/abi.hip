@@ -889,6 +889,158 @@ int moe_adamw_step(const moe_adamw* hyper, const moe_tensor* tensors, int64_t n_
   return MOE_OK;
 }
 
+static int check_score(const moe_score_desc* d) {
+  if (!d) return MOE_ERR_NULL;
+  if (d->reserved != 0) return MOE_ERR_SHAPE;
+  if (d->T < 0 || d->T >= ((int64_t)1 << 31) || d->E < 1 || d->E > 1024 || d->k < 1 || d->k > d->E || d->k > 64)
+    return MOE_ERR_SHAPE;
+  if (d->T * d->k >= ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
+  if (d->score != MOE_SCORE_SOFTMAX && d->score != MOE_SCORE_SIGMOID) return MOE_ERR_SHAPE;
+  if ((d->renormalise != 0 && d->renormalise != 1) || !isfinite(d->scale)) return MOE_ERR_SHAPE;
+  if (d->groups < 1 || d->groups > 64 || d->E % d->groups) return MOE_ERR_SHAPE;
+  if (d->group_topk < 1 || d->group_topk > d->groups || d->group_best < 1 || d->group_best > 2) return MOE_ERR_SHAPE;
+  return d->k > d->group_topk * (d->E / d->groups) ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+static ScoreArgs score_args(const moe_score_desc* d) {
+  ScoreArgs p;
+  p.T = (int)d->T;
+  p.E = (int)d->E;
+  p.k = (int)d->k;
+  p.groups = d->groups;
+  p.group_topk = d->group_topk;
+  p.group_best = d->group_best;
+  p.sigmoid = d->score == MOE_SCORE_SIGMOID;
+  p.renorm = d->renormalise != 0;
+  p.scale = d->scale;
+  return p;
+}
+
+int moe_score_workspace_bytes(const moe_score_desc* desc, size_t* out) {
+  const int rc = check_score(desc);
+  if (rc) return rc;
+  if (!out) return MOE_ERR_NULL;
+  *out = al256(score_ws_bytes(desc->T, desc->E, desc->k));
+  return MOE_OK;
+}
+
+int moe_score_route(const moe_score_desc* desc, const float* logits, const float* bias, const uint8_t* token_mask,
+                    int32_t* topk_ids, float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm,
+                    int32_t* inv_perm, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_score(desc);
+  if (rc) return rc;
+  const size_t need = al256(score_ws_bytes(desc->T, desc->E, desc->k));
+  if (!counts || !offsets) return MOE_ERR_NULL;
+  if (desc->T > 0 && (!logits || !topk_ids || !topk_w || !perm || !inv_perm)) return MOE_ERR_NULL;
+  if (need > 0 && !ws) return MOE_ERR_NULL;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (!al16(logits) || !al4(bias) || !al4(topk_ids) || !al4(topk_w) || !al4(counts) || !al4(offsets) || !al4(perm) ||
+      !al4(inv_perm) || !al256p(ws))
+    return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("score_route", launch_score_route(score_args(desc), logits, bias, token_mask, topk_ids, topk_w, counts,
+                                            offsets, perm, inv_perm, ws, st));
+  return MOE_OK;
+}
+
+int moe_score_backward(const moe_score_desc* desc, const float* logits, const int32_t* topk_ids,
+                       const float* d_topk_w, float* d_logits, void* stream) {
+  const int rc = check_score(desc);
+  if (rc) return rc;
+  if (desc->T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !d_topk_w || !d_logits) return MOE_ERR_NULL;
+  if (!al16(logits) || !al16(d_logits) || !al4(topk_ids) || !al4(d_topk_w)) return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("score_bwd", launch_score_backward(score_args(desc), logits, topk_ids, d_topk_w, d_logits, st));
+  return MOE_OK;
+}
+
+int moe_bias_update(int64_t E, const int32_t* counts, float rate, const float* bias, float* bias_out, void* stream) {
+  if (E < 1 || E > 1024 || !isfinite(rate)) return MOE_ERR_SHAPE;
+  if (!counts || !bias || !bias_out) return MOE_ERR_NULL;
+  if (!al4(counts) || !al4(bias) || !al4(bias_out)) return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("bias_update", launch_bias_update((int)E, counts, rate, bias, bias_out, st));
+  return MOE_OK;
+}
+
+constexpr int64_t kDenseSide = (int64_t)1 << 24;  // largest rows or columns of a blockwise operand
+constexpr int64_t kDenseLd = (int64_t)1 << 31;
+
+int moe_fp8_quantize(const void* src, int32_t src_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t form,
+                     void* codes, float* scales, void* stream) {
+  if (!is_elem(src_dtype)) return MOE_ERR_DTYPE;
+  if (form < MOE_BLOCK_ROWS || form > MOE_BLOCK_TILES) return MOE_ERR_SHAPE;
+  if (rows < 0 || rows > kDenseSide || cols < 16 || cols > kDenseSide || cols % 16) return MOE_ERR_SHAPE;
+  // a launch holds at most 2^32 threads, each of 8 values or more
+  if (rows * cols >= ((int64_t)1 << 34) || ld < cols || ld > kDenseLd || ld % 8) return MOE_ERR_SHAPE;
+  if (rows == 0) return MOE_OK;
+  if (!src || !codes || !scales) return MOE_ERR_NULL;
+  if (!al16(src) || !al16(codes) || !al4(scales)) return MOE_ERR_ALIGN;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("fp8_quantize", launch_fp8_quantize(src, src_dtype == MOE_F32, rows, cols, ld, form, (uint8_t*)codes,
+                                              scales, st));
+  return MOE_OK;
+}
+
+static int check_matmul(const moe_matmul_desc* d) {
+  if (!d) return MOE_ERR_NULL;
+  if (d->reserved != 0) return MOE_ERR_SHAPE;
+  if (d->c_dtype != MOE_BF16 && d->c_dtype != MOE_F32) return MOE_ERR_DTYPE;
+  if (d->b_form < MOE_B_KN || d->b_form > MOE_B_NK_ROWS) return MOE_ERR_SHAPE;
+  if (d->M < 0 || d->M > ((int64_t)1 << 30)) return MOE_ERR_SHAPE;
+  if (d->N < 16 || d->N % 16 || d->N > kDenseSide || d->K < 16 || d->K % 16 || d->K > kDenseSide) return MOE_ERR_SHAPE;
+  if (d->M * d->N >= ((int64_t)1 << 36)) return MOE_ERR_SHAPE;  // a launch holds at most 2^32 threads
+  if (d->lda < d->K || d->lda % 16 || d->lda > kDenseLd) return MOE_ERR_SHAPE;
+  if (d->ldb < (d->b_form == MOE_B_KN ? d->N : d->K) || d->ldb % 16 || d->ldb > kDenseLd) return MOE_ERR_SHAPE;
+  if (d->ldc < d->N || d->ldc % 8 || d->ldc > kDenseLd) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+static MatmulArgs matmul_args(const moe_matmul_desc* d) {
+  MatmulArgs g{};
+  g.M = d->M;
+  g.N = d->N;
+  g.K = d->K;
+  g.lda = d->lda;
+  g.ldb = d->ldb;
+  g.ldc = d->ldc;
+  g.b_form = d->b_form;
+  g.c_f32 = d->c_dtype == MOE_F32;
+  return g;
+}
+
+int moe_fp8_matmul_workspace_bytes(const moe_matmul_desc* desc, size_t* out) {
+  const int rc = check_matmul(desc);
+  if (rc) return rc;
+  if (!out) return MOE_ERR_NULL;
+  *out = al256(fp8_matmul_ws_bytes(matmul_args(desc)));
+  return MOE_OK;
+}
+
+int moe_fp8_matmul(const moe_matmul_desc* desc, const void* A, const float* A_scale, const void* B,
+                   const float* B_scale, const void* C_in, void* C, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_matmul(desc);
+  if (rc) return rc;
+  if (desc->M == 0) return MOE_OK;
+  if (!A || !A_scale || !B || !B_scale || !C) return MOE_ERR_NULL;
+  MatmulArgs g = matmul_args(desc);
+  const size_t need = al256(fp8_matmul_ws_bytes(g));
+  if (need > 0 && !ws) return MOE_ERR_NULL;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (!al16(A) || !al16(B) || !al16(C) || !al16(C_in) || !al4(A_scale) || !al4(B_scale) || !al256p(ws))
+    return MOE_ERR_ALIGN;
+  g.A = (const uint8_t*)A;
+  g.A_scale = A_scale;
+  g.B = (const uint8_t*)B;
+  g.B_scale = B_scale;
+  g.C_in = C_in;
+  g.C = C;
+  hipStream_t st = (hipStream_t)stream;
+  MOE_TRY("fp8_matmul", launch_fp8_matmul(g, ws, st));
+  return MOE_OK;
+}
+
 int moe_set_stage_hook(moe_stage_hook hook, void* user) {
   g_hook = hook;
   g_hook_user = user;

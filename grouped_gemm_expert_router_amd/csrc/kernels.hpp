@@ -208,4 +208,36 @@ size_t grad_norm_ws_bytes(const moe_tensor* t, int64_t n);
 hipError_t launch_grad_norm(const moe_tensor* t, int64_t n, float max_norm, float* norm, float* scale, double* part,
                             hipStream_t st);
 
+// routing by scores (sigmoid or softmax, balance bias, groups), its gradient and the bias's step
+struct ScoreArgs {
+  int T, E, k;
+  int groups, group_topk, group_best;
+  bool sigmoid, renorm;
+  float scale;
+};
+hipError_t launch_score_route(const ScoreArgs& p, const float* logits, const float* bias, const uint8_t* mask,
+                              int32_t* ids, float* w, int32_t* counts, int32_t* offsets, int32_t* perm,
+                              int32_t* inv_perm, void* ws, hipStream_t st);
+size_t score_ws_bytes(int64_t T, int64_t E, int64_t k);
+hipError_t launch_score_backward(const ScoreArgs& p, const float* logits, const int32_t* ids, const float* d_w,
+                                 float* d_logits, hipStream_t st);
+hipError_t launch_bias_update(int E, const int32_t* counts, float rate, const float* bias, float* out, hipStream_t st);
+
+// blockwise e4m3: quantiser (form: moe_block_form) and dense product (b_form: moe_b_form)
+hipError_t launch_fp8_quantize(const void* src, bool f32, int64_t rows, int64_t cols, int64_t ld, int form,
+                               uint8_t* codes, float* scales, hipStream_t st);
+struct MatmulArgs {
+  int64_t M, N, K, lda, ldb, ldc;
+  int b_form;
+  bool c_f32;
+  const uint8_t* A;
+  const float* A_scale;
+  const uint8_t* B;
+  const float* B_scale;
+  const void* C_in;
+  void* C;
+};
+size_t fp8_matmul_ws_bytes(const MatmulArgs& g);
+hipError_t launch_fp8_matmul(const MatmulArgs& g, void* ws, hipStream_t st);
+
 }  // namespace moe

@@ -44,8 +44,8 @@
  *   - Shapes (MOE_ERR_SHAPE otherwise): T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 64),
  *     d and f positive multiples of 128 (MOE_FP8_E4M3, MOE_MXFP8: of 256) and at most 65536,
  *     T*k < 2^31 (MOE_MXFP8: T*k + 127*E rounded up to 128 < 2^31).
- *     moe_norm_*, moe_grad_norm and moe_adamw_step take sizes of their own (see there); MOE_F32 is an
- *     element type of theirs and no dtype of the layer.
+ *     moe_norm_*, moe_grad_norm, moe_adamw_step, moe_score_*, moe_bias_update and moe_fp8_* take sizes of
+ *     their own (see there); MOE_F32 is an element type of theirs and no dtype of the layer.
  *   - fp8 (MOE_FP8_E4M3): codes are OCP e4m3 (bias 7, max 448, no infinities); a block's value
  *     is code * scale with its fp32 scale ([Prime] "Mit csinált a Prime Intellect?": blockwise
  *     FP8 is one of the kernel's data types).  Outputs and gradients stay bf16/fp32.
@@ -361,6 +361,105 @@ typedef struct {
 } moe_adamw;
 
 int moe_adamw_step(const moe_adamw* hyper, const moe_tensor* tensors, int64_t n_tensors, void* stream);
+
+/* Routing by scores, plus the expert plan: the gate's choice where moe_route's softmax over the k
+ * largest logits is not what a model was trained with ([JAX] "A dropless MoE minden tokent feldolgoz": a
+ * learned router scores the experts and keeps the top K).  With l a token's logits (fp32 [T, E]):
+ *   s = softmax(l) over all E, or sigmoid(l) of each         c = s + bias (fp32 [E]; NULL: zeros)
+ *   the E experts lie in `groups` groups of E / groups neighbours; a group's value is the sum of its
+ *   group_best (1 or 2) largest c; the group_topk groups of the largest value stay
+ *   ids = the k largest c among the experts that stay, descending
+ *   w_j = scale * s[ids_j] / sum_i s[ids_i] (renormalise = 1), or scale * s[ids_j]
+ * The bias moves the choice alone, never a weight.  Equal values go to the lower id (group, expert).  The
+ * choice is the one that c in 64 bits gives; weights are rounded once from more than their 32 bits.
+ * An expert whose logit or bias is -inf cannot be chosen: where fewer than k can, the slots behind them
+ * have id -1 and weight 0 (a group in which none can be chosen never stays, and one with a single such
+ * expert has its c for a value).  A token whose token_mask byte is 0 (uint8 [T]; NULL: none) has ids -1
+ * and weights 0; its logits are not read.  A token with a NaN among its logits or the bias, or a +inf
+ * logit where the score is a softmax, has ids -1 and weights NaN.
+ * counts, offsets, perm and inv_perm as moe_plan writes them; ws: moe_score_workspace_bytes.  T, E, k as
+ * for moe_route; 1 <= groups <= 64 divides E, 1 <= group_topk <= groups, k <= group_topk * E / groups.
+ * logits 16-byte aligned, the other arrays to their type. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  int64_t T, E, k;
+  int32_t score;        /* moe_score */
+  int32_t renormalise;  /* 0 or 1 */
+  int32_t groups, group_topk, group_best;
+  float scale;          /* finite */
+  int32_t reserved;     /* must be 0 */
+} moe_score_desc;
+
+int moe_score_workspace_bytes(const moe_score_desc* desc, size_t* out);
+int moe_score_route(const moe_score_desc* desc, const float* logits, const float* bias, const uint8_t* token_mask,
+                    int32_t* topk_ids, float* topk_w, int32_t* counts, int32_t* offsets, int32_t* perm,
+                    int32_t* inv_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_score_route's weights: d_logits (fp32 [T, E], written whole) for d_topk_w (fp32 [T, k],
+ * moe_backward's; call that one with d_logits NULL).  The choice carries no gradient.  With g = scale *
+ * d_topk_w over the slots whose id is in [0, E), S their scores' sum and q = s / S:
+ *   sigmoid              d_logits[ids_j] = g_j s_j (1 - s_j), and 0 elsewhere
+ *   sigmoid, renormalise d_logits[ids_j] = (g_j - sum_i g_i q_i) q_j (1 - s_j), and 0 elsewhere
+ *   softmax, renormalise d_logits[ids_j] = (g_j - sum_i g_i q_i) q_j, and 0 elsewhere
+ *   softmax              d_logits[e] = s_e (sum_{j: ids_j = e} g_j - sum_i g_i s[ids_i]) for every e
+ * A token without such a slot has a row of zeros; its logits are not read.  desc: T, E, k, score,
+ * renormalise and scale are used (the others checked).  logits and d_logits 16-byte aligned, the other
+ * arrays to their type; d_logits overlaps no input. */
+int moe_score_backward(const moe_score_desc* desc, const float* logits, const int32_t* topk_ids,
+                       const float* d_topk_w, float* d_logits, void* stream);
+
+/* The bias moved against uneven loads ([JAX] "Az egyenetlen terhelés lassítja a tanítást" [uneven load
+ * slows training]): bias_out[e] = bias[e] + rate * sign(mean(counts) - counts[e]), the sign from whole
+ * numbers.  counts int32 [E] as moe_score_route writes them (they may have been summed over GPUs);
+ * bias_out may be bias.  1 <= E <= 1024, rate finite.  Arrays aligned to their type. */
+int moe_bias_update(int64_t E, const int32_t* counts, float rate, const float* bias, float* bias_out, void* stream);
+
+/* Blockwise e4m3 quantisation, the layer's fp8 format (MOE_FP8_E4M3) on its own.  src: [rows, cols] of
+ * src_dtype (MOE_BF16 or MOE_F32), `ld` values from one row to the next.  With m = max(largest magnitude
+ * of a block, 448 * 2^-126): scale = m / 448 and code = e4m3(value * (448 / m)), to nearest even; a block of
+ * zeros has the scale 1.  A NaN gets the code of NaN; an infinity makes its block's scale infinite.
+ *   MOE_BLOCK_ROWS    128 values of a row (moe_forward's x):  codes [rows, cols], scales [rows, ceil(cols/128)]
+ *   MOE_BLOCK_TOKENS  128 rows of a column, transposed: codes [cols, R16] with R16 = rows rounded up to 16
+ *                     (codes behind the last row are 0), scales [cols, ceil(rows/128)]: an operand of a
+ *                     product over the rows, such as a weight gradient's
+ *   MOE_BLOCK_TILES   128 x 128 (weights):  codes [rows, cols], scales [ceil(rows/128), ceil(cols/128)]
+ * The last block of a row, column or matrix is a partial one.  rows >= 0, cols a positive multiple of 16,
+ * both at most 2^24, rows * cols < 2^34; cols <= ld <= 2^31, ld a multiple of 8.  src and codes 16-byte aligned. */
+typedef enum { MOE_BLOCK_ROWS = 0, MOE_BLOCK_TOKENS = 1, MOE_BLOCK_TILES = 2 } moe_block_form;
+
+int moe_fp8_quantize(const void* src, int32_t src_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t form,
+                     void* codes, float* scales, void* stream);
+
+/* Matrix product of blockwise e4m3 operands: C[M, N] = A . B (+ C_in), with A [M, K] codes and A_scale fp32
+ * [M, ceil(K/128)] (MOE_BLOCK_ROWS), and B by b_form:
+ *   MOE_B_KN       B [K, N], B_scale [ceil(K/128), ceil(N/128)]   a weight as the layer stores it: x . W
+ *   MOE_B_NK       B [N, K], B_scale [ceil(N/128), ceil(K/128)]   the same weight's rows: dy . W^T, or a weight
+ *                                                                 that is stored [out, in]
+ *   MOE_B_NK_ROWS  B [N, K], B_scale [N, ceil(K/128)]             two quantised activations: with both as
+ *                                                                 MOE_BLOCK_TOKENS writes them, x^T . dy
+ * Products of codes are summed over each block of 128 along K, each block's sum times its two scales is
+ * added in fp32, then C_in (c_dtype, C's layout; NULL: none; may be C itself), and C (bf16 or
+ * fp32) is rounded once.  For an fp32 C the block's sums are fp32; for a bf16 C they come from the fp8 matrix
+ * instruction, which drops what lies more than 13 bits below the largest of eight products (along K) before it
+ * adds them: 1.5e-5 of the result's norm on normal data.  Sums run in a fixed order (bitwise reproducible).  lda, ldb, ldc: codes or
+ * values from one row to the next; what lies between two rows is not touched.
+ * M of any size, 0 .. 2^30; N and K positive multiples of 16 up to 2^24, M * N < 2^36; lda, ldb
+ * multiples of 16, ldc of 8, at least the row's length and at most 2^31.  ws:
+ * moe_fp8_matmul_workspace_bytes (256-byte aligned; may be NULL where that is 0).  A, B, C and C_in 16-byte aligned. */
+typedef enum { MOE_B_KN = 0, MOE_B_NK = 1, MOE_B_NK_ROWS = 2 } moe_b_form;
+
+typedef struct {
+  int64_t M, N, K;
+  int64_t lda, ldb, ldc;
+  int32_t b_form;   /* moe_b_form */
+  int32_t c_dtype;  /* MOE_BF16 or MOE_F32 */
+  int32_t reserved; /* must be 0 */
+} moe_matmul_desc;
+
+int moe_fp8_matmul_workspace_bytes(const moe_matmul_desc* desc, size_t* out);
+int moe_fp8_matmul(const moe_matmul_desc* desc, const void* A, const float* A_scale, const void* B,
+                   const float* B_scale, const void* C_in, void* C, void* ws, size_t ws_bytes, void* stream);
 
 /* Optional profiling hook (process-wide; none by default).  When set, each call invokes
  * hook(stage, 1, stream, user) on the calling thread right before it enqueues a stage's kernel
