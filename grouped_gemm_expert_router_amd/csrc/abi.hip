@@ -966,6 +966,7 @@ int moe_bias_update(int64_t E, const int32_t* counts, float rate, const float* b
 
 constexpr int64_t kDenseSide = (int64_t)1 << 24;  // largest rows or columns of a blockwise operand
 constexpr int64_t kDenseLd = (int64_t)1 << 31;
+constexpr int64_t kCodeLd = (int64_t)1 << 28;  // eight rows of a product's operand within 32-bit offsets
 
 int moe_fp8_quantize(const void* src, int32_t src_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t form,
                      void* codes, float* scales, void* stream) {
@@ -991,8 +992,8 @@ static int check_matmul(const moe_matmul_desc* d) {
   if (d->M < 0 || d->M > ((int64_t)1 << 30)) return MOE_ERR_SHAPE;
   if (d->N < 16 || d->N % 16 || d->N > kDenseSide || d->K < 16 || d->K % 16 || d->K > kDenseSide) return MOE_ERR_SHAPE;
   if (d->M * d->N >= ((int64_t)1 << 36)) return MOE_ERR_SHAPE;  // a launch holds at most 2^32 threads
-  if (d->lda < d->K || d->lda % 16 || d->lda > kDenseLd) return MOE_ERR_SHAPE;
-  if (d->ldb < (d->b_form == MOE_B_KN ? d->N : d->K) || d->ldb % 16 || d->ldb > kDenseLd) return MOE_ERR_SHAPE;
+  if (d->lda < d->K || d->lda % 16 || d->lda > kCodeLd) return MOE_ERR_SHAPE;
+  if (d->ldb < (d->b_form == MOE_B_KN ? d->N : d->K) || d->ldb % 16 || d->ldb > kCodeLd) return MOE_ERR_SHAPE;
   if (d->ldc < d->N || d->ldc % 8 || d->ldc > kDenseLd) return MOE_ERR_SHAPE;
   return MOE_OK;
 }

@@ -3,6 +3,8 @@
 // one per 128 x 128 block or one per row and 128 values.  Blockwise FP8 is one of the data types of the
 // fused MoE backward on the Prime Mega MoE page ("Prime Mega MoE: tanításra is jó a DeepSeek MoE
 // kernele", section "Mit csinált a Prime Intellect?").
+#include <type_traits>
+
 #include "common.hpp"
 #include "gemm_common.hpp"
 #include "kernels.hpp"
@@ -278,14 +280,36 @@ __global__ __launch_bounds__(256) void fp8_matmul_sum_kernel(const MatmulArgs g,
 // What a tile kernel reads in the place of codes past K.
 __device__ const uint4 g_zero = {0, 0, 0, 0};
 
-// BM x BN tiles, WM x WN waves, a block of K (128 deep) a step through S LDS stages.  Operands and scales
-// reach LDS by DMA; the number of DMAs a wave issues in a step is fixed, so that the wait for a stage
-// counts those of the stages behind it.
+// LDS DMA of 16 or 4 bytes a lane from a wave's base address and a lane's 32-bit offset.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds_byte_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds_byte_addr)
+               : "memory");
+}
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds_byte_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds_byte_addr)
+               : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ const T* uniform_ptr(const T* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const T*)((uint64_t)lo | (uint64_t)hi << 32);
+}
+
+// BM x BN tiles, WM x WN waves, a block of K (128 deep) a step through S LDS stages, all by DMA.
+//
+// A step's DMAs go out one by one between the matrix instructions: issued together at the step's start
+// they held every wave up for a third of the step (21804x4096x7168 790 us).
 //
 // Scales.  A row's scales lie along K, so the 4 bytes a step needs of a row come with a cache line of
-// their own.  Scales are therefore fetched for eight blocks of K at a time, during the eight steps before
-// they are used: in step t each wave brings, for one block of K of the next eight, the scales of 32 rows; the
-// waves of a step share the rows, and with them the lines.  The scale of a B tile rides in the lanes behind.
+// their own.  They are therefore fetched for eight blocks of K at a time, in the steps before they are
+// used: one DMA brings one block's scales of 64 rows, and the waves of a step take the same rows for
+// different blocks, and with them the same lines.
 //
 // Each 32 x 32 block of C is held transposed (B is the MFMA's first operand): lane l has row l % 32 and 16
 // columns, so one A scale serves its 16 values.
@@ -295,83 +319,104 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void fp8_matmul_tile_kernel(const 
   constexpr bool KN = FORM == MOE_B_KN, ROWS = FORM == MOE_B_NK_ROWS;
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32, BK = 128;
   constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
-  constexpr int QA = A_BYTES / 1024 / NW, QB = B_BYTES / 1024 / NW;
-  constexpr int NG = (BM + (ROWS ? BN : 0)) / 32;      // groups of 32 rows with scales
-  constexpr int UPW = (NG + NW - 1) / NW;              // scale DMAs a wave and step
-  constexpr int SLOT = ROWS ? 128 : 144;               // bytes of a group's scales: 32 rows, up to 4 B tiles
-  constexpr int SC = 8 * NG * SLOT, NSC = S > 2 ? 3 : 2;  // of eight blocks of K; how many of those there are
-  constexpr int NDMA = QA + QB + UPW;
+  constexpr int QA = A_BYTES / 1024 / NW, QB = B_BYTES / 1024 / NW, NDMA = QA + QB;
+  constexpr int NG = (BM + (ROWS ? BN : 0)) / 64;       // groups of 64 rows with scales
+  constexpr int NBT = BN / 128;                         // B tiles with a scale
+  constexpr int SC = 8 * 64 * NG * 4, SB = ROWS ? 0 : 8 * NBT * 4;  // bytes for eight blocks of K
+  constexpr int NSC = S > 2 ? 3 : 2;                    // how many eights there are
   static_assert(QA * 1024 * NW == A_BYTES && QB * 1024 * NW == B_BYTES, "DMA split");
-  static_assert(!KN || BN == 128 || BN == 256, "[K, N] layouts");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + NSC * SC];
+  static_assert(FN == 2 && BM % 64 == 0 && (!KN || BN == 128 || BN == 256), "layouts");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + NSC * (SC + SB)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr_of(smem)), sc0 = lds0 + S * STAGE;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr_of(smem)), sc0 = lds0 + S * STAGE, sb0 = sc0 + NSC * SC;
   const int nM = (int)((g.M + BM - 1) / BM), nN = (int)((g.N + BN - 1) / BN);
   const int2 tile = grouped_tile(xcd_remap(blockIdx.x, gridDim.x), nM, nN, gm);
   const int64_t m0 = (int64_t)tile.x * BM, n0 = (int64_t)tile.y * BN;
-  const int KB = (int)((g.K + 127) / 128);
-  const int64_t NB = (g.N + 127) / 128;
+  const int mrows = (int)min((int64_t)BM, g.M - m0), ncols = (int)min((int64_t)BN, g.N - n0);
+  const int KB = (int)((g.K + 127) / 128), NB = (int)((g.N + 127) / 128);
   const int kb0 = blockIdx.y * per, nk = min(KB - kb0, per);
 
   // ------------------------------------------------------------------ DMA sources
-  const uint8_t* a_src[QA];
-  const uint8_t* b_src[QB];
-  int a_k[QA], b_k[QB];  // first code of K within the block
+  // DMA q of a wave: eight rows of 128 bytes (a [K, N] operand: 1024 / BN rows of BN bytes).  Rows and columns
+  // past the tile's last are the last one again; they feed values that are not stored.
+  auto a_row = [&](int q) __attribute__((always_inline)) { return min(8 * (wave * QA + q), mrows - 1); };
+  auto b_row = [&](int q) __attribute__((always_inline)) {
+    return KN ? 1024 / BN * (wave * QB + q) : min(8 * (wave * QB + q), ncols - 1);
+  };
+  // A lane's offset from its DMA's first row: the row's, at most that of the tile's last row, and the piece's.
+  // Which piece a lane takes (the swizzle) depends on the DMA's parity alone.
+  constexpr int BR = KN ? BN / 16 : 8;  // lanes a row of B
+  const uint32_t a_lane = (uint32_t)(lane / 8) * (uint32_t)g.lda, b_lane = (uint32_t)(lane / BR) * (uint32_t)g.ldb;
+  uint32_t piece[2], b_piece[2];
 #pragma unroll
-  for (int q = 0; q < QA; ++q) {
-    const int row = 8 * (wave * QA + q) + lane / 8, c = (lane % 8) ^ ((row >> 1) & 7);
-    a_k[q] = 16 * c;
-    a_src[q] = g.A + min(m0 + row, g.M - 1) * g.lda + (int64_t)kb0 * BK + a_k[q];
+  for (int p = 0; p < 2; ++p) {
+    piece[p] = 16 * ((lane % 8) ^ ((4 * p + lane / 16) & 7));
+    const int kr = (1024 / BN * p + lane / BR) & 7;
+    b_piece[p] = KN ? min(16 * (BN == 256 ? (lane % BR) ^ (2 * (kr & 7)) : (lane % BR) ^ (2 * ((kr >> 1) & 3))), ncols - 16)
+                    : piece[p];
   }
+  auto a_off = [&](int q) __attribute__((always_inline)) {
+    return min(a_lane, (uint32_t)min(mrows - 1 - a_row(q), 7) * (uint32_t)g.lda) + piece[q & 1];
+  };
+  auto b_off = [&](int q) __attribute__((always_inline)) {
+    const uint32_t p = b_piece[q & 1];
+    return KN ? b_lane + p : min(b_lane, (uint32_t)min(ncols - 1 - b_row(q), 7) * (uint32_t)g.ldb) + p;
+  };
+  static_assert(QA % 2 == 0 && QB % 2 == 0, "a DMA's parity is its number's, the same in every wave");
+  const uint8_t* a_base = uniform_ptr(g.A + m0 * g.lda + (int64_t)kb0 * BK);
+  const uint8_t* b_base = uniform_ptr(KN ? g.B + (int64_t)kb0 * BK * g.ldb + n0 : g.B + n0 * g.ldb + (int64_t)kb0 * BK);
+  const int64_t b_step = KN ? BK * g.ldb : BK;
+  // DMA n of stage t
+  auto dma = [&](int n, int t) __attribute__((always_inline)) {
+    const uint32_t at = lds0 + t % S * STAGE;
+    if (n < QA) dma16(a_base + (int64_t)t * BK + a_row(n) * g.lda, a_off(n), at + (wave * QA + n) * 1024);
+    else dma16(b_base + t * b_step + b_row(n - QA) * g.ldb, b_off(n - QA), at + A_BYTES + (wave * QB + n - QA) * 1024);
+  };
+  // the last stage where it is a partial block: zeros past K
+  auto dma_ragged = [&](int t) __attribute__((always_inline)) {
+    const uint32_t at = lds0 + t % S * STAGE;
+    const int left = (int)(g.K - (int64_t)(KB - 1) * BK);
 #pragma unroll
-  for (int q = 0; q < QB; ++q) {
-    if constexpr (KN) {
-      constexpr int RPD = 1024 / BN;  // K rows a DMA
-      const int kr = RPD * (wave * QB + q) + lane / (BN / 16), cl = lane % (BN / 16);
-      const int c = BN == 256 ? cl ^ (2 * (kr & 7)) : cl ^ (2 * ((kr >> 1) & 3));
-      b_k[q] = kr;
-      b_src[q] = g.B + ((int64_t)kb0 * BK + kr) * g.ldb + min(n0 + 16 * c, g.N - 16);
-    } else {
-      const int row = 8 * (wave * QB + q) + lane / 8, c = (lane % 8) ^ ((row >> 1) & 7);
-      b_k[q] = 16 * c;
-      b_src[q] = g.B + min(n0 + row, g.N - 1) * g.ldb + (int64_t)kb0 * BK + b_k[q];
+    for (int q = 0; q < QA; ++q) {
+      const int row = 8 * (wave * QA + q) + lane / 8, k = 16 * ((lane % 8) ^ ((row >> 1) & 7));
+      const uint8_t* src = a_base + (int64_t)t * BK + a_row(q) * g.lda + a_off(q);
+      dma16(k < left ? (const void*)src : (const void*)&g_zero, at + (wave * QA + q) * 1024);
     }
-  }
-  const bool ragged = g.K % BK != 0;
-  auto issue = [&](int t, int st) __attribute__((always_inline)) {
-    const uint32_t abase = lds0 + st * STAGE, bbase = abase + A_BYTES;
-    const int64_t k0 = (int64_t)t * BK;
-    if (ragged && kb0 + t == KB - 1) {
-      const int left = (int)(g.K - (int64_t)(KB - 1) * BK);
 #pragma unroll
-      for (int q = 0; q < QA; ++q)
-        dma16(a_k[q] < left ? (const void*)(a_src[q] + k0) : (const void*)&g_zero, abase + (wave * QA + q) * 1024);
-#pragma unroll
-      for (int q = 0; q < QB; ++q)
-        dma16(b_k[q] < left ? (const void*)(b_src[q] + (KN ? k0 * g.ldb : k0)) : (const void*)&g_zero,
-              bbase + (wave * QB + q) * 1024);
-    } else {
-#pragma unroll
-      for (int q = 0; q < QA; ++q) dma16(a_src[q] + k0, abase + (wave * QA + q) * 1024);
-#pragma unroll
-      for (int q = 0; q < QB; ++q) dma16(b_src[q] + (KN ? k0 * g.ldb : k0), bbase + (wave * QB + q) * 1024);
+    for (int q = 0; q < QB; ++q) {
+      const int row = 8 * (wave * QB + q) + lane / 8;
+      const int k = KN ? b_row(q) + lane / (BN / 16) : 16 * ((lane % 8) ^ ((row >> 1) & 7));
+      const uint8_t* src = b_base + t * b_step + b_row(q) * g.ldb + b_off(q);
+      dma16(k < left ? (const void*)src : (const void*)&g_zero, at + A_BYTES + (wave * QB + q) * 1024);
     }
   };
-  // scales of group grp (A's rows, then B's) for block k of the chunk at block k8 of the thread block's own
-  auto scales = [&](int k8, int k, int grp) __attribute__((always_inline)) {
-    const int kb = min(kb0 + k8 + k, KB - 1);
-    const float* src;
-    if (lane < 32 || ROWS) {
-      const bool of_b = ROWS && grp >= BM / 32;
-      const int64_t row = of_b ? min(n0 + 32 * (grp - BM / 32) + (lane & 31), g.N - 1) : min(m0 + 32 * grp + (lane & 31), g.M - 1);
-      src = (of_b ? g.B_scale : g.A_scale) + row * KB + kb;
-    } else {
-      const int64_t nb = min(n0 / 128 + (lane - 32), NB - 1);
-      src = g.B_scale + (KN ? kb * NB + nb : nb * KB + kb);
+  const bool ragged = g.K % BK != 0 && kb0 + nk == KB;
+  const float* sa_base = uniform_ptr(g.A_scale + m0 * KB);
+  const float* sb_base = uniform_ptr(ROWS ? g.B_scale + n0 * KB : g.B_scale + n0 / 128 * (KN ? 1 : KB));
+  // the scales of unit `id` of the eight blocks from the thread block's block k8 on: block id % 8, group id / 8
+  auto scales = [&](int k8, int id) __attribute__((always_inline)) {
+    const int k = id & 7, grp = id >> 3, kb = min(kb0 + k8 + k, KB - 1);
+    const bool of_b = ROWS && grp >= BM / 64;
+    const int row = of_b ? min(64 * (grp - BM / 64) + lane, ncols - 1) : min(64 * grp + lane, mrows - 1);
+    dma4(of_b ? sb_base : sa_base, 4u * (uint32_t)(row * KB + kb), sc0 + (k8 >> 3) % NSC * SC + (k * NG + grp) * 256);
+  };
+  auto b_tile_scales = [&](int k8) __attribute__((always_inline)) {
+    if constexpr (!ROWS) {
+      const int first = min(kb0 + k8, KB - 1), k = min(lane / NBT, KB - 1 - first);
+      const int nb = min(lane % NBT, (ncols + 127) / 128 - 1);
+      if (lane < 8 * NBT)
+        dma4(sb_base + (int64_t)first * (KN ? NB : 1), 4u * (uint32_t)(KN ? k * NB + nb : nb * KB + k),
+             sb0 + (k8 >> 3) % NSC * SB);
     }
-    if (lane < (ROWS ? 32 : 32 + BN / 128)) dma4(src, sc0 + (k8 >> 3) % NSC * SC + (k * NG + grp) * SLOT);
+  };
+  // the wave's share, in step t, of the scales of the eight blocks behind block t's eight
+  auto step_scales = [&](int t) __attribute__((always_inline)) {
+    static_assert(NG <= NW, "a wave has at most one unit a step");
+    const int id = (t & 7) * NW + wave;
+    if (id < 8 * NG) scales((t & ~7) + 8, id);
+    if ((t & 7) == 7 && wave == NW - 1) b_tile_scales((t & ~7) + 8);
   };
 
   f32x16_t acc[FM][FN];
@@ -380,89 +425,179 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void fp8_matmul_tile_kernel(const 
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x16_t{};
 
-  auto compute = [&](int t, int st) __attribute__((always_inline)) {
-    const uint32_t abase = lds0 + st * STAGE, bbase = abase + A_BYTES;
-    const uint32_t sbase = sc0 + (t >> 3) % NSC * SC + (t & 7) * NG * SLOT;
+  // Step t, with the DMAs of stage t + S - 1 between its matrix instructions where MORE.  (No branch decides
+  // on a DMA: the compiler would move the matrix instructions past it.)
+  auto compute = [&](int t, auto more) __attribute__((always_inline)) {
+    constexpr bool MORE = decltype(more)::value;
+    const uint32_t abase = lds0 + t % S * STAGE, bbase = abase + A_BYTES;
+    const uint32_t sbase = sc0 + (t >> 3) % NSC * SC + (t & 7) * NG * 256;
     auto b_frag = [&](int j, int kk) __attribute__((always_inline)) -> i32x8 {
       const int col = wn * TN + 32 * j;
       if constexpr (KN && BN == 256) return read_kn8(bbase, col, kk, lane);
       else if constexpr (KN) return read_kn8n(bbase, col, kk, lane);
       else return read_km8(bbase, col + (lane & 31), kk, lane);
     };
-    i32x8 b[2][FN];
+    auto a_frag = [&](int i, int kk) __attribute__((always_inline)) {
+      return read_km8(abase, wm * TM + 32 * i + (lane & 31), kk, lane);
+    };
+    auto fence = [] __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
+    int sent = 0;  // a constant at every place, once unrolled
+    auto send = [&](int n) __attribute__((always_inline)) {
+      if constexpr (MORE)
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
+        for (int u = 0; u < n; ++u, ++sent)
+          if (sent < NDMA) dma(sent, t + S - 1);
+    };
+    auto promote = [&](int i, int j, const f32x16_t& c, const float (&sa)[FM], float sb) __attribute__((always_inline)) {
+      if constexpr (ROWS) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) b[kk][j] = b_frag(j, kk);
-    float sa[FM], sb[FN];
+        for (int r = 0; r < 16; r += 4) {
+          const f32x4_t s4 = *(const LDS_AS f32x4_t*)(uintptr_t)(sbase + 4 * (BM + wn * TN + 32 * j + 2 * r + 4 * (lane >> 5)));
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = *(const LDS_AS float*)(uintptr_t)(sbase + (wm * FM + i) * SLOT + 4 * (lane & 31));
+          for (int x = 0; x < 4; ++x) acc[i][j][r + x] = fmaf(c[r + x] * sa[i], s4[x], acc[i][j][r + x]);
+        }
+      } else {
+        const float s = sa[i] * sb;
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      if constexpr (!ROWS) sb[j] = *(const LDS_AS float*)(uintptr_t)(sbase + 128 + 4 * ((wn * TN + 32 * j) / 128));
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(c[r], s, acc[i][j][r]);
+      }
+    };
+    auto load_scales = [&](float (&sa)[FM], float& sb) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int row = wm * TM + 32 * i + (lane & 31);
-      const i32x8 a0 = read_km8(abase, row, 0, lane), a1 = read_km8(abase, row, 1, lane);
+      for (int i = 0; i < FM; ++i) sa[i] = *(const LDS_AS float*)(uintptr_t)(sbase + 4 * (wm * TM + 32 * i + (lane & 31)));
+      if constexpr (!ROWS)  // a wave's columns lie in one B tile
+        sb = *(const LDS_AS float*)(uintptr_t)(sb0 + (t >> 3) % NSC * SB + 4 * ((t & 7) * NBT + wn * TN / 128));
+    };
+    float sa[FM], sb = 1.0f;
+    if constexpr (WHOLE) {
+      f32x16_t c[FM][FN] = {};
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        f32x16_t c = multiply<WHOLE>(b[0][j], a0, f32x16_t{});
-        c = multiply<WHOLE>(b[1][j], a1, c);
-        if constexpr (ROWS) {
+      for (int kk = 0; kk < 2; ++kk) {
+        i32x8 a[FM], b[FN];
 #pragma unroll
-          for (int r = 0; r < 16; r += 4) {
-            const f32x4_t s4 = *(const LDS_AS f32x4_t*)(uintptr_t)(sbase + (BM / 32 + (wn * TN) / 32 + j) * SLOT +
-                                                                  4 * (8 * (r >> 2) + 4 * (lane >> 5)));
-            acc[i][j][r] = fmaf(c[r] * sa[i], s4[0], acc[i][j][r]);
-            acc[i][j][r + 1] = fmaf(c[r + 1] * sa[i], s4[1], acc[i][j][r + 1]);
-            acc[i][j][r + 2] = fmaf(c[r + 2] * sa[i], s4[2], acc[i][j][r + 2]);
-            acc[i][j][r + 3] = fmaf(c[r + 3] * sa[i], s4[3], acc[i][j][r + 3]);
+        for (int j = 0; j < FN; ++j) b[j] = b_frag(j, kk);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) a[i] = a_frag(i, kk);
+        if (kk == 1) load_scales(sa, sb);
+        fence();
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          bf16x8_t bw[FN];
+#pragma unroll
+          for (int j = 0; j < FN; ++j) bw[j] = widened(b[j], s);
+#pragma unroll
+          for (int i = 0; i < FM; ++i) {
+            const bf16x8_t aw = widened(a[i], s);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) c[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[j], aw, c[i][j], 0, 0, 0);
           }
-        } else {
-          const float s = sa[i] * sb[j];
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(c[r], s, acc[i][j][r]);
+          fence();
+          send((NDMA + 7) / 8);
+          fence();
         }
       }
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) promote(i, j, c[i][j], sa, sb);
+    } else {
+      // In a fixed order (scheduling fences): a block's promotion runs under the next block's matrix
+      // instructions, with two blocks and two A fragments in flight.
+      auto mfma = [&](const i32x8& b, const i32x8& a, const f32x16_t& c) __attribute__((always_inline)) {
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 0, 0, 127, 0, 127);
+      };
+      constexpr int EACH = (NDMA + 3) / 4;
+      i32x8 b[2][2], a0, a1;
+      b[0][0] = b_frag(0, 0);
+      b[0][1] = b_frag(1, 0);
+      a0 = a_frag(0, 0);
+      b[1][0] = b_frag(0, 1);
+      b[1][1] = b_frag(1, 1);
+      a1 = a_frag(0, 1);
+      load_scales(sa, sb);
+      fence();
+      const f32x16_t z = {};
+      f32x16_t t0 = mfma(b[0][0], a0, z), t1 = mfma(b[0][1], a0, z);
+      fence();
+      if (FM > 1) a0 = a_frag(1, 0);
+      send(EACH);
+      fence();
+      t0 = mfma(b[1][0], a1, t0);
+      t1 = mfma(b[1][1], a1, t1);
+      fence();
+      if (FM > 1) a1 = a_frag(1, 1);
+      send(EACH);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        fence();
+        promote(i, 0, t0, sa, sb);
+        fence();
+        if (i + 1 < FM) t0 = mfma(b[0][0], a0, z);
+        fence();
+        promote(i, 1, t1, sa, sb);
+        fence();
+        if (i + 1 < FM) {
+          t1 = mfma(b[0][1], a0, z);
+          fence();
+          if (i + 2 < FM) a0 = a_frag(i + 2, 0);
+          send(EACH);
+          fence();
+          t0 = mfma(b[1][0], a1, t0);
+          t1 = mfma(b[1][1], a1, t1);
+          fence();
+          if (i + 2 < FM) a1 = a_frag(i + 2, 1);
+          send(EACH);
+        }
+      }
+      send(NDMA);
     }
   };
 
   // ------------------------------------------------------------------ main loop
-  // A batch: a stage's operands, and the wave's share of the scales of the eight blocks behind block t's
-  // eight, where all (group, block) pairs are numbered with the blocks first.
-  auto batch = [&](int stage, int t) __attribute__((always_inline)) {
-    issue(stage, stage % S);
+  // Stage t + S - 1 is sent in step t, and with it scales of the eight blocks behind block t + S - 2's eight:
+  // what is sent in a step is complete S - 1 steps later.
+  for (int id = wave; id < 8 * NG; id += NW) scales(0, id);
+  if (wave == NW - 1) b_tile_scales(0);
+  for (int t = 0; t < S - 1 && t < nk; ++t) {
+    if (ragged && t == nk - 1) {
+      dma_ragged(t);
+    } else {
 #pragma unroll
-    for (int u = 0; u < UPW; ++u) {
-      const int id = min(((t & 7) * UPW + u) * NW + wave, 8 * NG - 1);
-      scales((t & ~7) + 8, id & 7, id >> 3);
+      for (int n = 0; n < NDMA; ++n) dma(n, t);
     }
-  };
-  for (int id = wave; id < 8 * NG; id += NW) scales(0, id & 7, id >> 3);
-  for (int t = 0; t < S - 1 && t < nk; ++t) batch(t, max(t - 1, 0));
-  for (int t = 0; t < nk; ++t) {
-    if (t + S - 1 <= nk) vm_lgkm_wait_barrier<(S - 2) * NDMA>();  // S - 2 batches lie behind stage t's
-    else vm_lgkm_wait_barrier<0>();
-    // the batch of step t is complete in step t + S - 1: the scales of a chunk's first block go out S - 2 steps ahead
-    if (t + S - 1 < nk) batch(t + S - 1, t + S - 2);
-    compute(t, t % S);
+    if (t > 0) step_scales(t - 1);
   }
-  vm_wait<0>();  // no DMA outlives the thread block
+  const int whole = max(nk - (S - 1) - (ragged ? 1 : 0), 0);
+  for (int t = 0; t < whole; ++t) {
+    vm_lgkm_wait_barrier<(S - 2) * NDMA>();  // at least S - 2 batches lie behind stage t's
+    step_scales(t + S - 2);
+    compute(t, std::true_type{});
+  }
+  for (int t = whole; t < nk; ++t) {
+    if (t + S - 1 <= nk) vm_lgkm_wait_barrier<(S - 2) * NDMA>();
+    else vm_lgkm_wait_barrier<0>();
+    if (t + S - 1 < nk) {
+      step_scales(t + S - 2);
+      dma_ragged(t + S - 1);
+    }
+    compute(t, std::false_type{});
+  }
 
   // ------------------------------------------------------------------ C
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int64_t row = m0 + wm * TM + 32 * i + (lane & 31);
-    if (row >= g.M) continue;
+    const int lr = wm * TM + 32 * i + (lane & 31);
+    if (lr >= mrows) continue;
+    const int64_t row = m0 + lr;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
-        const int64_t col = n0 + wn * TN + 32 * j + 8 * (r >> 2) + 4 * (lane >> 5);
-        if (col >= g.N) continue;
+        const int col = wn * TN + 32 * j + 2 * r + 4 * (lane >> 5);
+        if (col >= ncols) continue;
         float v[4] = {acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
-        if (part) *(float4*)(part + ((int64_t)blockIdx.y * g.M + row) * g.N + col) = make_float4(v[0], v[1], v[2], v[3]);
-        else store4<WHOLE>(g, row * g.ldc + col, v);
+        if (part) *(float4*)(part + ((int64_t)blockIdx.y * g.M + row) * g.N + n0 + col) = make_float4(v[0], v[1], v[2], v[3]);
+        else store4<WHOLE>(g, row * g.ldc + n0 + col, v);
       }
   }
 }
@@ -523,7 +658,8 @@ TilePlan tile_plan(const MatmulArgs& g) {
   const int KB = (int)((g.K + 127) / 128);
   auto tiles = [&](int bm, int bn) { return (g.M + bm - 1) / bm * ((g.N + bn - 1) / bn); };
   if (tiles(256, 256) >= 192) {
-    f.bm = f.bn = 256;
+    f.bm = 256;
+    f.bn = g.c_f32 ? 128 : 256;
   } else {
     f.bm = g.M <= 64 ? 64 : 128;
     f.bn = 128;
@@ -541,9 +677,10 @@ TilePlan tile_plan(const MatmulArgs& g) {
 template <int FORM, bool WHOLE>
 void launch_tiles_form(const MatmulArgs& g, const TilePlan& f, float* part, hipStream_t st) {
   const dim3 grid((unsigned)((g.M + f.bm - 1) / f.bm * ((g.N + f.bn - 1) / f.bn)), (unsigned)f.splits);
-  if (f.bm == 256) fp8_matmul_tile_kernel<FORM, WHOLE, 256, 256, 2, 4, 2><<<grid, 512, 0, st>>>(g, part, f.per, 8);
+  if (f.bm == 256 && WHOLE) fp8_matmul_tile_kernel<FORM, true, 256, 128, 4, 2, 2><<<grid, 512, 0, st>>>(g, part, f.per, 8);
+  else if (f.bm == 256) fp8_matmul_tile_kernel<FORM, false, 256, 256, 2, 4, 2><<<grid, 512, 0, st>>>(g, part, f.per, 8);
   else if (f.bm == 128) fp8_matmul_tile_kernel<FORM, WHOLE, 128, 128, 2, 2, 3><<<grid, 256, 0, st>>>(g, part, f.per, 8);
-  else fp8_matmul_tile_kernel<FORM, WHOLE, 64, 128, 1, 4, 4><<<grid, 256, 0, st>>>(g, part, f.per, 8);
+  else fp8_matmul_tile_kernel<FORM, WHOLE, 64, 128, 2, 2, 4><<<grid, 256, 0, st>>>(g, part, f.per, 8);
 }
 
 template <bool WHOLE>

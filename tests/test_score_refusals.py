@@ -114,7 +114,7 @@ def test_matmul_refusals(lib):
     make = lambda **o: changed(moe.matmul_desc(40, 64, 96), **o)  # noqa: E731
     bad = [dict(M=-1), dict(M=(1 << 30) + 1), dict(N=0), dict(N=8), dict(N=72), dict(N=(1 << 24) + 16, ldb=1 << 25, ldc=1 << 25),
            dict(K=0), dict(K=8), dict(K=100), dict(K=(1 << 24) + 16, lda=1 << 25), dict(M=1 << 30, N=64), dict(lda=80), dict(lda=104),
-           dict(lda=1 << 32), dict(ldb=48), dict(ldb=72), dict(ldb=1 << 32), dict(ldc=56), dict(ldc=68), dict(ldc=1 << 32),
+           dict(lda=(1 << 28) + 16), dict(ldb=48), dict(ldb=72), dict(ldb=(1 << 28) + 16), dict(ldc=56), dict(ldc=68), dict(ldc=1 << 32),
            dict(b_form=-1), dict(b_form=3), dict(b_form=moe.MOE_B_NK), dict(b_form=moe.MOE_B_NK_ROWS), dict(reserved=1)]
     for over in bad:   # the two forms [N, K] want ldb >= K = 96
         md = make(**over)
