@@ -21,15 +21,33 @@ namespace {
 // Blocks of four waves, a token each, that walk the tokens behind (a launch holds at most 2^32 threads).
 unsigned token_grid(int T) { return (unsigned)(T < (1 << 24) ? (T + 3) / 4 : 1 << 22); }
 
+// A double of another lane by DPP; lanes that get none keep `old`.
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ double dpp64(double old, double v) {
+  const int hi = __builtin_amdgcn_update_dpp(__double2hiint(old), __double2hiint(v), kCtrl, kRowMask, 0xf, kRowMask == 0xf);
+  const int lo = __builtin_amdgcn_update_dpp(__double2loint(old), __double2loint(v), kCtrl, kRowMask, 0xf, kRowMask == 0xf);
+  return __hiloint2double(hi, lo);
+}
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane), __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
 __device__ __forceinline__ double wave_max_f64(double v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = fmax(v, __shfl_xor(v, m, 64));
-  return v;
+  v = fmax(v, dpp64<0x128, 0xf>(v, v));
+  v = fmax(v, dpp64<0x124, 0xf>(v, v));
+  v = fmax(v, dpp64<0x122, 0xf>(v, v));
+  v = fmax(v, dpp64<0x121, 0xf>(v, v));
+  v = fmax(v, dpp64<0x142, 0xa>(v, v));
+  v = fmax(v, dpp64<0x143, 0xc>(v, v));
+  return lane_f64(v, 63);
 }
 __device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
+  v += dpp64<0x128, 0xf>(0.0, v);
+  v += dpp64<0x124, 0xf>(0.0, v);
+  v += dpp64<0x122, 0xf>(0.0, v);
+  v += dpp64<0x121, 0xf>(0.0, v);
+  v += dpp64<0x142, 0xa>(0.0, v);
+  v += dpp64<0x143, 0xc>(0.0, v);
+  return lane_f64(v, 63);
 }
 
 // e^(min(l, 0) - m) / (1 + e^-|l|): the sigmoid of l times e^-m, without overflow at any l
@@ -111,7 +129,7 @@ __device__ __forceinline__ Slot score_choose_token(const ScoreArgs& p, const flo
     const double v = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
-      const double o = __shfl(v, g, 64);
+      const double o = lane_f64(v, g);
       rank += o > v || (o == v && g < lane);
     }
     const uint64_t stay = __ballot(lane < p.groups && rank < p.group_topk && v > -INFINITY);
@@ -123,23 +141,18 @@ __device__ __forceinline__ Slot score_choose_token(const ScoreArgs& p, const flo
   }
   int mine = -1;
   for (int j = 0; j < p.k; ++j) {
-    double bv = -INFINITY;
-    int be = 0x7FFFFFFF;
+    double best = -INFINITY;
+    int at = -1;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (c[i] > bv) {  // ids rise with i: a tie keeps the lower one
-        bv = c[i];
-        be = lane + 64 * i;
+      if (c[i] > best) {  // ids rise with i: a tie keeps the lower one
+        best = c[i];
+        at = lane + 64 * i;
       }
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) {
-      const double ov = __shfl_xor(bv, m, 64);
-      const int oe = __shfl_xor(be, m, 64);
-      if (ov > bv || (ov == bv && oe < be)) {
-        bv = ov;
-        be = oe;
-      }
-    }
+    const double m = wave_max_f64(best);
+    int be = 0x7FFFFFFF;  // the lowest id of those that have the maximum
+    for (uint64_t won = __ballot(at >= 0 && best == m); won; won &= won - 1)
+      be = min(be, __builtin_amdgcn_readlane(at, __builtin_ctzll(won)));
     if (be == 0x7FFFFFFF) break;  // the same in every lane
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
@@ -173,25 +186,29 @@ __global__ __launch_bounds__(256) void score_choose_kernel(const ScoreArgs p, co
 // ------------------------------------------------------------------------------ fast choice
 // LPT lanes a token (16: four tokens a wave; 64: one), for k <= 16 and a number of groups that divides
 // 16.  Each group's experts lie in the EPL registers of LPT / groups neighbouring lanes.  Scores are
-// fp32; a score's lowest four bits are replaced by its register's number, so that a value names its
-// expert within the lane, and a round of the choice is one maximum over the lanes (in the vector ALU) of
-// each lane's best, the winner moving up its second best.  The lanes' best two are what a group's value
-// is made of as well.
+// fp32; a value's lowest four bits are replaced by its register's number, so that it names its expert
+// within the lane.  A lane keeps its best four in order, and a round of the choice is one maximum over the
+// lanes (in the vector ALU) of their first, whose lane then moves up its others; a lane that has given
+// four takes the next four out of its registers.  (With the best two, most rounds of a wave had a lane to
+// fill up again: 21804x256 in groups 68 us for the whole call.)  The lanes' best two are what a group's
+// value is made of.
 //
-// An order that fp32 does not settle is found, not guessed: wherever two values that decide something
-// (neighbours in the order up to the first that is left out, the last group that stays and the first that
-// does not) differ by less than what scores can be off, or where a value is not an ordinary number, the token
-// is done again in 64 bits by the whole wave.  What a score is off, relative to |c| + max |bias|: sigmoid
-// 4 2^-24 (an exponential with its argument's rounding, a sum, a reciprocal: |x| s (1 - s) < 1/4), softmax 2^-18
-// (logits up to 60 below the largest), and 2^-20 for the four bits; twice that for two values: below 2^-18
-// and 2^-16.  About one token in a hundred (256 experts) is done again.
+// An order that fp32 does not settle is found, not guessed, wherever two values that decide something differ
+// by less than what scores can be off.  The chosen and the first left out (and no other could be among them: one
+// more round shows the next value): their values again in 64 bits, one a lane, and their order by counting.
+// The last group that stays and the first that does not, a softmax with a bias (whose sum would have to be
+// taken again), or a value that is no ordinary number: the whole token in 64 bits, by the wave.  What a score
+// is off, relative to |c| + max |bias|: sigmoid 4 2^-24 (an exponential with its argument's rounding, a sum, a
+// reciprocal: |x| s (1 - s) < 1/4), softmax 2^-18 (logits up to 60 below the largest), and 2^-20 for the four
+// bits; twice that for two values: below 2^-18 and 2^-16.
 //
 // A block takes `seg` tokens, keeps their ids, and gives each pair its rank among the block's pairs of the
-// same expert (each wave a quarter of the pairs, in order; lanes with the same expert by one ballot per id
-// bit) and each expert its count: the plan's first pass, without reading the ids back.  A batch that is one
+// same expert (each wave a share of the pairs, in order; lanes with the same expert by one ballot per id bit)
+// and each expert its count: the plan's first pass, without reading the ids back.  A batch that is one
 // block's writes the whole plan.
+constexpr int kChooseWaves = 8;
 constexpr int kSegPairs = 2048;   // pairs of a block, at most
-constexpr int kSegments = 512;    // blocks, at most, that the plan is made of
+constexpr int kSegments = 1024;   // blocks, at most, that the plan is made of
 constexpr int kOneBlock = 64;     // tokens that one block does by itself
 constexpr float kNone = -3.0e38f; // below every value that counts
 
@@ -200,10 +217,52 @@ struct SegPlan {
 };
 __host__ __device__ inline SegPlan seg_plan(int64_t T, int64_t k) {
   if (T <= kOneBlock) return SegPlan{kOneBlock, 1};
-  const int64_t seg = ((T + kSegments - 1) / kSegments + 15) / 16 * 16;
+  const int64_t seg = ((T + kSegments - 1) / kSegments + 31) / 32 * 32;
   return SegPlan{(int)seg, (int)((T + seg - 1) / seg)};
 }
 bool seg_plan_fits(int64_t T, int64_t k) { return T <= (int64_t)kSegments * kSegPairs && seg_plan(T, k).seg * k <= kSegPairs; }
+
+// Inclusive sum over a wave's lanes, in the vector ALU.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 of each row into the next: rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 into rows 2 and 3
+  return v;
+}
+
+// By the threads of a block, 256 of which have four experts each: first positions of the experts (start, in LDS, which may be the counts themselves) from
+// their counts, to offsets and counts too where they are asked for.
+__device__ __forceinline__ void expert_starts(int E, const int32_t* cnt, int* start, int32_t* __restrict__ offsets,
+                                              int32_t* __restrict__ counts) {
+  __shared__ int part[4];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, e0 = threadIdx.x * 4;
+  int c[4], sum = 0, x = 0;
+  if (wv < 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += c[i] = e0 + i < E ? cnt[e0 + i] : 0;
+    x = wave_scan(sum);
+    if (lane == 63) part[wv] = x;
+  }
+  __syncthreads();
+  if (wv < 4) {
+    int at = x - sum;
+    for (int i = 0; i < wv; ++i) at += part[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e0 + i < E) {
+        start[e0 + i] = at;
+        if (offsets) offsets[e0 + i] = at;
+        if (counts) counts[e0 + i] = c[i];
+      }
+      at += c[i];
+    }
+    if (offsets && threadIdx.x == 255) offsets[E] = at;
+  }
+  __syncthreads();
+}
 
 template <int LPT>
 __device__ __forceinline__ float lanes_max(float v) {
@@ -236,28 +295,39 @@ __device__ __forceinline__ void merge_best(float& a, float& b) {
   a = fmaxf(a, c);
 }
 
-template <int kRot>
-__device__ __forceinline__ void rank_by_rotation(float v, int grp, int lg, int& rank) {
+// Groups of kLg lanes of a row of 16: how many have a larger value, or the same and a lower number.
+template <int kLg, int kRot = kLg>
+__device__ __forceinline__ void rank_groups(float v, int& rank) {
   if constexpr (kRot < 16) {
     const float o = dpp<0x120 + kRot, 0xf>(v, v);  // the lane kRot below, around the row
-    const int og = (((int)threadIdx.x - kRot) & 15) / lg;
-    rank += o > v || (o == v && og < grp);
-    rank_by_rotation<kRot + 1>(v, grp, lg, rank);
+    rank += o > v || (o == v && ((int)threadIdx.x & 15) >= kRot);
+    rank_groups<kLg, kRot + kLg>(v, rank);
+  }
+}
+
+// Places of 16 lanes' values in descending order; equal ones by id.
+template <int kRot>
+__device__ __forceinline__ void rank_candidates(double v, int id, int& rank) {
+  if constexpr (kRot < 16) {
+    auto turn = [](int w) __attribute__((always_inline)) {
+      return __builtin_amdgcn_update_dpp(w, w, 0x120 + kRot, 0xf, 0xf, true);
+    };
+    const double o = __hiloint2double(turn(__double2hiint(v)), turn(__double2loint(v)));
+    const int oid = turn(id);
+    rank += o > v || (o == v && oid < id);
+    rank_candidates<kRot + 1>(v, id, rank);
   }
 }
 
 template <int LPT, int EPL, int EPL64, bool SIG>
-__global__ __launch_bounds__(256) void score_choose_fast_kernel(const ScoreArgs p, const float* __restrict__ logits,
-                                                                const float* __restrict__ bias,
-                                                                const uint8_t* __restrict__ mask,
-                                                                int32_t* __restrict__ ids, float* __restrict__ w, int seg,
-                                                                int32_t* __restrict__ segcnt, uint16_t* __restrict__ ranks,
-                                                                int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
-                                                                int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm) {
-  constexpr int TPW = 64 / LPT;  // tokens a wave and pass
-  __shared__ double sh_c[4][EPL64 * 64];
-  __shared__ int sh_ids[kSegPairs];
-  extern __shared__ int sh_cnt[];  // [4][E], where the plan is made here
+__global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 4 : 2) void score_choose_fast_kernel(
+    const ScoreArgs p, const float* __restrict__ logits, const float* __restrict__ bias, const uint8_t* __restrict__ mask,
+    int32_t* __restrict__ ids, float* __restrict__ w, int seg, int32_t* __restrict__ segcnt, uint16_t* __restrict__ ranks,
+    int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm) {
+  constexpr int NW = kChooseWaves, NT = 64 * NW, TPW = 64 / LPT;  // waves, threads, tokens a wave and pass
+  __shared__ double sh_c[NW][EPL64 * 64];
+  __shared__ int sh_ids[kSegPairs], sh_cand[NW][TPW][16];
+  extern __shared__ int sh_run[];  // [NW][E], where the plan is made here
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, sub = lane / LPT, l = lane % LPT;
   const int lg = LPT / p.groups, each = p.E / p.groups, grp = l / lg;
   const int epl = (each + lg - 1) / lg, first = (l % lg) * epl, n = max(min(each - first, epl), 0), base = grp * each + first;
@@ -265,15 +335,18 @@ __global__ __launch_bounds__(256) void score_choose_fast_kernel(const ScoreArgs 
   const int64_t t0 = (int64_t)blockIdx.x * seg;
   const int ntok = (int)min((int64_t)seg, p.T - t0);
 
+  // the biases; a register without an expert reads its neighbour's and is barred as by a bias of -inf
   float b[EPL], bm = 0.0f;
 #pragma unroll
+  for (int i = 0; i < EPL; ++i) b[i] = bias ? bias[min(base + i, p.E - 1)] : 0.0f;
+#pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    b[i] = i < n ? (bias ? bias[base + i] : 0.0f) : -INFINITY;
     if (fabsf(b[i]) < 1e30f) bm = fmaxf(bm, fabsf(b[i]));
+    if (b[i] == -INFINITY || i >= n) b[i] = kNone;
   }
   bm = lanes_max<LPT>(bm);
 
-  for (int r0 = wv * TPW; r0 < ntok; r0 += 4 * TPW) {
+  for (int r0 = wv * TPW; r0 < ntok; r0 += NW * TPW) {
     const int local = r0 + sub;
     const int64_t t = t0 + min(local, ntok - 1);
     const bool active = local < ntok && (!mask || mask[t] != 0);
@@ -282,41 +355,49 @@ __global__ __launch_bounds__(256) void score_choose_fast_kernel(const ScoreArgs 
     if (vec) {
 #pragma unroll
       for (int i = 0; i < EPL; i += 4) {
-        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (active && i < n) v = *(const float4*)(row + base + i);
+        const float4 v = *(const float4*)(row + min(base + i, p.E - 4));
         x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) x[i] = active && i < n ? row[base + i] : -INFINITY;
+      for (int i = 0; i < EPL; ++i) x[i] = row[min(base + i, p.E - 1)];
     }
     float top = 0.0f, sum = 1.0f, inv = 1.0f;
     if constexpr (!SIG) {
       top = x[0];
 #pragma unroll
-      for (int i = 1; i < EPL; ++i) top = fmaxf(top, x[i]);
+      for (int i = 1; i < EPL; ++i) top = fmaxf(top, x[i]);  // (a neighbour's logit counts once more: no matter)
       top = lanes_max<LPT>(top);
       if (top == -INFINITY) top = 0.0f;
       sum = 0.0f;
+      int here = n;
+      asm volatile("" : "+v"(here));  // compared where it is needed: 16 masks would fill the scalar registers
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) sum += c[i] = __expf(x[i] - top);
+      for (int i = 0; i < EPL; ++i) {
+        c[i] = __expf(x[i] - top);
+        if (i < here) sum += c[i];
+      }
       sum = lanes_sum<LPT>(sum);
       inv = 1.0f / sum;
     }
-    bool odd = false;  // something for the 64-bit path
-    float b1 = kNone, b2 = kNone;
+    float nought = 0.0f;  // NaN once a value is no ordinary number
+    float b1 = kNone, b2 = kNone, b3 = kNone, b4 = kNone;
+    auto insert = [&](float v) __attribute__((always_inline)) {
+      b4 = __builtin_amdgcn_fmed3f(b3, b4, v);
+      b3 = __builtin_amdgcn_fmed3f(b2, b3, v);
+      b2 = __builtin_amdgcn_fmed3f(b1, b2, v);
+      b1 = fmaxf(b1, v);
+    };
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const float s = SIG ? __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) : c[i] * inv;
-      const float v = s + b[i];
-      const bool barred = x[i] == -INFINITY || b[i] == -INFINITY;
-      odd |= !barred && !(fabsf(v) < 1e30f);
+      const float v = (SIG ? __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) : c[i] * inv) + b[i];
+      const bool barred = x[i] == -INFINITY;
+      nought = fmaf(barred ? b[i] : v, 0.0f, nought);
       c[i] = barred ? kNone : __uint_as_float((__float_as_uint(v) & ~15u) | (15 - i));
-      b2 = __builtin_amdgcn_fmed3f(b1, b2, c[i]);
-      b1 = fmaxf(b1, c[i]);
+      insert(c[i]);
     }
+    bool odd = !(nought == 0.0f);  // something for the 64-bit path
     constexpr float kOff = SIG ? 0x1p-18f : 0x1p-16f;
-    auto apart = [&](float hi, float lo) __attribute__((always_inline)) { return hi - lo > kOff * (fabsf(lo) + bm); };
     bool dropped = false;
     if (p.groups > 1) {
       float g1 = b1, g2 = b2;
@@ -329,8 +410,10 @@ __global__ __launch_bounds__(256) void score_choose_fast_kernel(const ScoreArgs 
       const float v = p.group_best == 2 && g2 > -1e38f ? g1 + g2 : g1;
       int rank = 0;
       if constexpr (LPT == 16) {
-        rank_by_rotation<1>(v, grp, lg, rank);
-        rank /= lg;
+        if (lg == 1) rank_groups<1>(v, rank);
+        else if (lg == 2) rank_groups<2>(v, rank);
+        else if (lg == 4) rank_groups<4>(v, rank);
+        else rank_groups<8>(v, rank);
       } else {
         for (int g = 0; g < p.groups; ++g) {
           const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), g * lg));
@@ -340,46 +423,69 @@ __global__ __launch_bounds__(256) void score_choose_fast_kernel(const ScoreArgs 
       dropped = !alive || rank >= p.group_topk;
       const float least = -lanes_max<LPT>(dropped ? kNone : -v), next = lanes_max<LPT>(dropped && alive ? v : kNone);
       odd |= next > -1e38f && !(least - next > 2 * kOff * (fabsf(next) + 2 * bm));
-      if (dropped) b1 = b2 = kNone;
+      if (dropped) b1 = b2 = b3 = b4 = kNone;
     }
     if (!active) b1 = kNone - 1e35f * l;  // one winner in every round, which takes nothing
-    bool half = false;                    // b2 has moved up
-    float before = INFINITY;
-    for (int j = 0; j <= p.k; ++j) {
+    const int keep = min(p.k + 1, 16);    // candidates: one more than are chosen, where the lanes hold it
+    int* cand = sh_cand[wv][sub];
+    float mine_v = 0.0f, last = 0.0f;     // lane j: the value of round j; the last round's
+    int given = 0;
+    bool several = false;                 // winners in a round
+    for (int j = 0; j <= keep; ++j) {
       const float m = lanes_max<LPT>(b1);
       const bool win = b1 == m;
-      odd |= __popcll(__ballot(win)) != TPW || (active && !apart(before, m));
-      before = m;
-      if (j == p.k) break;
-      odd |= active && !(fabsf(m) > 1e-30f && m > -1e38f);
-      const bool take = win && active;
-      if (take) sh_ids[local * p.k + j] = base + 15 - (int)(__float_as_uint(m) & 15u);
-      const bool refill = take && half;
-      if (take) {
+      several |= __popcll(__ballot(win)) != TPW;
+      last = m;
+      if (j == keep) break;
+      if (l == j) mine_v = m;
+      if (win && active) {
+        cand[j] = base + 15 - (int)(__float_as_uint(m) & 15u);
         b1 = b2;
-        b2 = kNone;
-        half = true;
+        b2 = b3;
+        b3 = b4;
+        b4 = kNone;
+        ++given;
       }
-      if (__ballot(refill)) {
-        float n1 = kNone, n2 = kNone;
+      if constexpr (EPL > 4) {
+        if (__ballot(given == 4)) {
+          const float a1 = b1, a2 = b2, a3 = b3, a4 = b4;
+          b1 = b2 = b3 = b4 = kNone;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const float v = c[i] < m && !dropped ? c[i] : kNone;
-          n2 = __builtin_amdgcn_fmed3f(n1, n2, v);
-          n1 = fmaxf(n1, v);
-        }
-        if (refill) {
-          b1 = n1;
-          b2 = n2;
-          half = false;
+          for (int i = 0; i < EPL; ++i) insert(c[i] < m && !dropped ? c[i] : kNone);
+          if (given == 4) {
+            given = 0;
+          } else {
+            b1 = a1, b2 = a2, b3 = a3, b4 = a4;
+          }
         }
       }
+    }
+    // what follows each candidate (the last: the value of the round behind it), and whether it is apart from it
+    float after = __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(last), __float_as_uint(mine_v), 0x101, 0xf, 0xf, false));
+    if (l == keep - 1) after = last;
+    auto apart = [&](float hi, float lo) __attribute__((always_inline)) { return hi - lo > kOff * (fabsf(lo) + bm); };
+    const bool unsure = active && l < p.k && !apart(mine_v, after);
+    odd |= several || (active && l < p.k && !(fabsf(mine_v) > 1e-30f && mine_v > -1e38f));
+    if (!SIG && bias) odd |= unsure;
+    odd |= active && l == p.k - 1 && !apart(mine_v, last);
+    // the lanes' candidates (an id past the experts: none was left, and the token is done again below)
+    int mine = active && l < keep ? min(cand[l], p.E - 1) : 0;
+    if ((SIG || !bias) && __ballot(unsure)) {
+      double v = -INFINITY;
+      if (active && l < keep) {
+        const double x1 = row[mine];
+        v = SIG ? sigmoid_scaled(x1, 0.0) + (bias ? (double)bias[mine] : 0.0) : x1;
+      }
+      int rank = 0;
+      rank_candidates<1>(v, mine, rank);
+      if (active && l < keep) cand[rank] = mine;
+      if (active && l < keep) mine = min(cand[l], p.E - 1);
     }
     // slot l of the lanes' token, and its weight
     const bool slot = l < p.k && local < ntok;
     int id = -1;
     float q = 0.0f;
-    if (slot && active) id = min(sh_ids[local * p.k + l], p.E - 1);  // (past it: no expert was left, done again below)
+    if (slot && active) id = mine;
     const float x1 = id >= 0 ? row[id] : 0.0f;
     float z;
     if constexpr (SIG) {
@@ -414,107 +520,106 @@ __global__ __launch_bounds__(256) void score_choose_fast_kernel(const ScoreArgs 
   if (!segcnt && !perm) return;  // the plan is made elsewhere
 
   // ------------------------------------------------------------------ ranks and counts
-  const int pairs = ntok * p.k, quarter = ((pairs + 3) / 4 + 63) / 64 * 64;
-  const int lo = min(wv * quarter, pairs), hi = min(lo + quarter, pairs);
-  int* run = sh_cnt + wv * p.E;
-  for (int e = threadIdx.x; e < 4 * p.E; e += 256) sh_cnt[e] = 0;
+  constexpr int STEPS = kSegPairs / NT;
+  const int pairs = ntok * p.k, share = ((pairs + NW - 1) / NW + 63) / 64 * 64;
+  const int lo = min(wv * share, pairs), hi = min(lo + share, pairs);
+  int* run = sh_run + wv * p.E;
+  for (int e = lane; e < p.E; e += 64) run[e] = 0;
   __syncthreads();
-  for (int i = lo + lane; i < hi; i += 64)
-    if (sh_ids[i] >= 0) atomicAdd(&run[sh_ids[i]], 1);
-  __syncthreads();
-  int* start = (int*)sh_c;  // first positions of the experts, where the block is the whole batch
-  for (int e = threadIdx.x; e < p.E; e += 256) {
-    int at = 0;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int c = sh_cnt[v * p.E + e];
-      sh_cnt[v * p.E + e] = at;
-      at += c;
-    }
-    if (perm) start[e] = at;
-    else segcnt[(int64_t)blockIdx.x * p.E + e] = at;
-  }
-  __syncthreads();
-  if (perm) {  // counts, and their exclusive sum by one wave
-    if (wv == 0) {
-      int before = 0;
-      for (int e0 = 0; e0 < p.E; e0 += 64) {
-        const int e = e0 + lane, c = e < p.E ? start[e] : 0;
-        int x = c;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-          const int y = __shfl_up(x, o, 64);
-          if (lane >= o) x += y;
-        }
-        if (e < p.E) {
-          counts[e] = c;
-          offsets[e] = start[e] = before + x - c;
-        }
-        before += __shfl(x, 63, 64);
-      }
-      if (lane == 0) offsets[p.E] = before;
-    }
-    __syncthreads();
-  }
   int bits = 1;
   while ((1 << bits) < p.E) ++bits;
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
-  for (int i0 = lo; i0 < hi; i0 += 64) {
-    const int i = i0 + lane;
-    const int e = i < hi ? sh_ids[i] : -1;
+  int of[STEPS], rank[STEPS];  // the lane's pairs: expert, rank in the wave's share
+#pragma unroll
+  for (int u = 0; u < STEPS; ++u) {
+    of[u] = -1;
+    rank[u] = 0;
+    if (lo + 64 * u >= hi) continue;
+    const int i = lo + 64 * u + lane, e = i < hi ? sh_ids[i] : -1;
     uint64_t same = __ballot(e >= 0);
     for (int x = 0; x < bits; ++x) {
       const uint64_t set = __ballot((e >> x) & 1);
       same &= (e >> x) & 1 ? set : ~set;
     }
-    int rank = 0;
-    if (e >= 0) rank = run[e] + __popcll(same & below);
+    if (e >= 0) rank[u] = run[e] + __popcll(same & below);
     __builtin_amdgcn_wave_barrier();
     if (e >= 0 && (same & below) == 0) run[e] += __popcll(same);
     __builtin_amdgcn_wave_barrier();
-    if (i < hi) {
-      if (!perm) {
-        ranks[t0 * p.k + i] = (uint16_t)rank;
-      } else if (e >= 0) {
-        perm[start[e] + rank] = i;
-        inv_perm[i] = start[e] + rank;
-      } else {
-        inv_perm[i] = -1;
-      }
+    of[u] = e;
+  }
+  __syncthreads();
+  int* start = (int*)sh_c;  // first positions of the experts, where the block is the whole batch
+  for (int e = threadIdx.x; e < p.E; e += NT) {
+    int at = 0;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) {
+      const int c = sh_run[v * p.E + e];
+      sh_run[v * p.E + e] = at;
+      at += c;
+    }
+    if (perm) start[e] = at;  // the total, turned into first positions below
+    else segcnt[(int64_t)blockIdx.x * p.E + e] = at;
+  }
+  __syncthreads();
+  if (perm) expert_starts(p.E, start, start, offsets, counts);
+#pragma unroll
+  for (int u = 0; u < STEPS; ++u) {
+    const int i = lo + 64 * u + lane;
+    if (i >= hi) break;
+    const int at = of[u] >= 0 ? run[of[u]] + rank[u] : 0;
+    if (!perm) {
+      ranks[t0 * p.k + i] = (uint16_t)at;
+    } else if (of[u] >= 0) {
+      perm[start[of[u]] + at] = i;
+      inv_perm[i] = start[of[u]] + at;
+    } else {
+      inv_perm[i] = -1;
     }
   }
 }
 
-// Each expert's counts over the blocks: exclusive sums in their place, the total in counts.  64 experts a
-// block, a sixteenth of the rows a wave.
+// Each expert's counts over the blocks: exclusive sums in their place, the total in counts.  16 experts a
+// block (64 bytes of a row); 64 groups of neighbouring rows.
 __global__ __launch_bounds__(1024) void score_scan_kernel(int32_t* __restrict__ segcnt, int E, int S,
                                                           int32_t* __restrict__ counts) {
-  __shared__ int part[16][64];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, e = blockIdx.x * 64 + lane;
-  constexpr int ROWS = kSegments / 16;
-  const int per = (S + 15) / 16, lo = wv * per;
+  __shared__ int part[64][16];
+  const int l = threadIdx.x & 15, grp = threadIdx.x >> 4, e = blockIdx.x * 16 + l;
+  constexpr int ROWS = kSegments / 64;
+  const int per = (S + 63) / 64, lo = grp * per;
   int v[ROWS], sum = 0;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     v[i] = i < per && lo + i < S && e < E ? segcnt[(int64_t)(lo + i) * E + e] : 0;
     sum += v[i];
   }
-  part[wv][lane] = sum;
+  part[grp][l] = sum;
   __syncthreads();
-  int at = 0, total = 0;
+  if (threadIdx.x < 256) {  // the groups' sums, in place: 16 threads an expert, four groups each
+    const int x = threadIdx.x & 15, q = threadIdx.x >> 4;
+    int s4[4], t = 0;
 #pragma unroll
-  for (int x = 0; x < 16; ++x) {
-    if (x < wv) at += part[x][lane];
-    total += part[x][lane];
+    for (int i = 0; i < 4; ++i) {
+      s4[i] = t;
+      t += part[4 * x + i][q];
+    }
+    int y = t;
+    y += __builtin_amdgcn_update_dpp(0, y, 0x111, 0xf, 0xf, true);
+    y += __builtin_amdgcn_update_dpp(0, y, 0x112, 0xf, 0xf, true);
+    y += __builtin_amdgcn_update_dpp(0, y, 0x114, 0xf, 0xf, true);
+    y += __builtin_amdgcn_update_dpp(0, y, 0x118, 0xf, 0xf, true);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[4 * x + i][q] = y - t + s4[i];
+    if (x == 15 && blockIdx.x * 16 + q < E) counts[blockIdx.x * 16 + q] = y;
   }
+  __syncthreads();
   if (e >= E) return;
+  int at = part[grp][l];
 #pragma unroll
   for (int i = 0; i < ROWS; ++i)
     if (i < per && lo + i < S) {
       segcnt[(int64_t)(lo + i) * E + e] = at;
       at += v[i];
     }
-  if (wv == 0) counts[e] = total;
 }
 
 // Positions of the pairs: the expert's first, its pairs in the blocks before, the rank in the block.
@@ -523,42 +628,23 @@ __global__ __launch_bounds__(256) void score_place_kernel(const int32_t* __restr
                                                           const uint16_t* __restrict__ ranks,
                                                           const int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                           int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm) {
-  __shared__ int start[1024], part[4];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int e0 = threadIdx.x * 4;
-  int c[4], sum = 0;
+  __shared__ int start[1024];
+  constexpr int PER = 2;
+  int e[PER], at[PER];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sum += c[i] = e0 + i < E ? counts[e0 + i] : 0;
-  int x = sum;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(x, o, 64);
-    if (lane >= o) x += y;
+  for (int i = 0; i < PER; ++i) {
+    const int64_t q = (int64_t)blockIdx.x * (256 * PER) + 256 * i + threadIdx.x;
+    e[i] = q < pairs ? ids[q] : -1;
+    at[i] = q < pairs ? ranks[q] : 0;
+    if (e[i] >= 0) at[i] += segbase[q / seg_pairs * E + e[i]];
   }
-  if (lane == 63) part[wv] = x;
-  __syncthreads();
-  int at = x - sum;
-  for (int i = 0; i < wv; ++i) at += part[i];
+  expert_starts(E, counts, start, blockIdx.x == 0 ? offsets : nullptr, nullptr);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (e0 + i < E) {
-      start[e0 + i] = at;
-      if (blockIdx.x == 0) offsets[e0 + i] = at;
-    }
-    at += c[i];
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 255) offsets[E] = at;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t q = (int64_t)blockIdx.x * 1024 + 256 * i + threadIdx.x;
+  for (int i = 0; i < PER; ++i) {
+    const int64_t q = (int64_t)blockIdx.x * (256 * PER) + 256 * i + threadIdx.x;
     if (q >= pairs) return;
-    const int e = ids[q];
-    int pos = -1;
-    if (e >= 0) {
-      pos = start[e] + segbase[q / seg_pairs * E + e] + ranks[q];
-      perm[pos] = (int32_t)q;
-    }
+    const int pos = e[i] >= 0 ? start[e[i]] + at[i] : -1;
+    if (pos >= 0) perm[pos] = (int32_t)q;
     inv_perm[q] = pos;
   }
 }
@@ -588,14 +674,15 @@ struct RouteOut {
 template <int LPT, int EPL, int EPL64>
 void launch_fast(const ScoreArgs& p, const float* logits, const float* bias, const uint8_t* mask, const RouteOut& o,
                  const SegPlan& sp, int32_t* segcnt, uint16_t* ranks, hipStream_t st) {
-  const size_t lds = 4 * (size_t)p.E * sizeof(int);
+  const size_t lds = kChooseWaves * (size_t)p.E * sizeof(int);
+  const unsigned block = 64 * kChooseWaves;
   int32_t* perm = sp.S == 1 && o.perm ? o.perm : nullptr;
   const unsigned grid = (unsigned)sp.S;
   if (p.sigmoid)
-    score_choose_fast_kernel<LPT, EPL, EPL64, true><<<grid, 256, lds, st>>>(p, logits, bias, mask, o.ids, o.w, sp.seg, segcnt,
+    score_choose_fast_kernel<LPT, EPL, EPL64, true><<<grid, block, lds, st>>>(p, logits, bias, mask, o.ids, o.w, sp.seg, segcnt,
                                                                            ranks, o.counts, o.offsets, perm, o.inv_perm);
   else
-    score_choose_fast_kernel<LPT, EPL, EPL64, false><<<grid, 256, lds, st>>>(p, logits, bias, mask, o.ids, o.w, sp.seg, segcnt,
+    score_choose_fast_kernel<LPT, EPL, EPL64, false><<<grid, block, lds, st>>>(p, logits, bias, mask, o.ids, o.w, sp.seg, segcnt,
                                                                             ranks, o.counts, o.offsets, perm, o.inv_perm);
 }
 
@@ -624,8 +711,8 @@ hipError_t launch_score_route(const ScoreArgs& p, const float* logits, const flo
     else if (lane_share(p, 64) <= 8) launch_fast<64, 8, 8>(p, logits, bias, mask, o, sp, segcnt, ranks, st);
     else launch_fast<64, 16, 16>(p, logits, bias, mask, o, sp, segcnt, ranks, st);
     if (segcnt) {
-      score_scan_kernel<<<(p.E + 63) / 64, 1024, 0, st>>>(segcnt, p.E, sp.S, counts);
-      score_place_kernel<<<(unsigned)((pairs + 1023) / 1024), 256, 0, st>>>(ids, pairs, p.E, sp.seg * p.k, segcnt, ranks,
+      score_scan_kernel<<<(p.E + 15) / 16, 1024, 0, st>>>(segcnt, p.E, sp.S, counts);
+      score_place_kernel<<<(unsigned)((pairs + 511) / 512), 256, 0, st>>>(ids, pairs, p.E, sp.seg * p.k, segcnt, ranks,
                                                                             counts, offsets, perm, inv_perm);
     }
     const hipError_t e = hipGetLastError();

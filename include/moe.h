@@ -375,7 +375,7 @@ int moe_adamw_step(const moe_adamw* hyper, const moe_tensor* tensors, int64_t n_
  * An expert whose logit or bias is -inf cannot be chosen: where fewer than k can, the slots behind them
  * have id -1 and weight 0 (a group in which none can be chosen never stays, and one with a single such
  * expert has its c for a value).  A token whose token_mask byte is 0 (uint8 [T]; NULL: none) has ids -1
- * and weights 0; its logits are not read.  A token with a NaN among its logits or the bias, or a +inf
+ * and weights 0, whatever its logits are.  A token with a NaN among its logits or the bias, or a +inf
  * logit where the score is a softmax, has ids -1 and weights NaN.
  * counts, offsets, perm and inv_perm as moe_plan writes them; ws: moe_score_workspace_bytes.  T, E, k as
  * for moe_route; 1 <= groups <= 64 divides E, 1 <= group_topk <= groups, k <= group_topk * E / groups.
