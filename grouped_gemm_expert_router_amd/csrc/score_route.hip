@@ -120,12 +120,14 @@ __device__ __forceinline__ Slot score_choose_token(const ScoreArgs& p, const flo
     for (int i = 0; i < EPL; ++i) sh[lane + 64 * i] = c[i];
     __builtin_amdgcn_wave_barrier();
     double b1 = -INFINITY, b2 = -INFINITY;
-    if (lane < p.groups)
+    if (lane < p.groups) {
+#pragma unroll 4
       for (int i = 0; i < each; ++i) {
         const double v = sh[lane * each + i];
-        b2 = fmax(b2, fmin(b1, v));
-        b1 = fmax(b1, v);
+        b2 = v > b1 ? b1 : v > b2 ? v : b2;
+        b1 = v > b1 ? v : b1;
       }
+    }
     const double v = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
@@ -190,8 +192,8 @@ __global__ __launch_bounds__(256) void score_choose_kernel(const ScoreArgs p, co
 // within the lane.  A lane keeps its best four in order, and a round of the choice is one maximum over the
 // lanes (in the vector ALU) of their first, whose lane then moves up its others; a lane that has given
 // four takes the next four out of its registers.  (With the best two, most rounds of a wave had a lane to
-// fill up again: 21804x256 in groups 68 us for the whole call.)  The lanes' best two are what a group's
-// value is made of.
+// fill up again: 21804x256 in groups 68 us for the whole call.)  A group's value
+// is made of its best two as they were, without register numbers.
 //
 // An order that fp32 does not settle is found, not guessed, wherever two values that decide something differ
 // by less than what scores can be off.  The chosen and the first left out (and no other could be among them: one
@@ -200,17 +202,22 @@ __global__ __launch_bounds__(256) void score_choose_kernel(const ScoreArgs p, co
 // taken again), or a value that is no ordinary number: the whole token in 64 bits, by the wave.  What a score
 // is off, relative to |c| + max |bias|: sigmoid 4 2^-24 (an exponential with its argument's rounding, a sum, a
 // reciprocal: |x| s (1 - s) < 1/4), softmax 2^-18 (logits up to 60 below the largest), and 2^-20 for the four
-// bits; twice that for two values: below 2^-18 and 2^-16.
+// bits; twice that for two values: below 2^-18 and 2^-16.  A group's value v: two scores' part without the four
+// bits, and |c1| + |c2| <= |v| + 4 max |bias|: for two groups below 2^-20 (2^-15) (|v| + 6 max |bias|).
+//
+// Tokens that are done again wait until the block's others are through: what they need in registers is then
+// no longer kept through the choice (16384x128 22 -> 20 us, 21804x256 in groups 57 -> 52; four waves a block 49).
 //
 // A block takes `seg` tokens, keeps their ids, and gives each pair its rank among the block's pairs of the
 // same expert (each wave a share of the pairs, in order; lanes with the same expert by one ballot per id bit)
 // and each expert its count: the plan's first pass, without reading the ids back.  A batch that is one
 // block's writes the whole plan.
-constexpr int kChooseWaves = 8;
+constexpr int kChooseWaves = 4;
 constexpr int kSegPairs = 2048;   // pairs of a block, at most
 constexpr int kSegments = 1024;   // blocks, at most, that the plan is made of
 constexpr int kOneBlock = 64;     // tokens that one block does by itself
 constexpr float kNone = -3.0e38f; // below every value that counts
+constexpr int kRedo = -2;         // in the place of a token's ids: to be done again
 
 struct SegPlan {
   int seg, S;  // tokens a block; blocks
@@ -320,7 +327,7 @@ __device__ __forceinline__ void rank_candidates(double v, int id, int& rank) {
 }
 
 template <int LPT, int EPL, int EPL64, bool SIG>
-__global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 4 : 2) void score_choose_fast_kernel(
+__global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_choose_fast_kernel(
     const ScoreArgs p, const float* __restrict__ logits, const float* __restrict__ bias, const uint8_t* __restrict__ mask,
     int32_t* __restrict__ ids, float* __restrict__ w, int seg, int32_t* __restrict__ segcnt, uint16_t* __restrict__ ranks,
     int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv_perm) {
@@ -381,7 +388,7 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 4 : 2) void score_ch
       inv = 1.0f / sum;
     }
     float nought = 0.0f;  // NaN once a value is no ordinary number
-    float b1 = kNone, b2 = kNone, b3 = kNone, b4 = kNone;
+    float b1 = kNone, b2 = kNone, b3 = kNone, b4 = kNone, g1 = kNone, g2 = kNone;
     auto insert = [&](float v) __attribute__((always_inline)) {
       b4 = __builtin_amdgcn_fmed3f(b3, b4, v);
       b3 = __builtin_amdgcn_fmed3f(b2, b3, v);
@@ -393,14 +400,16 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 4 : 2) void score_ch
       const float v = (SIG ? __builtin_amdgcn_rcpf(1.0f + __expf(-x[i])) : c[i] * inv) + b[i];
       const bool barred = x[i] == -INFINITY;
       nought = fmaf(barred ? b[i] : v, 0.0f, nought);
-      c[i] = barred ? kNone : __uint_as_float((__float_as_uint(v) & ~15u) | (15 - i));
+      const float u = barred ? kNone : v;
+      g2 = __builtin_amdgcn_fmed3f(g1, g2, u);
+      g1 = fmaxf(g1, u);
+      c[i] = __uint_as_float((__float_as_uint(u) & ~15u) | (15 - i));
       insert(c[i]);
     }
     bool odd = !(nought == 0.0f);  // something for the 64-bit path
-    constexpr float kOff = SIG ? 0x1p-18f : 0x1p-16f;
+    constexpr float kOff = SIG ? 0x1p-18f : 0x1p-16f, kGroupOff = SIG ? 0x1p-20f : 0x1p-15f;
     bool dropped = false;
     if (p.groups > 1) {
-      float g1 = b1, g2 = b2;
       if (lg >= 2) merge_best<1>(g1, g2);
       if (lg >= 4) merge_best<2>(g1, g2);
       if (lg >= 8) merge_best<4>(g1, g2);
@@ -422,7 +431,7 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 4 : 2) void score_ch
       }
       dropped = !alive || rank >= p.group_topk;
       const float least = -lanes_max<LPT>(dropped ? kNone : -v), next = lanes_max<LPT>(dropped && alive ? v : kNone);
-      odd |= next > -1e38f && !(least - next > 2 * kOff * (fabsf(next) + 2 * bm));
+      odd |= next > -1e38f && !(least - next > kGroupOff * (fabsf(next) + 6 * bm));
       if (dropped) b1 = b2 = b3 = b4 = kNone;
     }
     if (!active) b1 = kNone - 1e35f * l;  // one winner in every round, which takes nothing
@@ -498,23 +507,31 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 4 : 2) void score_ch
       z /= p.renorm ? lanes_sum<LPT>(z) : sum;
     }
     q = active ? z * p.scale : 0.0f;
-    // tokens that are done again
-    uint64_t again = __ballot(odd && active);
-    while (again) {
-      const int r = __builtin_ctzll(again) / LPT;
-      again &= LPT == 64 ? 0 : ~(0xFFFFull << (16 * r));
-      const Slot s = score_choose_token<EPL64>(p, logits + (t0 + r0 + r) * p.E, bias, sh_c[wv]);
-      const int sid = LPT == 64 ? s.id : __shfl(s.id, l, 64);
-      const float sw = LPT == 64 ? s.w : __shfl(s.w, l, 64);
-      if (sub == r) {
-        id = sid;
-        q = sw;
-      }
-    }
+    // (a token that is done again gets its ids below)
+    const uint64_t again = __ballot(odd && active);
+    const bool redo = LPT == 64 ? again != 0 : (again >> (16 * sub) & 0xFFFF) != 0;
     if (slot) {
-      ids[t * p.k + l] = id;
-      w[t * p.k + l] = q;
-      sh_ids[local * p.k + l] = id;
+      if (!redo) {
+        ids[t * p.k + l] = id;
+        w[t * p.k + l] = q;
+      }
+      sh_ids[local * p.k + l] = redo ? kRedo : id;
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  // The tokens that are done again: after the others, so that what these need in registers is not kept meanwhile.
+  for (int r0 = wv * TPW; r0 < ntok; r0 += NW * TPW) {
+    uint64_t again = __ballot(l == 0 && r0 + sub < ntok && sh_ids[min(r0 + sub, ntok - 1) * p.k] == kRedo);
+    while (again) {
+      const int local = r0 + __builtin_ctzll(again) / LPT;
+      again &= again - 1;
+      const int64_t t = t0 + local;
+      const Slot s = score_choose_token<EPL64>(p, logits + t * p.E, bias, sh_c[wv]);
+      if (lane < p.k) {
+        ids[t * p.k + lane] = s.id;
+        w[t * p.k + lane] = s.w;
+        sh_ids[local * p.k + lane] = s.id;
+      }
     }
   }
   if (!segcnt && !perm) return;  // the plan is made elsewhere
