@@ -83,17 +83,24 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const void* __restri
 }
 
 // 128 rows x 64 columns a block: thread (r, c) of 32 x 8 holds rows 4r .. 4r+3 of columns 8c .. 8c+7, so
-// that a column's four codes are one word of the transposed row.
+// that a column's four codes are one word of the transposed row.  LDS keeps a column's words with their
+// 16-byte pieces exchanged by the column's thread (8 c + j: piece ^ c), without which four lanes of a store
+// meet in a bank.
+// The rows of codes are padded to 16 tokens only, so that neighbouring blocks along the tokens share lines of
+// 128 bytes: thread blocks are dealt out to the eight L2 caches so that each has a run of neighbours, and a line
+// leaves its cache whole (21804x4096 bf16 79 -> 62 us; 4.4 TB/s, a copy 5.1).
 template <bool F32>
 __global__ __launch_bounds__(256) void quantize_tokens_kernel(const void* __restrict__ src, int64_t ld, int64_t rows,
-                                                              int cols, int64_t r16, int64_t nb,
+                                                              int cols, int64_t r16, int64_t nb, int64_t tiles,
                                                               uint8_t* __restrict__ codes, float* __restrict__ scales) {
   constexpr int LD = 36;  // words of a column in LDS: 32 and padding that keeps 16-byte rows
   __shared__ float sh_max[4][64];
   __shared__ __attribute__((aligned(16))) uint32_t sh[64 * LD];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int64_t tb = blockIdx.x % nb;
-  const int c0 = (int)(blockIdx.x / nb) * 64, cc = tid % 8, rr = tid / 8;
+  const int64_t each = gridDim.x / 8, tile = blockIdx.x % 8 * each + blockIdx.x / 8;
+  if (tile >= tiles) return;
+  const int64_t tb = tile % nb;
+  const int c0 = (int)(tile / nb) * 64, cc = tid % 8, rr = tid / 8;
   const int col = c0 + 8 * cc;
   float v[4][8] = {};
 #pragma unroll
@@ -116,7 +123,7 @@ __global__ __launch_bounds__(256) void quantize_tokens_kernel(const void* __rest
   for (int j = 0; j < 8; ++j) {
     const int c = 8 * cc + j;
     const Scale s = scale_of(fmaxf(fmaxf(sh_max[0][c], sh_max[1][c]), fmaxf(sh_max[2][c], sh_max[3][c])));
-    sh[c * LD + rr] = codes4(v[0][j] * s.factor, v[1][j] * s.factor, v[2][j] * s.factor, v[3][j] * s.factor);
+    sh[c * LD + (rr / 4 ^ cc) * 4 + rr % 4] = codes4(v[0][j] * s.factor, v[1][j] * s.factor, v[2][j] * s.factor, v[3][j] * s.factor);
     if (rr == 0 && col < cols) scales[(int64_t)(col + j) * nb + tb] = s.scale;
   }
   __syncthreads();
@@ -124,7 +131,7 @@ __global__ __launch_bounds__(256) void quantize_tokens_kernel(const void* __rest
   for (int i = 0; i < 2; ++i) {
     const int c = (tid + 256 * i) / 8, q = tid % 8;
     const int64_t at = tb * 128 + 16 * q;
-    if (c0 + c < cols && at < r16) *(uint4*)(codes + (c0 + c) * r16 + at) = *(const uint4*)&sh[c * LD + 4 * q];
+    if (c0 + c < cols && at < r16) *(uint4*)(codes + (c0 + c) * r16 + at) = *(const uint4*)&sh[c * LD + 4 * (q ^ (c / 8 & 7))];
   }
 }
 
@@ -171,8 +178,9 @@ hipError_t quantize(const void* src, int64_t rows, int64_t cols, int64_t ld, int
     const int64_t blocks = rows * nb;
     quantize_rows_kernel<F32><<<(unsigned)((blocks + 15) / 16), 256, 0, st>>>(src, ld, blocks, (int)cols, nb, codes, scales);
   } else if (form == MOE_BLOCK_TOKENS) {
-    const unsigned grid = (unsigned)(rb * ((cols + 63) / 64));
-    quantize_tokens_kernel<F32><<<grid, 256, 0, st>>>(src, ld, rows, (int)cols, (rows + 15) / 16 * 16, rb, codes, scales);
+    const int64_t tiles = rb * ((cols + 63) / 64);
+    quantize_tokens_kernel<F32><<<(unsigned)((tiles + 7) / 8 * 8), 256, 0, st>>>(src, ld, rows, (int)cols, (rows + 15) / 16 * 16, rb,
+                                                                            tiles, codes, scales);
   } else {
     quantize_tiles_kernel<F32><<<(unsigned)(rb * nb), 256, 0, st>>>(src, ld, rows, (int)cols, nb, codes, scales);
   }
