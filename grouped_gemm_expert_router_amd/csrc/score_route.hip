@@ -805,8 +805,119 @@ __global__ __launch_bounds__(256) void score_backward_kernel(const ScoreArgs p, 
     score_backward_token<EPL>(p, logits + t * p.E, ids + t * p.k, d_w + t * p.k, d + t * p.E);
 }
 
+// For k <= 16: four tokens a wave, a row of 16 lanes each, lane j with slot j.  The values are made in 64 bits as
+// above, once for four tokens; the wave's four rows of the gradient, which lie behind one another, are laid out in
+// LDS and written in one piece, 16 bytes a lane, whatever E is.  A softmax that is not renormalised goes through
+// LDS too: its rows' exponentials lie where the gradient comes to lie.  An id that occurs twice in a token gets
+// the sum in slot order, the same in each of its lanes.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ double row16_max_f64(double v) {
+  v = fmax(v, dpp64<0x128, 0xf>(v, v));
+  v = fmax(v, dpp64<0x124, 0xf>(v, v));
+  v = fmax(v, dpp64<0x122, 0xf>(v, v));
+  return fmax(v, dpp64<0x121, 0xf>(v, v));
+}
+__device__ __forceinline__ double row16_sum_f64(double v) {
+  v += dpp64<0x128, 0xf>(0.0, v);
+  v += dpp64<0x124, 0xf>(0.0, v);
+  v += dpp64<0x122, 0xf>(0.0, v);
+  return v + dpp64<0x121, 0xf>(0.0, v);
+}
+
+template <bool SIG, bool DENSE>
+__global__ __launch_bounds__(256) void score_backward_rows_kernel(const ScoreArgs p, const float* __restrict__ logits,
+                                                                  const int32_t* __restrict__ ids,
+                                                                  const float* __restrict__ d_w, float* __restrict__ d) {
+  extern __shared__ __attribute__((aligned(16))) float sh_rows[];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, sub = lane >> 4, l = lane & 15;
+  float* rows = sh_rows + (int64_t)wv * 4 * p.E;
+  float* mine = rows + sub * p.E;
+  const int64_t waves = blockDim.x / 64;
+  for (int64_t t0 = (blockIdx.x * waves + wv) * 4; t0 < p.T; t0 += gridDim.x * waves * 4) {
+    const int ntok = (int)min((int64_t)4, p.T - t0), words = ntok * p.E;
+    const int64_t t = t0 + min(sub, ntok - 1);
+    const float* row = logits + t * p.E;
+    const int id = l < p.k ? ids[t * p.k + l] : -1;
+    const bool there = id >= 0 && id < p.E;
+    const double g = there ? (double)d_w[t * p.k + l] * p.scale : 0.0;
+    const double x = there ? (double)row[id] : 0.0;
+    double m = 0.0, sum = 1.0;
+    if constexpr (DENSE) {
+      float xmax = -INFINITY;
+      for (int i = 4 * lane; i < words; i += 256) {
+        if (i + 4 <= words) {
+          *(f32x4*)(rows + i) = *(const f32x4_u*)(logits + t0 * p.E + i);
+        } else {
+          for (int e = i; e < words; ++e) rows[e] = logits[t0 * p.E + e];
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+      if (sub < ntok) {
+#pragma unroll 4
+        for (int e = l; e < p.E; e += 16) xmax = fmaxf(xmax, mine[e]);
+      }
+      xmax = row16_max(xmax);
+      m = xmax;
+      float part = 0.0f;
+      if (sub < ntok) {
+#pragma unroll 4
+        for (int e = l; e < p.E; e += 16) part += mine[e] = expf(mine[e] - xmax);
+      }
+      sum = row16_sum_f64(part);
+    } else {
+      for (int i = 4 * lane; i < 4 * p.E; i += 256) *(f32x4*)(rows + i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (p.renorm) m = row16_max_f64(there ? (SIG ? fmin(x, 0.0) : x) : -INFINITY);
+    }
+    __builtin_amdgcn_wave_barrier();
+    double q = there ? (SIG ? sigmoid_scaled(x, m) : exp(x - m)) : 0.0;
+    if (p.renorm) sum = row16_sum_f64(q);
+    q = there ? q / sum : 0.0;
+    const double dot = p.renorm || DENSE ? row16_sum_f64(g * q) : 0.0;
+    const float v = there ? (float)(DENSE ? g : SIG ? (g - dot) * q * sigmoid_scaled(-x, 0.0) : (g - dot) * q) : 0.0f;
+    float all = 0.0f;  // over the slots with this id
+    for (int j = 0; j < p.k; ++j) {
+      const float o = __shfl(v, j, 16);
+      if (__shfl(id, j, 16) == id) all += o;
+    }
+    if constexpr (DENSE) {
+      const float total = (float)sum, off = (float)dot;
+      const bool any = (__ballot(there) >> (16 * sub) & 0xFFFF) != 0;
+      const float at = there ? (all - off) * (mine[id] / total) : 0.0f;
+      __builtin_amdgcn_wave_barrier();
+      if (sub < ntok) {
+#pragma unroll 4
+        for (int e = l; e < p.E; e += 16) mine[e] = any ? -off * (mine[e] / total) : 0.0f;
+      }
+      all = at;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (there && sub < ntok) mine[id] = all;
+    __builtin_amdgcn_wave_barrier();
+    float* out = d + t0 * p.E;
+    for (int i = 4 * lane; i < words; i += 256) {
+      if (i + 4 <= words) {
+        *(f32x4_u*)(out + i) = *(const f32x4*)(rows + i);
+      } else {
+        for (int e = i; e < words; ++e) out[e] = rows[e];
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 hipError_t launch_score_backward(const ScoreArgs& p, const float* logits, const int32_t* ids, const float* d_w,
                                  float* d_logits, hipStream_t st) {
+  if (p.k <= 16) {
+    const int waves = p.T <= 4096 ? 1 : 4;  // few tokens: a wave a block, on as many compute units
+    const dim3 grid((token_grid(p.T) + waves - 1) / waves), block(64 * waves);
+    const size_t lds = waves * 4 * (size_t)p.E * sizeof(float);
+    if (p.sigmoid) score_backward_rows_kernel<true, false><<<grid, block, lds, st>>>(p, logits, ids, d_w, d_logits);
+    else if (p.renorm) score_backward_rows_kernel<false, false><<<grid, block, lds, st>>>(p, logits, ids, d_w, d_logits);
+    else score_backward_rows_kernel<false, true><<<grid, block, lds, st>>>(p, logits, ids, d_w, d_logits);
+    return hipGetLastError();
+  }
   const dim3 grid(token_grid(p.T)), block(256);
   if (p.E <= 64) score_backward_kernel<1><<<grid, block, 0, st>>>(p, logits, ids, d_w, d_logits);
   else if (p.E <= 128) score_backward_kernel<2><<<grid, block, 0, st>>>(p, logits, ids, d_w, d_logits);
