@@ -5,6 +5,7 @@
 // kernele", section "Mit csinált a Prime Intellect?").
 #include <type_traits>
 
+
 #include "common.hpp"
 #include "gemm_common.hpp"
 #include "kernels.hpp"
@@ -105,19 +106,17 @@ __device__ __forceinline__ void store4(const MatmulArgs& g, int64_t at, float (&
 //
 // B [N, K]: 16 NF columns a thread block, whose eight waves take the blocks of K in turn, U at a time.
 // B [K, N]: 128 columns, one cache line, and four waves; the LDS transpose read makes the operands.
-constexpr int kFewRows = 16;
-
-template <bool KN, bool ROWS, bool WHOLE, int MF, int NF, int U, int CW>
+template <bool KN, bool ROWS, bool WHOLE, int MF, int NF, int U>
 __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g, float* __restrict__ part,
                                                                         int per) {
-  constexpr int KW = 8 / CW;           // waves that share K; CW of them stand side by side
-  constexpr int BLK = 2048 * NF;       // bytes of a block of K
+  constexpr int KW = 8;                // waves, which share K
+  constexpr bool AL = MF > 1;          // A by way of LDS too
+  constexpr int B_BLK = 2048 * NF, BLK = B_BLK + (AL ? 2048 * MF : 0);  // bytes of a block of K
   static_assert(!KN || !ROWS, "");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[8 * U * BLK];
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kw = wave / CW;
-  const int64_t nblk = (int64_t)xcd_remap(blockIdx.x, gridDim.x) * (16 * NF * CW), n0 = nblk + 16 * NF * (wave % CW);
+  const int64_t n0 = (int64_t)xcd_remap(blockIdx.x, gridDim.x) * (16 * NF);
   const int KB = (int)((g.K + 127) / 128);
   const int64_t NB = (g.N + 127) / 128;
   const int kb0 = blockIdx.y * per, kb1 = min(KB, kb0 + per);
@@ -153,9 +152,16 @@ __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g,
       }
       dma16(src, mine + u * BLK + 1024 * j);
     }
+    if constexpr (AL) {
+#pragma unroll
+      for (int j = 0; j < 2 * MF; ++j) {
+        const int r = 8 * j + (lane >> 3), c = (lane & 7) ^ ((r >> 1) & 7);
+        dma16(g.A + min((int64_t)r, g.M - 1) * g.lda + min(k0 + 16 * c, g.K - 16), mine + u * BLK + B_BLK + 1024 * j);
+      }
+    }
   };
   struct Row {
-    i32x8 a[MF];
+    i32x8 a[AL ? 1 : MF];
     float sa[MF], sb[ROWS ? 4 * NF : KN ? 1 : NF];
   };
   // the 32 bytes of K that lane l has of its row: 16-byte pieces q and q + 4 of the block
@@ -163,10 +169,12 @@ __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g,
     const int64_t k0 = (int64_t)kb * 128 + 16 * q;
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
-      u32x4 lo = {}, hi = {};
-      if (k0 < g.K) lo = *(const u32x4*)(a_row[i] + k0);
-      if (k0 + 64 < g.K) hi = *(const u32x4*)(a_row[i] + k0 + 64);
-      c.a[i] = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+      if constexpr (!AL) {
+        u32x4 lo = {}, hi = {};
+        if (k0 < g.K) lo = *(const u32x4*)(a_row[i] + k0);
+        if (k0 + 64 < g.K) hi = *(const u32x4*)(a_row[i] + k0 + 64);
+        c.a[i] = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+      }
       c.sa[i] = a_scale[i][kb];
     }
     if constexpr (KN) {
@@ -187,6 +195,27 @@ __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g,
   auto add = [&](const Row& c, int kb, int u) __attribute__((always_inline)) {
     const uint32_t base = mine + u * BLK;
     const int64_t left = g.K - (int64_t)kb * 128 - 16 * q;  // codes of K from the lane's first on
+    auto pieces = [&](uint32_t at, int row) __attribute__((always_inline)) {
+      const u32x4 lo = *(const LDS_AS u32x4*)(uintptr_t)(at + km_off<64>(row, q));
+      const u32x4 hi = *(const LDS_AS u32x4*)(uintptr_t)(at + km_off<64>(row, q + 4));
+      return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    // the last block: a NaN code would outlive the other operand's zero
+    auto clear = [&](i32x8& v) __attribute__((always_inline)) {
+#pragma unroll
+      for (int w = 0; w < 8; ++w)
+        if (left <= 64 * (w >> 2)) v[w] = 0;
+    };
+    i32x8 a[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      if constexpr (AL) {
+        a[i] = pieces(base + B_BLK, 16 * i + l16);
+        clear(a[i]);
+      } else {
+        a[i] = c.a[i];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
       i32x8 b;
@@ -202,23 +231,18 @@ __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g,
           b[2 * h + 1] = t.y;
         }
       } else {
-        const u32x4 lo = *(const LDS_AS u32x4*)(uintptr_t)(base + km_off<64>(16 * j + l16, q));
-        const u32x4 hi = *(const LDS_AS u32x4*)(uintptr_t)(base + km_off<64>(16 * j + l16, q + 4));
-        b = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+        b = pieces(base, 16 * j + l16);
       }
-      // the last block: a NaN code would outlive A's zero
-#pragma unroll
-      for (int w = 0; w < 8; ++w)
-        if (left <= 64 * (w >> 2)) b[w] = 0;
+      clear(b);
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
-        const f32x4_t t = multiply16<WHOLE>(b, c.a[i]);
+        const f32x4_t t = multiply16<WHOLE>(b, a[i]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(t[r], c.sa[i] * c.sb[ROWS ? 4 * j + r : KN ? 0 : j], acc[i][j][r]);
       }
     }
   };
-  for (int kb = kb0 + kw; kb < kb1; kb += KW * U) {
+  for (int kb = kb0 + wave; kb < kb1; kb += KW * U) {
     lds_wait();  // the wave's reads of what it now overwrites
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -234,7 +258,7 @@ __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g,
   }
   // Lane l holds columns 4q .. 4q+3 of row l % 16 of each 16 x 16 piece.  Sixteen rows at a time.
   float4* red = (float4*)smem;
-  constexpr int UNITS = CW * NF * 64;
+  constexpr int UNITS = NF * 64;
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
     __syncthreads();
@@ -249,7 +273,7 @@ __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g,
         const float4 a = red[k * UNITS + u];
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
       }
-      const int64_t m = 16 * i + (u & 15), n = nblk + 16 * (u >> 6) + 4 * ((u & 63) >> 4);
+      const int64_t m = 16 * i + (u & 15), n = n0 + 16 * (u >> 6) + 4 * ((u & 63) >> 4);
       if (m >= g.M || n >= g.N) continue;
       if (part) *(float4*)(part + ((int64_t)blockIdx.y * g.M + m) * g.N + n) = make_float4(v[0], v[1], v[2], v[3]);
       else store4<WHOLE>(g, m * g.ldc + n, v);
@@ -257,21 +281,31 @@ __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g,
   }
 }
 
+// What was cut along K: the tiles from `first` on, each held `splits` times as [bm][bn] in fp32.
+struct Cut {
+  int64_t first, tiles;  // the tile number the cut ones start at; how many there are
+  int splits, per;       // parts; blocks of K a part
+  int64_t bm, bn;
+  int nM, nN, gm;
+};
+
 // The sums of the parts of K, in order; four values a thread.
 template <bool F32>
-__global__ __launch_bounds__(256) void fp8_matmul_sum_kernel(const MatmulArgs g, const float* __restrict__ part,
-                                                             int splits) {
-  const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (u * 4 >= g.M * g.N) return;
-  const int64_t m = u * 4 / g.N, n = u * 4 - m * g.N;
+__global__ __launch_bounds__(256) void fp8_matmul_sum_kernel(const MatmulArgs g, const float* __restrict__ part, const Cut cut) {
+  const int64_t u = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, size = cut.bm * cut.bn, tile = u / size;
+  if (tile >= cut.tiles) return;
+  const int2 at = grouped_tile((int)(cut.first + tile), cut.nM, cut.nN, cut.gm);
+  const int64_t r = (u - tile * size) / cut.bn, c = u - tile * size - r * cut.bn;
+  const int64_t m = at.x * cut.bm + r, n = at.y * cut.bn + c;
+  if (m >= g.M || n >= g.N) return;
   float v[4] = {};
-  for (int s0 = 0; s0 < splits; s0 += 8) {  // eight loads in flight
+  for (int s0 = 0; s0 < cut.splits; s0 += 8) {  // eight loads in flight
     float4 a[8];
 #pragma unroll
-    for (int s = 0; s < 8; ++s) a[s] = *(const float4*)(part + min(s0 + s, splits - 1) * g.M * g.N + u * 4);
+    for (int s = 0; s < 8; ++s) a[s] = *(const float4*)(part + min(s0 + s, cut.splits - 1) * cut.tiles * size + u);
 #pragma unroll
     for (int s = 0; s < 8; ++s)
-      if (s0 + s < splits) v[0] += a[s].x, v[1] += a[s].y, v[2] += a[s].z, v[3] += a[s].w;
+      if (s0 + s < cut.splits) v[0] += a[s].x, v[1] += a[s].y, v[2] += a[s].z, v[3] += a[s].w;
   }
   store4<F32>(g, m * g.ldc + n, v);
 }
@@ -314,8 +348,7 @@ __device__ __forceinline__ const T* uniform_ptr(const T* p) {
 // Each 32 x 32 block of C is held transposed (B is the MFMA's first operand): lane l has row l % 32 and 16
 // columns, so one A scale serves its 16 values.
 template <int FORM, bool WHOLE, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN, 1) void fp8_matmul_tile_kernel(const MatmulArgs g, float* __restrict__ part, int per,
-                                                                          int gm) {
+__global__ __launch_bounds__(64 * WM * WN, 1) void fp8_matmul_tile_kernel(const MatmulArgs g, float* __restrict__ part, const Cut cut) {
   constexpr bool KN = FORM == MOE_B_KN, ROWS = FORM == MOE_B_NK_ROWS;
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32, BK = 128;
   constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
@@ -331,12 +364,16 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void fp8_matmul_tile_kernel(const 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr_of(smem)), sc0 = lds0 + S * STAGE, sb0 = sc0 + NSC * SC;
-  const int nM = (int)((g.M + BM - 1) / BM), nN = (int)((g.N + BN - 1) / BN);
-  const int2 tile = grouped_tile(xcd_remap(blockIdx.x, gridDim.x), nM, nN, gm);
+  const int KB = (int)((g.K + 127) / 128), NB = (int)((g.N + 127) / 128);
+  // tiles whole along K, then those that are cut
+  const bool whole_tile = (int64_t)blockIdx.x < cut.first;
+  const int nth = whole_tile ? xcd_remap(blockIdx.x, (int)cut.first)
+                             : xcd_remap(blockIdx.x - (int)cut.first, gridDim.x - (int)cut.first);
+  const int of_tile = whole_tile ? nth : nth / cut.splits, of_k = whole_tile ? 0 : nth - of_tile * cut.splits;
+  const int kb0 = whole_tile ? 0 : of_k * cut.per, nk = whole_tile ? KB : min(KB - kb0, cut.per);
+  const int2 tile = grouped_tile(whole_tile ? of_tile : (int)cut.first + of_tile, cut.nM, cut.nN, cut.gm);
   const int64_t m0 = (int64_t)tile.x * BM, n0 = (int64_t)tile.y * BN;
   const int mrows = (int)min((int64_t)BM, g.M - m0), ncols = (int)min((int64_t)BN, g.N - n0);
-  const int KB = (int)((g.K + 127) / 128), NB = (int)((g.N + 127) / 128);
-  const int kb0 = blockIdx.y * per, nk = min(KB - kb0, per);
 
   // ------------------------------------------------------------------ DMA sources
   // DMA q of a wave: eight rows of 128 bytes (a [K, N] operand: 1024 / BN rows of BN bytes).  Rows and columns
@@ -596,7 +633,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void fp8_matmul_tile_kernel(const 
         const int col = wn * TN + 32 * j + 2 * r + 4 * (lane >> 5);
         if (col >= ncols) continue;
         float v[4] = {acc[i][j][r], acc[i][j][r + 1], acc[i][j][r + 2], acc[i][j][r + 3]};
-        if (part) *(float4*)(part + ((int64_t)blockIdx.y * g.M + row) * g.N + n0 + col) = make_float4(v[0], v[1], v[2], v[3]);
+        if (!whole_tile && cut.splits > 1)
+          *(float4*)(part + ((of_k * cut.tiles + of_tile) * BM + lr) * BN + col) = make_float4(v[0], v[1], v[2], v[3]);
         else store4<WHOLE>(g, row * g.ldc + n0 + col, v);
       }
   }
@@ -604,106 +642,140 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void fp8_matmul_tile_kernel(const 
 
 namespace {
 
-// Few rows: columns of a thread block, and the parts of K (`per` blocks of 128 each) that make their
-// number fill the card.
+constexpr int kCus = 256;
+
+// Few rows: 16 of them with any B, 48 with a B [N, K] (48x7168x2048 8.5 us, in tiles 11.7; 48x4096x8192 13.2 and
+// 14.3; 40x2048x16384 15.1 and 14.4; a 64th row's operands no longer fit twice into a compute unit: 64x7168x4096
+// 16.5 and 14.3).
+bool is_few(const MatmulArgs& g) { return g.M <= (g.b_form == MOE_B_KN ? 16 : 48); }
+// A short K with B [K, N]: 32 columns a thread block and no parts of K (1x2048x1024 3.0 us against 4.6 in 128
+// columns, 1x2048x2048 5.8 and 7.3, 1x7168x2048 8.9 and 9.2); a long one takes whole lines of B
+// (1x4096x7168 11.1 us against 14.2).
+constexpr int kShortK = 2048;
+// Columns of a thread block, and the parts of K (`per` blocks of 128 each) that make their number fill the card.
 struct FewPlan {
-  int nf;
   int64_t groups;
   int per, splits;
 };
-#ifndef WANT
-#define WANT 256
-#define NFS 1
-#define CWK 2
-#endif
 FewPlan few_plan(const MatmulArgs& g) {
   FewPlan f;
-  const int KB = (int)((g.K + 127) / 128);
-  const bool wide = g.b_form == MOE_B_KN;
-  f.nf = wide ? 8 * CWK : g.M <= 16 ? NFS : 2;
-  f.groups = (g.N + 16 * f.nf - 1) / (16 * f.nf);
-  const int waves = wide ? 8 / CWK : 8;
-  const int64_t want = (WANT + f.groups - 1) / f.groups;
-  f.per = (int)((KB + want - 1) / want);
-  f.per = (f.per + waves - 1) / waves * waves;
+  const int KB = (int)((g.K + 127) / 128), cols = g.b_form != MOE_B_KN ? 16 : g.K <= kShortK ? 32 : 128;
+  f.groups = (g.N + cols - 1) / cols;
+  f.per = KB;
+  if (g.K > kShortK) {
+    const int64_t want = (kCus + f.groups - 1) / f.groups;
+    f.per = (int)((KB + want - 1) / want);
+    f.per = (f.per + 7) / 8 * 8;  // a block of K for each of the eight waves
+  }
   f.splits = (KB + f.per - 1) / f.per;
   return f;
 }
 
-template <bool KN, bool ROWS, bool WHOLE>
+template <bool WHOLE>
+void launch_sum(const MatmulArgs& g, const float* part, const Cut& cut, hipStream_t st) {
+  const int64_t units = cut.tiles * cut.bm * cut.bn / 4;
+  fp8_matmul_sum_kernel<WHOLE><<<(unsigned)((units + 255) / 256), 256, 0, st>>>(g, part, cut);
+}
+
+template <int FORM, bool WHOLE>
 void launch_few_form(const MatmulArgs& g, const FewPlan& f, float* part, hipStream_t st) {
   const dim3 grid((unsigned)f.groups, (unsigned)f.splits), block(512);
-  if constexpr (KN) fp8_matmul_few_kernel<KN, ROWS, WHOLE, 1, 8, 1, 2><<<grid, block, 0, st>>>(g, part, f.per);
-  else fp8_matmul_few_kernel<KN, ROWS, WHOLE, 1, 1, 4, 1><<<grid, block, 0, st>>>(g, part, f.per);
+  if constexpr (FORM == MOE_B_KN) {
+    if (g.K <= kShortK) fp8_matmul_few_kernel<true, false, WHOLE, 1, 2, 2><<<grid, block, 0, st>>>(g, part, f.per);
+    else fp8_matmul_few_kernel<true, false, WHOLE, 1, 8, 1><<<grid, block, 0, st>>>(g, part, f.per);
+  } else {
+    constexpr bool ROWS = FORM == MOE_B_NK_ROWS;
+    if (g.M <= 16) fp8_matmul_few_kernel<false, ROWS, WHOLE, 1, 1, 4><<<grid, block, 0, st>>>(g, part, f.per);
+    else if (g.M <= 32) fp8_matmul_few_kernel<false, ROWS, WHOLE, 2, 1, 1><<<grid, block, 0, st>>>(g, part, f.per);
+    else fp8_matmul_few_kernel<false, ROWS, WHOLE, 3, 1, 1><<<grid, block, 0, st>>>(g, part, f.per);
+  }
 }
 
 template <bool WHOLE>
 void launch_few(const MatmulArgs& g, float* ws, hipStream_t st) {
   const FewPlan f = few_plan(g);
   float* part = f.splits > 1 ? ws : nullptr;
-  if (g.b_form == MOE_B_KN) launch_few_form<true, false, WHOLE>(g, f, part, st);
-  else if (g.b_form == MOE_B_NK) launch_few_form<false, false, WHOLE>(g, f, part, st);
-  else launch_few_form<false, true, WHOLE>(g, f, part, st);
-  if (part)
-    fp8_matmul_sum_kernel<WHOLE><<<(unsigned)((g.M * g.N / 4 + 255) / 256), 256, 0, st>>>(g, part, f.splits);
+  if (g.b_form == MOE_B_KN) launch_few_form<MOE_B_KN, WHOLE>(g, f, part, st);
+  else if (g.b_form == MOE_B_NK) launch_few_form<MOE_B_NK, WHOLE>(g, f, part, st);
+  else launch_few_form<MOE_B_NK_ROWS, WHOLE>(g, f, part, st);
+  if (part) launch_sum<WHOLE>(g, part, Cut{0, 1, f.splits, f.per, g.M, g.N, 1, 1, 1}, st);
 }
 
-// Tiles: rows, columns, parts of K.
-struct TilePlan {
-  int bm, bn;
-  int per, splits;
+// The shapes of tiles, what a step (128 of K) of a full card of them takes in ns, and where two fit a compute unit,
+// also of one each (measured: 4096x4096x4096 and 7168x4096x21808 in every shape, 2048x2048x7168 for the last).
+struct Shape {
+  int bm, bn, per_cu, step, step_alone;
 };
-TilePlan tile_plan(const MatmulArgs& g) {
-  TilePlan f;
+constexpr Shape kShapes[2][4] = {{{256, 256, 1, 2080, 2080}, {256, 128, 1, 1330, 1330}, {128, 128, 2, 1320, 930}, {64, 128, 2, 900, 600}},
+                                 {{256, 128, 1, 2250, 2250}, {128, 128, 2, 2500, 1750}, {64, 128, 2, 1300, 900}, {0, 0, 0, 0, 0}}};
+
+// The shape, and into how many parts of K the tiles behind the last full card are cut, by the time that the steps
+// take, 3 us for each round of tiles, and 3 us and both ways of the parts' bytes at 5 TB/s for the sums:
+// 21804x4096x7168, 1376 tiles of 256 x 256: 96 cut in two, 5.5 rounds instead of 6 (650 -> 640 us); 7168x4096x21808 in fp32, 896 of
+// 256 x 128: 128 cut in two, 3.5 instead of 4 (1434 -> 1351 us).
+Cut tile_plan(const MatmulArgs& g) {
   const int KB = (int)((g.K + 127) / 128);
-  auto tiles = [&](int bm, int bn) { return (g.M + bm - 1) / bm * ((g.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192) {
-    f.bm = 256;
-    f.bn = g.c_f32 ? 128 : 256;
-  } else {
-    f.bm = g.M <= 64 ? 64 : 128;
-    f.bn = 128;
+  Cut best{};
+  double least = 0.0;
+  for (const Shape& sh : kShapes[g.c_f32]) {
+    if (sh.bm == 0) continue;
+    Cut c{};
+    c.bm = sh.bm, c.bn = sh.bn, c.gm = 8;
+    c.nM = (int)((g.M + sh.bm - 1) / sh.bm), c.nN = (int)((g.N + sh.bn - 1) / sh.bn);
+    const int64_t all = (int64_t)c.nM * c.nN, slots = kCus * sh.per_cu, rem = all % slots;
+    const double full = (double)(all / slots) * ((double)KB * sh.step + 3e3);
+    for (int want = 1; want == 1 || (want * rem <= slots && KB >= 4 * want); ++want) {
+      c.per = (KB + want - 1) / want;
+      c.splits = (KB + c.per - 1) / c.per;
+      c.tiles = c.splits > 1 ? rem : 0;
+      c.first = all - c.tiles;
+      double t = full;
+      if (rem > 0) {  // between one and two a compute unit: between both times
+        const double two = rem * c.splits > kCus ? (double)(rem * c.splits - kCus) / kCus : 0.0;
+        t += c.per * (sh.step_alone + two * (sh.step - sh.step_alone)) + 3e3;
+      }
+      if (c.tiles > 0) t += 3e3 + (double)(c.tiles * c.splits) * sh.bm * sh.bn * 8 / 5e3;
+      if (least == 0.0 || t < least) least = t, best = c;
+      if (rem == 0) break;
+    }
   }
-  f.per = KB;
-  if (f.bm < 256) {
-    const int64_t want = (256 + tiles(f.bm, f.bn) - 1) / tiles(f.bm, f.bn);
-    f.per = (int)((KB + want - 1) / want);
-    if (f.per < 4) f.per = KB < 4 ? KB : 4;
-  }
-  f.splits = (KB + f.per - 1) / f.per;
-  return f;
+  return best;
 }
 
 template <int FORM, bool WHOLE>
-void launch_tiles_form(const MatmulArgs& g, const TilePlan& f, float* part, hipStream_t st) {
-  const dim3 grid((unsigned)((g.M + f.bm - 1) / f.bm * ((g.N + f.bn - 1) / f.bn)), (unsigned)f.splits);
-  if (f.bm == 256 && WHOLE) fp8_matmul_tile_kernel<FORM, true, 256, 128, 4, 2, 2><<<grid, 512, 0, st>>>(g, part, f.per, 8);
-  else if (f.bm == 256) fp8_matmul_tile_kernel<FORM, false, 256, 256, 2, 4, 2><<<grid, 512, 0, st>>>(g, part, f.per, 8);
-  else if (f.bm == 128) fp8_matmul_tile_kernel<FORM, WHOLE, 128, 128, 2, 2, 3><<<grid, 256, 0, st>>>(g, part, f.per, 8);
-  else fp8_matmul_tile_kernel<FORM, WHOLE, 64, 128, 2, 2, 4><<<grid, 256, 0, st>>>(g, part, f.per, 8);
+void launch_tiles_form(const MatmulArgs& g, const Cut& c, float* part, hipStream_t st) {
+  const unsigned grid = (unsigned)(c.first + c.tiles * c.splits);
+  if (c.bm == 256 && c.bn == 128) fp8_matmul_tile_kernel<FORM, WHOLE, 256, 128, 4, 2, 2><<<grid, 512, 0, st>>>(g, part, c);
+  else if (c.bm == 256) {
+    if constexpr (!WHOLE) fp8_matmul_tile_kernel<FORM, false, 256, 256, 2, 4, 2><<<grid, 512, 0, st>>>(g, part, c);
+  }
+  else if (c.bm == 128) fp8_matmul_tile_kernel<FORM, WHOLE, 128, 128, 2, 2, 2><<<grid, 256, 0, st>>>(g, part, c);
+  else fp8_matmul_tile_kernel<FORM, WHOLE, 64, 128, 2, 2, FORM == MOE_B_NK_ROWS ? 2 : 3><<<grid, 256, 0, st>>>(g, part, c);
 }
 
 template <bool WHOLE>
 void launch_tiles(const MatmulArgs& g, float* ws, hipStream_t st) {
-  const TilePlan f = tile_plan(g);
-  float* part = f.splits > 1 ? ws : nullptr;
-  if (g.b_form == MOE_B_KN) launch_tiles_form<MOE_B_KN, WHOLE>(g, f, part, st);
-  else if (g.b_form == MOE_B_NK) launch_tiles_form<MOE_B_NK, WHOLE>(g, f, part, st);
-  else launch_tiles_form<MOE_B_NK_ROWS, WHOLE>(g, f, part, st);
-  if (part)
-    fp8_matmul_sum_kernel<WHOLE><<<(unsigned)((g.M * g.N / 4 + 255) / 256), 256, 0, st>>>(g, part, f.splits);
+  const Cut c = tile_plan(g);
+  if (g.b_form == MOE_B_KN) launch_tiles_form<MOE_B_KN, WHOLE>(g, c, ws, st);
+  else if (g.b_form == MOE_B_NK) launch_tiles_form<MOE_B_NK, WHOLE>(g, c, ws, st);
+  else launch_tiles_form<MOE_B_NK_ROWS, WHOLE>(g, c, ws, st);
+  if (c.tiles > 0) launch_sum<WHOLE>(g, ws, c, st);
 }
 
 }  // namespace
 
 size_t fp8_matmul_ws_bytes(const MatmulArgs& g) {
   if (g.M == 0) return 0;
-  const int splits = g.M <= kFewRows ? few_plan(g).splits : tile_plan(g).splits;
-  return splits > 1 ? (size_t)splits * g.M * g.N * sizeof(float) : 0;
+  if (is_few(g)) {
+    const int splits = few_plan(g).splits;
+    return splits > 1 ? (size_t)splits * g.M * g.N * sizeof(float) : 0;
+  }
+  const Cut c = tile_plan(g);
+  return (size_t)(c.tiles * c.splits * c.bm * c.bn) * sizeof(float);
 }
 
 hipError_t launch_fp8_matmul(const MatmulArgs& g, void* ws, hipStream_t st) {
-  if (g.M <= kFewRows) {
+  if (is_few(g)) {
     if (g.c_f32) launch_few<true>(g, (float*)ws, st);
     else launch_few<false>(g, (float*)ws, st);
   } else {
