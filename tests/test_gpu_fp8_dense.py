@@ -232,6 +232,21 @@ def test_product_large(case):
     check_exact(M, N, K, form, BF16 if M % 2 else F32, 5, add=M % 3 == 0)
 
 
+# tiles of every shape: whole ones, all of them cut along K, and a card full of whole ones with cut ones behind; a
+# stop of K inside a block where a part ends there; rows and columns that end inside a tile
+TILES = [(128, 4096, 3100), (300, 8192, 8192), (1023, 4104, 1040), (1500, 2048, 4096), (4099, 4096, 2064), (4100, 4112, 1024),
+         (2100, 8192, 1936), (2048, 2048, 7168), (700, 512, 20000), (33000, 272, 656)]
+
+
+@pytest.mark.parametrize("form", sorted(B_FORMS))
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_product_tiles(form, dtype):
+    for M, N, K in TILES:
+        N, K = up(N, 16), up(K, 16)
+        print(f"[case] product {form} {M}x{N}x{K}", flush=True)
+        check_exact(M, N, K, form, dtype, N, pad=M % 2, add=M % 4 == 0)
+
+
 def test_product_nan_and_infinite_scales_stay_in_their_rows():
     M, N, K = 70, 144, 272
     for form in B_FORMS:
