@@ -312,9 +312,9 @@ __device__ __forceinline__ void rank_groups(float v, int& rank) {
   }
 }
 
-// Places of 16 lanes' values in descending order; equal ones by id.
+// Places of 16 lanes' values in descending order; equal ones by id.  near: another value within 2^-40, but not equal.
 template <int kRot>
-__device__ __forceinline__ void rank_candidates(double v, int id, int& rank) {
+__device__ __forceinline__ void rank_candidates(double v, int id, int& rank, bool& near) {
   if constexpr (kRot < 16) {
     auto turn = [](int w) __attribute__((always_inline)) {
       return __builtin_amdgcn_update_dpp(w, w, 0x120 + kRot, 0xf, 0xf, true);
@@ -322,7 +322,8 @@ __device__ __forceinline__ void rank_candidates(double v, int id, int& rank) {
     const double o = __hiloint2double(turn(__double2hiint(v)), turn(__double2loint(v)));
     const int oid = turn(id);
     rank += o > v || (o == v && oid < id);
-    rank_candidates<kRot + 1>(v, id, rank);
+    near |= o != v && fabs(o - v) < 0x1p-40;
+    rank_candidates<kRot + 1>(v, id, rank, near);
   }
 }
 
@@ -486,7 +487,9 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
         v = SIG ? sigmoid_scaled(x1, 0.0) + (bias ? (double)bias[mine] : 0.0) : x1;
       }
       int rank = 0;
-      rank_candidates<1>(v, mine, rank);
+      bool near = false;
+      rank_candidates<1>(v, mine, rank, near);
+      if constexpr (!SIG) odd |= near && active && l < keep;  // logits whose scores may be equal in 64 bits
       if (active && l < keep) cand[rank] = mine;
       if (active && l < keep) mine = min(cand[l], p.E - 1);
     }

@@ -153,6 +153,19 @@ def test_bad_values(E, groups):
     assert (got["ids"][:, 0] == E // 2).all()
 
 
+@pytest.mark.parametrize("sigmoid", [True, False], ids=["sigmoid", "softmax"])
+def test_logits_whose_scores_are_equal_in_64_bits(sigmoid):
+    """Logits that differ while their scores do not: tiny ones, and far ones whose scores underflow."""
+    rng = np.random.default_rng(8)
+    for E, k in ((32, 6), (128, 8), (256, 8), (512, 4)):
+        x = (rng.standard_normal((40, E)) * 2.0 ** rng.integers(-126, -40, (40, E))).astype(np.float32)
+        x[:, 5] = 3.0
+        x[20:30, ::3] = rng.standard_normal((10, x[:, ::3].shape[1])).astype(np.float32) * np.float32(2.0 ** -30)
+        x[30:, 7:] = -np.abs(rng.standard_normal((10, E - 7)).astype(np.float32)) * 100 - 900
+        check_route(x, k, sigmoid, True)
+        check_route(x, k, sigmoid, False, bias=np.zeros(E, np.float32))
+
+
 def test_far_logits():
     """Scores that underflow or saturate in 32 bits, and in 64: weights stay quotients."""
     x = np.stack([np.linspace(-80, 80, 16), np.linspace(-120, -90, 16), np.linspace(30, 36, 16), np.linspace(-900, -800, 16),
