@@ -444,7 +444,8 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
     for (int j = 0; j <= keep; ++j) {
       const float m = lanes_max<LPT>(b1);
       const bool win = b1 == m;
-      several |= __popcll(__ballot(win)) != TPW;
+      const uint64_t won = __ballot(win);
+      if (__popcll(won) != TPW) several |= LPT == 64 || __popcll(won >> (16 * sub) & 0xFFFF) != 1;
       last = m;
       if (j == keep) break;
       if (l == j) mine_v = m;
