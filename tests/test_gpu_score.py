@@ -153,6 +153,23 @@ def test_bad_values(E, groups):
     assert (got["ids"][:, 0] == E // 2).all()
 
 
+@pytest.mark.parametrize("E", [132, 160, 256])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+def test_few_tokens(T, E):
+    rng = np.random.default_rng(T + E)
+    bias, mask = (rng.standard_normal(E) * 0.05).astype(np.float32), (rng.random(T) < 0.7).astype(np.uint8)
+    for groups, keep, best in ((1, 1, 1), (2, 1, 2), (4, 3, 1), (4, 2, 2), (8, 4, 2), (16, 5, 2)):
+        if E % groups:
+            continue
+        for k in (1, 8, 16):
+            if k > E // groups * keep:
+                continue
+            for sigmoid in (True, False):
+                x = draw(T, E, T + k)
+                check_route(x, k, sigmoid, k > 1, 2.5, bias, mask, groups, keep, best)
+                check_route(np.round(x * 2) / np.float32(2), k, sigmoid, k > 1, 1.0, None, None, groups, keep, best)
+
+
 @pytest.mark.parametrize("sigmoid", [True, False], ids=["sigmoid", "softmax"])
 def test_logits_whose_scores_are_equal_in_64_bits(sigmoid):
     """Logits that differ while their scores do not: tiny ones, and far ones whose scores underflow."""
