@@ -215,7 +215,7 @@ __global__ __launch_bounds__(256) void score_choose_kernel(const ScoreArgs p, co
 constexpr int kChooseWaves = 4;
 constexpr int kSegPairs = 2048;   // pairs of a block, at most
 constexpr int kSegments = 1024;   // blocks, at most, that the plan is made of
-constexpr int kOneBlock = 64;     // tokens that one block does by itself
+constexpr int kOneBlock = 32;     // tokens that one block does by itself (64x256: 20 us, 17.7 in two blocks)
 constexpr float kNone = -3.0e38f; // below every value that counts
 constexpr int kRedo = -2;         // in the place of a token's ids: to be done again
 

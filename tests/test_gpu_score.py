@@ -154,7 +154,7 @@ def test_bad_values(E, groups):
 
 
 @pytest.mark.parametrize("E", [132, 160, 256])
-@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 31, 32, 33, 65])
 def test_few_tokens(T, E):
     rng = np.random.default_rng(T + E)
     bias, mask = (rng.standard_normal(E) * 0.05).astype(np.float32), (rng.random(T) < 0.7).astype(np.uint8)
