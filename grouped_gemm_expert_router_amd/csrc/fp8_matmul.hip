@@ -97,15 +97,16 @@ __device__ __forceinline__ void store4(const MatmulArgs& g, int64_t at, float (&
 }  // namespace
 
 // ------------------------------------------------------------------------------------ few rows
-// Up to 16 rows: the product is a reading of B.  A wave takes whole blocks of K (128 deep) of a few
-// columns, its own ones, so that no wave waits for another until the end: B by DMA into LDS of the
-// wave's own, whole cache lines a row (a load that takes 64 bytes of 16 rows ran at half the rate), A's
-// rows into registers from L2.  The waves' sums meet in LDS in a fixed order; where the columns alone
-// give too few thread blocks, K is cut once more over `splits` of them, whose fp32 sums
-// fp8_matmul_sum_kernel adds in order.
+// The product of few rows is a reading of B.  A wave takes whole blocks of K (128 deep) of a few columns, its own
+// ones, so that no wave waits for another until the end: B by DMA into LDS of the wave's own, whole cache
+// lines a row (a load that takes 64 bytes of 16 rows ran at half the rate).  Up to 16 rows of A go into registers
+// from L2; more of them through the wave's LDS as well (48x7168x2048: 8.5 us, from L2 into registers 15.5).  The
+// waves' sums meet in LDS in a fixed order; where the columns alone give too few thread blocks, K is cut once
+// more over `splits` of them, whose fp32 sums fp8_matmul_sum_kernel adds in order.
 //
-// B [N, K]: 16 NF columns a thread block, whose eight waves take the blocks of K in turn, U at a time.
-// B [K, N]: 128 columns, one cache line, and four waves; the LDS transpose read makes the operands.
+// B [N, K]: 16 columns a thread block, whose eight waves take the blocks of K in turn, U at a time.
+// B [K, N]: 16 NF columns, 128 (one cache line) where K is long; the LDS transpose read makes the operands.
+// 1x4096x7168: 8.4 us (3.5 TB/s of B) and 2.5 for the sum; a plain read of as many bytes takes 5.4.
 template <bool KN, bool ROWS, bool WHOLE, int MF, int NF, int U>
 __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g, float* __restrict__ part,
                                                                         int per) {
@@ -726,13 +727,15 @@ void launch_few(const MatmulArgs& g, float* ws, hipStream_t st) {
 struct Shape {
   int bm, bn, per_cu, step, step_alone;
 };
-constexpr Shape kShapes[2][4] = {{{256, 256, 1, 2080, 2080}, {256, 128, 1, 1330, 1330}, {128, 128, 2, 1320, 930}, {64, 128, 2, 900, 600}},
-                                 {{256, 128, 1, 2250, 2250}, {128, 128, 2, 2500, 1750}, {64, 128, 2, 1300, 900}, {0, 0, 0, 0, 0}}};
+constexpr Shape kShapes[2][4] = {  // bf16 C, fp32 C
+    {{256, 256, 1, 2080, 2080}, {256, 128, 1, 1330, 1330}, {128, 128, 2, 1320, 930}, {64, 128, 2, 900, 600}},
+    {{256, 128, 1, 2250, 2250}, {128, 128, 2, 2500, 1750}, {64, 128, 2, 1300, 900}, {0, 0, 0, 0, 0}}};
 
 // The shape, and into how many parts of K the tiles behind the last full card are cut, by the time that the steps
 // take, 3 us for each round of tiles, and 3 us and both ways of the parts' bytes at 5 TB/s for the sums:
-// 21804x4096x7168, 1376 tiles of 256 x 256: 96 cut in two, 5.5 rounds instead of 6 (650 -> 640 us); 7168x4096x21808 in fp32, 896 of
-// 256 x 128: 128 cut in two, 3.5 instead of 4 (1434 -> 1351 us).
+// 21804x4096x7168, 1376 tiles of 256 x 256: 96 cut in two, 5.5 rounds instead of 6 (650 -> 640 us); 7168x4096x21808 in
+// fp32, 896 of 256 x 128: 128 cut in two, 3.5 instead of 4 (1434 -> 1351 us).  Shapes against each other, bf16, in us:
+// 1023x7168x4096 256x256 55, 256x128 43, 128x128 45, 64x128 54; 4096x4096x4096 74, 91, 89, 112; 300x8192x8192 53, 59, 56, 47.
 Cut tile_plan(const MatmulArgs& g) {
   const int KB = (int)((g.K + 127) / 128);
   Cut best{};

@@ -192,21 +192,27 @@ __global__ __launch_bounds__(256) void score_choose_kernel(const ScoreArgs p, co
 // within the lane.  A lane keeps its best four in order, and a round of the choice is one maximum over the
 // lanes (in the vector ALU) of their first, whose lane then moves up its others; a lane that has given
 // four takes the next four out of its registers.  (With the best two, most rounds of a wave had a lane to
-// fill up again: 21804x256 in groups 68 us for the whole call.)  A group's value
-// is made of its best two as they were, without register numbers.
+// fill up again: 21804x256 in groups 68 us for the whole call.)  A group's value is made of its best two as they
+// were, without register numbers.
 //
 // An order that fp32 does not settle is found, not guessed, wherever two values that decide something differ
 // by less than what scores can be off.  The chosen and the first left out (and no other could be among them: one
 // more round shows the next value): their values again in 64 bits, one a lane, and their order by counting.
 // The last group that stays and the first that does not, a softmax with a bias (whose sum would have to be
-// taken again), or a value that is no ordinary number: the whole token in 64 bits, by the wave.  What a score
-// is off, relative to |c| + max |bias|: sigmoid 4 2^-24 (an exponential with its argument's rounding, a sum, a
-// reciprocal: |x| s (1 - s) < 1/4), softmax 2^-18 (logits up to 60 below the largest), and 2^-20 for the four
-// bits; twice that for two values: below 2^-18 and 2^-16.  A group's value v: two scores' part without the four
-// bits, and |c1| + |c2| <= |v| + 4 max |bias|: for two groups below 2^-20 (2^-15) (|v| + 6 max |bias|).
+// taken again), or a value that is no ordinary number: the whole token in 64 bits, by the wave.
+// What a score is off, relative to itself, in u = 2^-24: a sigmoid |x| + 5 (the exponential's argument is rounded, which
+// counts |x| (1 - s); the exponential 2, the sum 1, the reciprocal 2), a softmax |x - max| + 5 and a sum of up to 16 terms a lane; the
+// addition of the bias 1, and the four bits 16 between two values.  As |s| <= |c| + max |bias|, two sigmoids are apart above
+// 2^-18 (64 u) of |c| + max |bias| as long as that is above 1e-6 (x > -14: 2 (14 + 5 + 1) + 16), two softmaxes above 2^-16
+// for values above 1e-30 (69 below the largest).  A group's value v has two scores without the four bits, |c1| + |c2| <= |v| + 4 max
+// |bias|: apart above 2^-19 (32 u) of |v| + 6 max |bias| as long as that is above 1e-3 (of x below -10 there is then no
+// more than u / 500 in it), for a softmax above 2^-15.  What is smaller goes to 64 bits.
 //
 // Tokens that are done again wait until the block's others are through: what they need in registers is then
-// no longer kept through the choice (16384x128 22 -> 20 us, 21804x256 in groups 57 -> 52; four waves a block 49).
+// no longer kept through the choice (16384x128 22 -> 20 us, 21804x256 in groups 57 -> 52; with four waves a block 49, and
+// 39 since a tie is its own token's matter).  Kernels of 21804x256 in groups: choice 28 us, scan 5, places 5.  What bounds the choice
+// are the chains of a wave's two passes: vector ALU a third of the time (1500 instructions a wave), memory and LDS waits half.  Asking
+// for the second pass's logits during the first costs registers: 43 us.
 //
 // A block takes `seg` tokens, keeps their ids, and gives each pair its rank among the block's pairs of the
 // same expert (each wave a share of the pairs, in order; lanes with the same expert by one ballot per id bit)
@@ -240,8 +246,8 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// By the threads of a block, 256 of which have four experts each: first positions of the experts (start, in LDS, which may be the counts themselves) from
-// their counts, to offsets and counts too where they are asked for.
+// By the threads of a block, 256 of which have four experts each: first positions of the experts (start, in LDS, which
+// may be the counts themselves) from their counts, to offsets and counts too where they are asked for.
 __device__ __forceinline__ void expert_starts(int E, const int32_t* cnt, int* start, int32_t* __restrict__ offsets,
                                               int32_t* __restrict__ counts) {
   __shared__ int part[4];
@@ -408,7 +414,7 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
       insert(c[i]);
     }
     bool odd = !(nought == 0.0f);  // something for the 64-bit path
-    constexpr float kOff = SIG ? 0x1p-18f : 0x1p-16f, kGroupOff = SIG ? 0x1p-20f : 0x1p-15f;
+    constexpr float kOff = SIG ? 0x1p-18f : 0x1p-16f, kGroupOff = SIG ? 0x1p-19f : 0x1p-15f;
     bool dropped = false;
     if (p.groups > 1) {
       if (lg >= 2) merge_best<1>(g1, g2);
@@ -432,7 +438,8 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
       }
       dropped = !alive || rank >= p.group_topk;
       const float least = -lanes_max<LPT>(dropped ? kNone : -v), next = lanes_max<LPT>(dropped && alive ? v : kNone);
-      odd |= next > -1e38f && !(least - next > kGroupOff * (fabsf(next) + 6 * bm));
+      const float near = fabsf(next) + 6 * bm;
+      odd |= next > -1e38f && !(least - next > kGroupOff * near && (!SIG || near > 1e-3f));
       if (dropped) b1 = b2 = b3 = b4 = kNone;
     }
     if (!active) b1 = kNone - 1e35f * l;  // one winner in every round, which takes nothing
@@ -476,7 +483,7 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
     if (l == keep - 1) after = last;
     auto apart = [&](float hi, float lo) __attribute__((always_inline)) { return hi - lo > kOff * (fabsf(lo) + bm); };
     const bool unsure = active && l < p.k && !apart(mine_v, after);
-    odd |= several || (active && l < p.k && !(fabsf(mine_v) > 1e-30f && mine_v > -1e38f));
+    odd |= several || (active && l < p.k && !(fabsf(mine_v) + (SIG ? bm : 0.0f) > (SIG ? 1e-6f : 1e-30f) && mine_v > -1e38f));
     if (!SIG && bias) odd |= unsure;
     odd |= active && l == p.k - 1 && !apart(mine_v, last);
     // the lanes' candidates (an id past the experts: none was left, and the token is done again below)
@@ -817,7 +824,8 @@ __global__ __launch_bounds__(256) void score_backward_kernel(const ScoreArgs p, 
 // above, once for four tokens; the wave's four rows of the gradient, which lie behind one another, are laid out in
 // LDS and written in one piece, 16 bytes a lane, whatever E is.  A softmax that is not renormalised goes through
 // LDS too: its rows' exponentials lie where the gradient comes to lie.  An id that occurs twice in a token gets
-// the sum in slot order, the same in each of its lanes.
+// the sum in slot order, the same in each of its lanes.  21804x256, sigmoid: 8.5 us where the bytes take 4.8 (one token a
+// wave, written 4 bytes a lane: 18); what is left is two dependent loads (ids, then logits) before the first store.
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 

@@ -183,6 +183,19 @@ def test_logits_whose_scores_are_equal_in_64_bits(sigmoid):
         check_route(x, k, sigmoid, False, bias=np.zeros(E, np.float32))
 
 
+def test_small_sigmoids_in_groups():
+    """Scores far below one, with no bias, with a bias of their own size and with a larger one: what fp32 exponentials are off
+    there is more than the scores' distances."""
+    rng = np.random.default_rng(12)
+    T, E = 400, 256
+    for low in (-6, -12, -20, -45, -66):
+        x = (low + rng.standard_normal((T, E)) * 1e-3).astype(np.float32)
+        for bias in (None, rng.standard_normal(E).astype(np.float32) * np.float32(np.exp(low) * 1e-3),
+                     rng.standard_normal(E).astype(np.float32) * np.float32(1e-5)):
+            check_route(x, 8, True, True, bias=bias, groups=8, keep=4, best=2)
+            check_route(x, 8, True, False, bias=bias)
+
+
 def test_far_logits():
     """Scores that underflow or saturate in 32 bits, and in 64: weights stay quotients."""
     x = np.stack([np.linspace(-80, 80, 16), np.linspace(-120, -90, 16), np.linspace(30, 36, 16), np.linspace(-900, -800, 16),
