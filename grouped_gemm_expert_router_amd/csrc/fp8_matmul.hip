@@ -346,16 +346,18 @@ __device__ __forceinline__ const T* uniform_ptr(const T* p) {
 // used: one DMA brings one block's scales of 64 rows, and the waves of a step take the same rows for
 // different blocks, and with them the same lines.
 //
-// Waves that have their fragments run at a higher priority (s_setprio) until their matrix instructions are out, so that those of
-// a compute unit take turns between LDS and the matrix cores (1023x7168x4096 42.4 -> 41.0 us, with fp32 C 66.9 -> 64.3,
-// 7168x4096x21808 with fp32 C 1335 -> 1263).  Counters at 4096x4096x7168: matrix cores busy 50 % of the time, vector ALU
-// (promotion, addresses) 39 %, LDS without conflicts; the rest is the barrier each step and the fragments that every wave
-// reads behind it.  A second barrier inside the step, to send B's next block earlier, gave nothing.
+// Waves that have their fragments run at a higher priority (s_setprio) until their matrix instructions are out, so
+// that those of a compute unit take turns between LDS and the matrix cores (1023x7168x4096 42.4 -> 41.0 us, with
+// fp32 C 66.9 -> 64.3, 7168x4096x21808 with fp32 C 1335 -> 1263).  Counters at 4096x4096x7168: matrix cores busy 50 %
+// of the time, vector ALU (promotion, addresses) 39 %, LDS without conflicts; the rest is the barrier each step and
+// the fragments that every wave reads behind it.  A second barrier inside the step, to send B's next block earlier,
+// gave nothing.
 //
 // Each 32 x 32 block of C is held transposed (B is the MFMA's first operand): lane l has row l % 32 and 16
 // columns, so one A scale serves its 16 values.
 template <int FORM, bool WHOLE, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN, 1) void fp8_matmul_tile_kernel(const MatmulArgs g, float* __restrict__ part, const Cut cut) {
+__global__ __launch_bounds__(64 * WM * WN, 1) void fp8_matmul_tile_kernel(const MatmulArgs g, float* __restrict__ part,
+                                                                          const Cut cut) {
   constexpr bool KN = FORM == MOE_B_KN, ROWS = FORM == MOE_B_NK_ROWS;
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32, BK = 128;
   constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;

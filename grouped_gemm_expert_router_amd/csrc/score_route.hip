@@ -200,19 +200,20 @@ __global__ __launch_bounds__(256) void score_choose_kernel(const ScoreArgs p, co
 // more round shows the next value): their values again in 64 bits, one a lane, and their order by counting.
 // The last group that stays and the first that does not, a softmax with a bias (whose sum would have to be
 // taken again), or a value that is no ordinary number: the whole token in 64 bits, by the wave.
-// What a score is off, relative to itself, in u = 2^-24: a sigmoid |x| + 5 (the exponential's argument is rounded, which
-// counts |x| (1 - s); the exponential 2, the sum 1, the reciprocal 2), a softmax |x - max| + 5 and a sum of up to 16 terms a lane; the
-// addition of the bias 1, and the four bits 16 between two values.  As |s| <= |c| + max |bias|, two sigmoids are apart above
-// 2^-18 (64 u) of |c| + max |bias| as long as that is above 1e-6 (x > -14: 2 (14 + 5 + 1) + 16), two softmaxes above 2^-16
-// for values above 1e-30 (69 below the largest).  A group's value v has two scores without the four bits, |c1| + |c2| <= |v| + 4 max
-// |bias|: apart above 2^-19 (32 u) of |v| + 6 max |bias| as long as that is above 1e-3 (of x below -10 there is then no
-// more than u / 500 in it), for a softmax above 2^-15.  What is smaller goes to 64 bits.
+// What a score is off, relative to itself, in u = 2^-24: a sigmoid |x| + 5 (the exponential's argument is rounded,
+// which counts |x| (1 - s); the exponential 2, the sum 1, the reciprocal 2), a softmax |x - max| + 5 and a sum of up
+// to 16 terms a lane; the addition of the bias 1, and the four bits 16 between two values.  As |s| <= |c| + max |bias|,
+// two sigmoids are apart above 2^-18 (64 u) of |c| + max |bias| as long as that is above 1e-6 (x > -14:
+// 2 (14 + 5 + 1) + 16), two softmaxes above 2^-16 for values above 1e-30 (69 below the largest).  A group's value v has
+// two scores without the four bits, |c1| + |c2| <= |v| + 4 max |bias|: apart above 2^-19 (32 u) of |v| + 6 max |bias|
+// as long as that is above 1e-3 (of x below -10 there is then no more than u / 500 in it), for a softmax above 2^-15.
+// What is smaller goes to 64 bits.
 //
-// Tokens that are done again wait until the block's others are through: what they need in registers is then
-// no longer kept through the choice (16384x128 22 -> 20 us, 21804x256 in groups 57 -> 52; with four waves a block 49, and
-// 39 since a tie is its own token's matter).  Kernels of 21804x256 in groups: choice 28 us, scan 5, places 5.  What bounds the choice
-// are the chains of a wave's two passes: vector ALU a third of the time (1500 instructions a wave), memory and LDS waits half.  Asking
-// for the second pass's logits during the first costs registers: 43 us.
+// Tokens that are done again wait until the block's others are through: what they need in registers is then no
+// longer kept through the choice (16384x128 22 -> 20 us, 21804x256 in groups 57 -> 52; with four waves a block 49,
+// and 39 since a tie is its own token's matter).  Kernels of 21804x256 in groups: choice 28 us, scan 5, places 5.
+// What bounds the choice are the chains of a wave's two passes: vector ALU a third of the time (2400 instructions a
+// wave), memory and LDS waits half.  Asking for the second pass's logits during the first costs registers: 43 us.
 //
 // A block takes `seg` tokens, keeps their ids, and gives each pair its rank among the block's pairs of the
 // same expert (each wave a share of the pairs, in order; lanes with the same expert by one ballot per id bit)
@@ -479,7 +480,8 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
       }
     }
     // what follows each candidate (the last: the value of the round behind it), and whether it is apart from it
-    float after = __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(last), __float_as_uint(mine_v), 0x101, 0xf, 0xf, false));
+    float after = __uint_as_float(
+        __builtin_amdgcn_update_dpp(__float_as_uint(last), __float_as_uint(mine_v), 0x101, 0xf, 0xf, false));
     if (l == keep - 1) after = last;
     auto apart = [&](float hi, float lo) __attribute__((always_inline)) { return hi - lo > kOff * (fabsf(lo) + bm); };
     const bool unsure = active && l < p.k && !apart(mine_v, after);

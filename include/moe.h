@@ -403,7 +403,7 @@ int moe_score_route(const moe_score_desc* desc, const float* logits, const float
  *   sigmoid, renormalise d_logits[ids_j] = (g_j - sum_i g_i q_i) q_j (1 - s_j), and 0 elsewhere
  *   softmax, renormalise d_logits[ids_j] = (g_j - sum_i g_i q_i) q_j, and 0 elsewhere
  *   softmax              d_logits[e] = s_e (sum_{j: ids_j = e} g_j - sum_i g_i s[ids_i]) for every e
- * A token without such a slot has a row of zeros; its logits are not read.  desc: T, E, k, score,
+ * A token without such a slot has a row of zeros, whatever its logits are.  desc: T, E, k, score,
  * renormalise and scale are used (the others checked).  logits and d_logits 16-byte aligned, the other
  * arrays to their type; d_logits overlaps no input. */
 int moe_score_backward(const moe_score_desc* desc, const float* logits, const int32_t* topk_ids,
@@ -442,8 +442,9 @@ int moe_fp8_quantize(const void* src, int32_t src_dtype, int64_t rows, int64_t c
  * added in fp32, then C_in (c_dtype, C's layout; NULL: none; may be C itself), and C (bf16 or
  * fp32) is rounded once.  For an fp32 C the block's sums are fp32; for a bf16 C they come from the fp8 matrix
  * instruction, which drops what lies more than 13 bits below the largest of eight products (along K) before it
- * adds them: 1.5e-5 of the result's norm on normal data.  Sums run in a fixed order (bitwise reproducible).  lda, ldb, ldc: codes or
- * values from one row to the next; what lies between two rows is not touched.
+ * adds them: 1.5e-5 of the result's norm on normal data.  Sums run in a fixed order (bitwise reproducible), which
+ * M, N and K decide.  lda, ldb, ldc: codes or values from one row to the next; what lies between two rows is
+ * not touched.
  * M of any size, 0 .. 2^30; N and K positive multiples of 16 up to 2^24, M * N < 2^36; lda, ldb
  * multiples of 16, ldc of 8, at least the row's length; lda and ldb at most 2^28, ldc 2^31.  ws:
  * moe_fp8_matmul_workspace_bytes (256-byte aligned; may be NULL where that is 0).  A, B, C and C_in 16-byte aligned. */

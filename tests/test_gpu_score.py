@@ -299,6 +299,22 @@ def test_backward_by_differences(sigmoid, renorm):
         assert (np.abs(diff - d[:, e])[ok] <= bound[ok]).all()
 
 
+@pytest.mark.parametrize("sigmoid,renorm", [(True, True), (False, True), (False, False)])
+def test_backward_of_tokens_without_a_slot(sigmoid, renorm):
+    """Rows of zeros where no id is an expert's, with NaN and infinities for logits; their neighbours as ever."""
+    for T in (7, 5000):
+        x = draw(T, 40, 3)
+        ids = np.tile(np.array([3, 39, 0], np.int32), (T, 1))
+        clean = run_backward(desc(T, 40, 3, sigmoid, renorm), dev(x), dev(ids, I32), dev(np.ones((T, 3)))).cpu().numpy()
+        gone = np.arange(0, T, 3)
+        ids[gone] = -1
+        x[gone] = np.array([np.nan, np.inf, -np.inf, 1], np.float32)[np.arange(40) % 4]
+        got = run_backward(desc(T, 40, 3, sigmoid, renorm), dev(x), dev(ids, I32), dev(np.ones((T, 3)))).cpu().numpy()
+        assert (got[gone] == 0).all()
+        keep = np.setdiff1d(np.arange(T), gone)
+        assert np.array_equal(got[keep], clean[keep])
+
+
 def test_backward_of_ids_out_of_range_and_repeated():
     x, g = draw(3, 10, 1), np.ones((3, 3), np.float32)
     ids = np.array([[10, 5, -7], [1 << 30, -1, 12], [4, 4, 2]])
