@@ -223,7 +223,8 @@ constexpr int kChooseWaves = 4;
 constexpr int kSegPairs = 2048;   // pairs of a block, at most
 constexpr int kSegments = 1024;   // blocks, at most, that the plan is made of
 constexpr int kOneBlock = 32;     // tokens that one block does by itself (64x256: 20 us, 17.7 in two blocks)
-constexpr float kNone = -3.0e38f; // below every value that counts
+constexpr float kNone = -3.0e38f; // below every value that counts: those are above -2 kFarBias
+constexpr float kFarBias = 1e30f; // a finite bias from here on: every token in 64 bits
 constexpr int kRedo = -2;         // in the place of a token's ids: to be done again
 
 struct SegPlan {
@@ -356,10 +357,11 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
   for (int i = 0; i < EPL; ++i) b[i] = bias ? bias[min(base + i, p.E - 1)] : 0.0f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    if (fabsf(b[i]) < 1e30f) bm = fmaxf(bm, fabsf(b[i]));
+    if (fabsf(b[i]) < INFINITY) bm = fmaxf(bm, fabsf(b[i]));
     if (b[i] == -INFINITY || i >= n) b[i] = kNone;
   }
   bm = lanes_max<LPT>(bm);
+  const bool far = bm >= kFarBias;
 
   for (int r0 = wv * TPW; r0 < ntok; r0 += NW * TPW) {
     const int local = r0 + sub;
@@ -414,7 +416,7 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
       c[i] = __uint_as_float((__float_as_uint(u) & ~15u) | (15 - i));
       insert(c[i]);
     }
-    bool odd = !(nought == 0.0f);  // something for the 64-bit path
+    bool odd = far || !(nought == 0.0f);  // something for the 64-bit path
     constexpr float kOff = SIG ? 0x1p-18f : 0x1p-16f, kGroupOff = SIG ? 0x1p-19f : 0x1p-15f;
     bool dropped = false;
     if (p.groups > 1) {
