@@ -294,6 +294,12 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return LPT == 64 ? wave_sum_dpp(v) : row16_sum(v);
 }
 
+// e^(x - m), finite x and m, with the difference's rounding put back: from |x - m| = 64 on that alone is 2^-18.
+__device__ __forceinline__ float exp_apart(float x, float m) {
+  const float d = x - m, t = d - x, rest = (x - (d - t)) - (m + t), e = expf(d);
+  return fmaf(e, rest, e);
+}
+
 // Exchange with the lane whose number differs in the bit `of`, or (in a row, once pairs agree) the mirror image.
 template <int kOf>
 __device__ __forceinline__ float partner(float v) {
@@ -514,11 +520,11 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
     float z;
     if constexpr (SIG) {
       const float m = p.renorm ? lanes_max<LPT>(id >= 0 ? fminf(x1, 0.0f) : -INFINITY) : 0.0f;
-      z = id >= 0 ? expf(fminf(x1, 0.0f) - m) / (1.0f + expf(-fabsf(x1))) : 0.0f;
+      z = id >= 0 ? exp_apart(fminf(x1, 0.0f), m) / (1.0f + expf(-fabsf(x1))) : 0.0f;
       if (p.renorm) z /= lanes_sum<LPT>(z);
     } else {
       const float m = p.renorm ? lanes_max<LPT>(id >= 0 ? x1 : -INFINITY) : top;
-      z = id >= 0 ? expf(x1 - m) : 0.0f;
+      z = id >= 0 ? exp_apart(x1, m) : 0.0f;
       z /= p.renorm ? lanes_sum<LPT>(z) : sum;
     }
     q = active ? z * p.scale : 0.0f;

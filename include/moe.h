@@ -371,7 +371,8 @@ int moe_adamw_step(const moe_adamw* hyper, const moe_tensor* tensors, int64_t n_
  *   ids = the k largest c among the experts that stay, descending
  *   w_j = scale * s[ids_j] / sum_i s[ids_i] (renormalise = 1), or scale * s[ids_j]
  * The bias moves the choice alone, never a weight.  Equal values go to the lower id (group, expert).  The
- * choice is the one that c in 64 bits gives; weights are computed in fp32, to 2^-18 of their value.
+ * choice is the one that c in 64 bits gives; weights are computed in fp32, to 2^-18 of their value (from
+ * a score below fp32's normal range: to 2^-148 times the larger of 1 and scale).
  * An expert whose logit or bias is -inf cannot be chosen: where fewer than k can, the slots behind them
  * have id -1 and weight 0 (a group in which none can be chosen never stays, and one with a single such
  * expert has its c for a value).  A token whose token_mask byte is 0 (uint8 [T]; NULL: none) has ids -1

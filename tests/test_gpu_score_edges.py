@@ -2,8 +2,11 @@
 of test_gpu_score."""
 import numpy as np
 import pytest
+import torch
 
-from test_gpu_score import check_route, draw
+from oracle import score_ref as S
+from block_testlib import assert_close, dev
+from test_gpu_score import check_route, desc, draw, run_route
 
 pytestmark = pytest.mark.gpu
 LOWEST = float(np.finfo(np.float32).min)
@@ -46,3 +49,29 @@ def test_biases_of_any_finite_size(E, k, groups, sigmoid):
                     if k <= keep * (E // groups):
                         for best in (1, 2):
                             check_route(x, k, sigmoid, True, bias=bias, groups=groups, keep=keep, best=best)
+
+
+# ------------------------------------------------------------------------- weights of far logits
+def far_logits(T, E, low, high, seed):
+    """Logits over the whole range, with a full mantissa each."""
+    return np.random.default_rng(seed).uniform(low, high, (T, E)).astype(np.float32)
+
+
+# Bound, in u = 2^-24.  A chosen expert's exponential: 2 (the function) and 1 (its argument's rounding put back); a
+# sigmoid's quotient 4 more; the sum of up to 16 of them 4 additions, or over all logits 22 and (3 |x - max| + 2) a
+# term, which the terms' own size keeps below 3 log 1024 + 2; quotient 1, scale 1: 50 of 64 at most.  Below fp32's
+# normal range a score has steps of 2^-149, which the scale multiplies.
+@pytest.mark.parametrize("T,E,k,groups", [(4, 256, 8, 8), (500, 16, 8, 1), (500, 64, 6, 4), (300, 256, 16, 2), (40, 600, 9, 1), (60, 40, 20, 1)])
+@pytest.mark.parametrize("sigmoid", [True, False], ids=["sigmoid", "softmax"])
+def test_weights_of_far_logits(T, E, k, groups, sigmoid):
+    for low, high in ((-40, 40), (-85, 2), (-100, 0), (-150, 90), (-9, 9)):
+        x = far_logits(T, E, low, high, E - low)
+        bias = np.random.default_rng(E).uniform(0.1, 4, E).astype(np.float32)   # the choice does not go by the scores alone
+        for b in (None, bias):
+            for renorm in (True, False):
+                sd = desc(T, E, k, sigmoid, renorm, 2.5, groups, max(1, groups // 2), 2)
+                got = run_route(sd, dev(x), None if b is None else dev(b), None)
+                for t in range(T):
+                    ids = got["ids"][t]
+                    w = S.weights(x[t], ids, sigmoid, renorm, 2.5)
+                    assert_close(f"w[{t}]", torch.from_numpy(got["w"][t]), w, w * 2.0 ** -18 + 2.0 ** -147)
