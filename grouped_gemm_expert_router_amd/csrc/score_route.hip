@@ -11,6 +11,8 @@
 // the bias acts against the uneven loads of its section "Az egyenetlen terhelés lassítja a tanítást".
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -774,6 +776,11 @@ hipError_t launch_score_route(const ScoreArgs& p, const float* logits, const flo
 
 // -------------------------------------------------------------------------------- backward
 // One wave per token; lane j < k holds slot j, and the lanes then write the row.
+//
+// A softmax that is not renormalised subtracts: d_e = s_e (G_e - sum_i g_i s_i) with G_e the g of e's slots.  Of a confident
+// token s_e is near 1 and the difference what the other experts leave, so it is taken in 64 bits, of scores whose sum
+// is 64-bit too and whose chosen terms are 64-bit exponentials.  The others' are fp32 ones, |x - max| + 2 units of
+// 2^-24 each, and that is the difference's relative error (with fp32 sums it was 2^-7 where the others have 2e-5).
 template <int EPL>
 __device__ __forceinline__ void score_backward_token(const ScoreArgs& p, const float* __restrict__ row,
                                                      const int32_t* __restrict__ ids, const float* __restrict__ d_w,
@@ -788,6 +795,8 @@ __device__ __forceinline__ void score_backward_token(const ScoreArgs& p, const f
   float x[EPL], out[EPL];
   double top = 0.0, sum = 1.0;
   if (dense) {
+    bool first = there;  // the lowest of the slots with this id: its term of the sum in 64 bits
+    for (int j = 0; j < p.k; ++j) first = first && (__builtin_amdgcn_readlane(id, j) != id || j >= lane);
     float xmax = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -796,29 +805,38 @@ __device__ __forceinline__ void score_backward_token(const ScoreArgs& p, const f
       xmax = fmaxf(xmax, x[i]);
     }
     top = wave_max_f64(xmax);
-    float part = 0.0f;
+    double part = first ? exp(l - top) - (double)expf((float)l - (float)top) : 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) part += x[i] = expf(x[i] - (float)top);
     sum = wave_sum_f64(part);
   }
   const double q = chosen_weight(p, there, l, top, sum);
   const double dot = p.renorm || dense ? wave_sum_f64(g * q) : 0.0;
-  // what slot j adds at its expert
-  float v = 0.0f;
-  if (there) v = (float)(dense ? g : p.sigmoid ? (g - dot) * q * sigmoid_scaled(-l, 0.0) : (g - dot) * q);
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) out[i] = dense ? -(float)dot : 0.0f;
+  // what slot j adds at its expert, and there the sum over the slots with this id
+  const float v = there && !dense ? (float)(p.sigmoid ? (g - dot) * q * sigmoid_scaled(-l, 0.0) : (g - dot) * q) : 0.0f;
+  float all = 0.0f;
+  double all_g = 0.0;
   for (int j = 0; j < p.k; ++j) {
-    const int e = __shfl(id, j, 64);
-    const float u = __shfl(v, j, 64);
+    const bool same = __builtin_amdgcn_readlane(id, j) == id;
+    const float u = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), j));
+    const double u_g = lane_f64(g, j);
+    if (same) all += u, all_g += u_g;
+  }
+  if (dense) all = (float)((all_g - dot) * q);
+  const float off = dense ? (float)(dot / sum) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) out[i] = dense ? -off * x[i] : 0.0f;
+  for (int j = 0; j < p.k; ++j) {
+    const int e = __builtin_amdgcn_readlane(id, j);
+    const float u = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(all), j));
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (e == lane + 64 * i) out[i] += u;
+      if (e == lane + 64 * i) out[i] = u;
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
-    if (e < p.E) d[e] = dense ? out[i] * (x[i] / (float)sum) : out[i];
+    if (e < p.E) d[e] = out[i];
   }
 }
 
@@ -830,8 +848,8 @@ __global__ __launch_bounds__(256) void score_backward_kernel(const ScoreArgs p, 
     score_backward_token<EPL>(p, logits + t * p.E, ids + t * p.k, d_w + t * p.k, d + t * p.E);
 }
 
-// For k <= 16: four tokens a wave, a row of 16 lanes each, lane j with slot j.  The values are made in 64 bits as
-// above, once for four tokens; the wave's four rows of the gradient, which lie behind one another, are laid out in
+// For k <= 16: four tokens a wave, a row of 16 lanes each, lane j with slot j.  The chosen experts' values are made in
+// 64 bits as above, once for four tokens; the wave's four rows of the gradient, which lie behind one another, are laid out in
 // LDS and written in one piece, 16 bytes a lane, whatever E is.  A softmax that is not renormalised goes through
 // LDS too: its rows' exponentials lie where the gradient comes to lie.  An id that occurs twice in a token gets
 // the sum in slot order, the same in each of its lanes.  21804x256, sigmoid: 8.5 us where the bytes take 4.8 (one token a
@@ -869,7 +887,7 @@ __global__ __launch_bounds__(256) void score_backward_rows_kernel(const ScoreArg
     const bool there = id >= 0 && id < p.E;
     const double g = there ? (double)d_w[t * p.k + l] * p.scale : 0.0;
     const double x = there ? (double)row[id] : 0.0;
-    double m = 0.0, sum = 1.0;
+    double m = 0.0, sum = DENSE ? 0.0 : 1.0;
     if constexpr (DENSE) {
       float xmax = -INFINITY;
       for (int i = 4 * lane; i < words; i += 256) {
@@ -886,37 +904,43 @@ __global__ __launch_bounds__(256) void score_backward_rows_kernel(const ScoreArg
       }
       xmax = row16_max(xmax);
       m = xmax;
-      float part = 0.0f;
       if (sub < ntok) {
 #pragma unroll 4
-        for (int e = l; e < p.E; e += 16) part += mine[e] = expf(mine[e] - xmax);
+        for (int e = l; e < p.E; e += 16) sum += mine[e] = expf(mine[e] - xmax);
       }
-      sum = row16_sum_f64(part);
     } else {
       for (int i = 4 * lane; i < 4 * p.E; i += 256) *(f32x4*)(rows + i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       if (p.renorm) m = row16_max_f64(there ? (SIG ? fmin(x, 0.0) : x) : -INFINITY);
     }
     __builtin_amdgcn_wave_barrier();
     double q = there ? (SIG ? sigmoid_scaled(x, m) : exp(x - m)) : 0.0;
+    if constexpr (DENSE) {
+      bool first = there;  // the lowest of the slots with this id: its term of the sum in 64 bits
+      for (int j = 0; j < p.k; ++j) first = first && (__shfl(id, j, 16) != id || j >= l);
+      if (first) sum += q - (double)mine[id];
+      sum = row16_sum_f64(sum);
+    }
     if (p.renorm) sum = row16_sum_f64(q);
     q = there ? q / sum : 0.0;
     const double dot = p.renorm || DENSE ? row16_sum_f64(g * q) : 0.0;
-    const float v = there ? (float)(DENSE ? g : SIG ? (g - dot) * q * sigmoid_scaled(-x, 0.0) : (g - dot) * q) : 0.0f;
-    float all = 0.0f;  // over the slots with this id
+    typedef typename std::conditional<DENSE, double, float>::type part_t;
+    part_t v = 0, total = 0;  // the slot's part of the gradient (DENSE: g); over the slots with this id
+    if (DENSE) v = g;
+    else if (there) v = (part_t)(SIG ? (g - dot) * q * sigmoid_scaled(-x, 0.0) : (g - dot) * q);
     for (int j = 0; j < p.k; ++j) {
-      const float o = __shfl(v, j, 16);
-      if (__shfl(id, j, 16) == id) all += o;
+      const part_t o = __shfl(v, j, 16);
+      if (__shfl(id, j, 16) == id) total += o;
     }
+    float all = (float)total;
     if constexpr (DENSE) {
-      const float total = (float)sum, off = (float)dot;
+      const float off = (float)(dot / sum);
       const bool any = (__ballot(there) >> (16 * sub) & 0xFFFF) != 0;
-      const float at = there ? (all - off) * (mine[id] / total) : 0.0f;
+      all = (float)((total - dot) * q);
       __builtin_amdgcn_wave_barrier();
       if (sub < ntok) {
 #pragma unroll 4
-        for (int e = l; e < p.E; e += 16) mine[e] = any ? -off * (mine[e] / total) : 0.0f;
+        for (int e = l; e < p.E; e += 16) mine[e] = any ? -off * mine[e] : 0.0f;
       }
-      all = at;
     }
     __builtin_amdgcn_wave_barrier();
     if (there && sub < ntok) mine[id] = all;

@@ -404,6 +404,9 @@ int moe_score_route(const moe_score_desc* desc, const float* logits, const float
  *   sigmoid, renormalise d_logits[ids_j] = (g_j - sum_i g_i q_i) q_j (1 - s_j), and 0 elsewhere
  *   softmax, renormalise d_logits[ids_j] = (g_j - sum_i g_i q_i) q_j, and 0 elsewhere
  *   softmax              d_logits[e] = s_e (sum_{j: ids_j = e} g_j - sum_i g_i s[ids_i]) for every e
+ * The subtractions are made in 64 bits, of 64-bit scores of the chosen experts, so a confident token's
+ * gradient keeps fp32's digits (the other experts' scores are fp32 exponentials, to |logit - max| + 2 units of
+ * 2^-24) until it falls below 2^-48 of the g.
  * A token without such a slot has a row of zeros, whatever its logits are.  desc: T, E, k, score,
  * renormalise and scale are used (the others checked).  logits and d_logits 16-byte aligned, the other
  * arrays to their type; d_logits overlaps no input. */

@@ -6,7 +6,7 @@ import torch
 
 from oracle import score_ref as S
 from block_testlib import assert_close, dev
-from test_gpu_score import check_route, desc, draw, run_route
+from test_gpu_score import check_route, desc, draw, run_backward, run_route
 
 pytestmark = pytest.mark.gpu
 LOWEST = float(np.finfo(np.float32).min)
@@ -75,3 +75,67 @@ def test_weights_of_far_logits(T, E, k, groups, sigmoid):
                     ids = got["ids"][t]
                     w = S.weights(x[t], ids, sigmoid, renorm, 2.5)
                     assert_close(f"w[{t}]", torch.from_numpy(got["w"][t]), w, w * 2.0 ** -18 + 2.0 ** -147)
+
+
+# ------------------------------------------------------------- gradient of confident tokens
+def softmax_gradient(x, ids, g):
+    """d_e = s_e sum_f s_f (G_e - G_f) over all experts f, G the sum of an expert's g: nothing cancels but what does in
+    the gradient itself.  And s_e times the terms' magnitudes, those of chosen f without what cancels among them."""
+    T, E = x.shape
+    d, size, s_all = np.zeros((T, E)), np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        s, G = S.scores(x[t], False), np.zeros(E)
+        np.add.at(G, ids[t], g[t].astype(np.float64))
+        among = np.zeros(E, bool)
+        among[ids[t]] = True
+        inner = (s[None, :] * (G[:, None] - G[None, :]) * among[None, :]).sum(1)   # over the chosen f
+        outer = np.abs(G) * s[~among].sum()
+        d[t], size[t], s_all[t] = s * (inner + G * s[~among].sum()), s * (np.abs(inner) + outer), s
+    return d, size, s_all
+
+
+def units(x):
+    """The relative bound below, of each token."""
+    far = np.where(np.isinf(x), 0, x.max(1, keepdims=True) - x).max(1, keepdims=True).astype(np.float64)
+    return (12 + 2 * far) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("T,E,k", [(6, 64, 1), (40, 64, 1), (40, 64, 6), (30, 100, 20), (5000, 32, 2), (9, 1024, 16), (5, 1000, 17)])
+def test_softmax_gradient_of_confident_tokens(T, E, k):
+    """Tokens whose chosen experts have nearly all of the softmax, down to 2^-24 of it left over.
+
+    Bound, in u = 2^-24, of the terms that the gradient is made of: the other experts' exponentials |x - max| (the
+    argument's rounding) and 2 (the function), twice where their sum counts too, a quotient or product 2 each, one
+    rounding at the end: below 12 + 2 |x - max|.  The subtraction in 64 bits adds 2^-48 of s_e times the gradients'
+    magnitudes (k terms, each of a few 2^-53)."""
+    rng = np.random.default_rng(E + k)
+    for gap in (0, 4, 8, 12, 17):
+        x = draw(T, E, E + gap, 1.0)
+        ids = np.argsort(rng.random((T, E)), 1)[:, :k]
+        np.put_along_axis(x, ids, np.take_along_axis(x, ids, 1) + np.float32(gap), 1)
+        if E > 64:
+            x[::3, ::5] = np.where(np.isin(np.arange(E)[::5], ids[0]), x[::3, ::5], -100 - gap)   # far ones among the others
+        if k > 1:
+            ids[1::4, 1] = ids[1::4, 0]     # the same expert twice
+        for g in (np.ones((T, k), np.float32), rng.standard_normal((T, k)).astype(np.float32)):
+            got = run_backward(desc(T, E, k, False, False), dev(x), dev(ids, torch.int32), dev(g)).cpu().numpy()
+            ref, size, s = softmax_gradient(x, ids, g)
+            bound = size * units(x) + s * np.abs(g).astype(np.float64).sum(1, keepdims=True) * 2.0 ** -48 + 2.0 ** -140
+            assert_close(f"gap {gap}", torch.from_numpy(got), ref, bound)
+            assert (np.abs(got.astype(np.float64).sum(1)) <= bound.sum(1)).all()   # a softmax's gradient sums to 0
+
+
+def test_softmax_gradient_beside_barred_experts():
+    x = draw(30, 40, 2)
+    x[:, 7:30:3] = -np.inf
+    ids = np.tile(np.array([3, 39, 0]), (30, 1))
+    g = np.random.default_rng(1).standard_normal((30, 3)).astype(np.float32)
+    for k in (3, 17):
+        more = np.full((30, k), -1)
+        more[:, :3] = ids
+        gk = np.full((30, k), np.nan, np.float32)
+        gk[:, :3] = g
+        got = run_backward(desc(30, 40, k, False, False), dev(x), dev(more, torch.int32), dev(gk)).cpu().numpy()
+        ref, size, s = softmax_gradient(x, ids, g)
+        assert (got[:, 7:30:3] == 0).all()
+        assert_close("d", torch.from_numpy(got), ref, size * units(x) + s * np.abs(g).sum(1, keepdims=True) * 2.0 ** -48)
