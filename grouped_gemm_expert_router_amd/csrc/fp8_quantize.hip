@@ -1,6 +1,8 @@
 // Blockwise e4m3 quantisation: one fp32 scale (largest magnitude / 448) for 128 values of a row, for
 // 128 rows of a column (written transposed, an operand of a product over the rows) or for 128 x 128.
-// The codes are those the layer's fp8 path makes of its activations.  ("NVIDIA מציגה דרך יעילה לאמן
+// By rows the codes and scales are bit for bit those that the layer's fp8 path makes of dy, but in two cases: the
+// layer saturates a NaN to -448 where this keeps it, and its scales follow a block's largest magnitude
+// below 448 * 2^-126 too, past fp32's normal range.  ("NVIDIA מציגה דרך יעילה לאמן
 // מודלי MoE בביולוגיה", section "צמצום הזיכרון ותקורות הכימות": quantisation adds work on top of the
 // 16-bit master weights.)
 //

@@ -421,8 +421,10 @@ int moe_bias_update(int64_t E, const int32_t* counts, float rate, const float* b
 
 /* Blockwise e4m3 quantisation, the layer's fp8 format (MOE_FP8_E4M3) on its own.  src: [rows, cols] of
  * src_dtype (MOE_BF16 or MOE_F32), `ld` values from one row to the next.  With m = max(largest magnitude
- * of a block, 448 * 2^-126): scale = m / 448 and code = e4m3(value * (448 / m)), to nearest even; a block of
- * zeros has the scale 1.  A NaN gets the code of NaN; an infinity makes its block's scale infinite.
+ * of a block, 448 * 2^-126): scale = m / 448 and code = e4m3(value * (448 / m)), each quotient and product
+ * rounded to fp32, the code to nearest even; a block of zeros has the scale 1.  A NaN gets the code of NaN; an
+ * infinity makes its block's scale infinite.  (moe_forward and moe_backward make the same codes of what they
+ * quantise themselves, but for a NaN, -448 there, and without the least m.)
  *   MOE_BLOCK_ROWS    128 values of a row (moe_forward's x):  codes [rows, cols], scales [rows, ceil(cols/128)]
  *   MOE_BLOCK_TOKENS  128 rows of a column, transposed: codes [cols, R16] with R16 = rows rounded up to 16
  *                     (codes behind the last row are 0), scales [cols, ceil(rows/128)]: an operand of a
