@@ -740,7 +740,7 @@ hipError_t launch_score_route(const ScoreArgs& p, const float* logits, const flo
   if (p.T > 0 && is_fast(p)) {
     const bool here = seg_plan_fits(p.T, p.k);
     SegPlan sp = seg_plan(p.T, p.k);
-    if (!here) sp = SegPlan{kSegPairs / p.k, (int)((p.T + kSegPairs / p.k - 1) / (kSegPairs / p.k))};
+    if (!here) sp = SegPlan{kSegPairs / p.k, (int)(((int64_t)p.T + kSegPairs / p.k - 1) / (kSegPairs / p.k))};
     int32_t* segcnt = here && sp.S > 1 ? (int32_t*)ws : nullptr;
     uint16_t* ranks = (uint16_t*)(segcnt ? segcnt + (size_t)sp.S * p.E : nullptr);
     const RouteOut o{ids, w, counts, offsets, here ? perm : nullptr, inv_perm};

@@ -7,6 +7,8 @@ within 2^-16 of its terms' magnitudes."""
 import pytest
 import torch
 
+import grouped_gemm_expert_router_amd as moe
+from block_testlib import Guarded, workspace
 from test_gpu_score import desc, run_backward, run_route
 
 pytestmark = pytest.mark.gpu
@@ -131,3 +133,86 @@ def test_as_many_experts_as_are_chosen(E, k, groups, keep, sigmoid):
         x[:, 0] = 0.5                                               # no token without an expert: its softmax would be NaN here
         check_batch(x, k, sigmoid, True, None, None, groups, keep, 2)
         check_batch(x, k, sigmoid, False, bias, None, groups, keep, 2)
+
+
+# ------------------------------------------------------------------------- as many tokens as there may be
+def chunks(n, step=1 << 27):
+    for i in range(0, n, step):
+        yield i, min(n, i + step)
+
+
+def room(gib):
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"needs {gib} GiB of GPU memory")
+
+
+def test_the_largest_batch():
+    """2^31 - 1 pairs: every third token goes to expert 0, the others to expert 1; the plan, the weights and the gradient in
+    closed form.  Plain scores of sigmoids: w = s, d_l = s (1 - s)."""
+    room(120)
+    T = (1 << 31) - 1
+    x = torch.zeros(T, 2, device="cuda")
+    x[:, 1] = 1
+    x[::3, 1] = -1
+    sd = desc(T, 2, 1, True, False)
+    o = {"ids": Guarded((T, 1), I32, fill=77), "w": Guarded((T, 1), torch.float32), "counts": Guarded((2,), I32, fill=77),
+         "offsets": Guarded((3,), I32, fill=77), "perm": Guarded((T,), I32, fill=77), "inv_perm": Guarded((T,), I32, fill=77)}
+    moe.moe_score_route(sd, x, None, None, *[o[n].t for n in ("ids", "w", "counts", "offsets", "perm", "inv_perm")],
+                        workspace(moe.moe_score_workspace_bytes(sd)))
+    torch.cuda.synchronize()
+    o = {n: g.check().view(-1) for n, g in o.items()}
+    n0 = (T + 2) // 3
+    assert o["counts"].tolist() == [n0, T - n0] and o["offsets"].tolist() == [0, n0, T]
+    s0, s1 = 0.5, 1 / (1 + 2.718281828459045 ** -1)
+    for a, b in chunks(T):
+        t = torch.arange(a, b, device="cuda")
+        third = t % 3 == 0
+        pos = torch.where(third, t // 3, n0 + t - (t + 2) // 3)
+        assert torch.equal(o["ids"][a:b], (~third).to(I32)) and torch.equal(o["inv_perm"][a:b].long(), pos)
+        assert torch.equal(o["perm"][pos].long(), t)
+        want = torch.where(third, s0, s1)
+        assert ((o["w"][a:b] - want).abs() <= want * 2.0 ** -18).all()
+        del t, third, pos, want
+    ids = o["ids"].view(T, 1)
+    del o
+    g = torch.ones(T, 1, device="cuda")
+    d = Guarded((T, 2), torch.float32)
+    moe.moe_score_backward(sd, x, ids, g, d.t)
+    torch.cuda.synchronize()
+    d = d.check()
+    for a, b in chunks(T):
+        third = torch.arange(a, b, device="cuda") % 3 == 0
+        want = torch.stack([torch.where(third, s0 * (1 - s0), 0.0), torch.where(third, 0.0, s1 * (1 - s1))], 1)
+        assert ((d[a:b] - want).abs() <= want * 2.0 ** -18).all()
+        del third, want
+
+
+@pytest.mark.parametrize("k,sigmoid", [(2, True), (2, False), (17, False)])
+def test_logits_past_32_bit_offsets(k, sigmoid):
+    """More than 2^31 logits of more than 2^24 tokens, whose rows repeat: choice, weights and gradient repeat with them."""
+    room(100)
+    T, E, period = (1 << 24) + 77, 136, 1009
+    gen = torch.Generator("cuda").manual_seed(1)
+    base = torch.randn(period, E, generator=gen, device="cuda").mul_(1.5).clamp_(-8, 8)
+    g0 = torch.randn(period, k, generator=gen, device="cuda")
+    times = -(-T // period)
+    x, g = base.repeat(times, 1)[:T], g0.repeat(times, 1)[:T]
+    sd, small = desc(T, E, k, sigmoid, False), desc(period, E, k, sigmoid, False)
+    ids, w = torch.empty(T, k, dtype=I32, device="cuda"), torch.empty(T, k, device="cuda")
+    rest = [torch.empty(n, dtype=I32, device="cuda") for n in (E, E + 1, T * k, T * k)]
+    moe.moe_score_route(sd, x, None, None, ids, w, *rest, workspace(moe.moe_score_workspace_bytes(sd)))
+    d = torch.empty(T, E, device="cuda")
+    moe.moe_score_backward(sd, x, ids, g, d)
+    one = run_route(small, base, None, None)
+    ids0, w0 = torch.from_numpy(one["ids"]).cuda(), torch.from_numpy(one["w"]).cuda()
+    d0 = run_backward(small, base, ids0, g0)
+    for got, want in ((ids, ids0), (w, w0), (d, d0)):
+        whole = T // period * period
+        assert torch.equal(got[:whole].view(-1, period, got.shape[1]), want.expand(whole // period, -1, -1))
+        assert torch.equal(got[whole:], want[:T - whole])
+    want, score = choice(base, k, sigmoid, None, None, 1, 1, 1)
+    assert torch.equal(ids0, want) and ((w0.double() - score).abs() <= score * 2.0 ** -18).all()
+    flat = ids.view(-1)
+    assert torch.equal(rest[0].long(), torch.bincount(flat, minlength=E))
+    assert (flat[rest[2].long()].diff() >= 0).all()                 # pairs by expert
+    assert torch.equal(rest[2][rest[3].long()], torch.arange(T * k, dtype=I32, device="cuda"))
