@@ -5,7 +5,6 @@
 // kernele", section "Mit csinált a Prime Intellect?").
 #include <type_traits>
 
-
 #include "common.hpp"
 #include "gemm_common.hpp"
 #include "kernels.hpp"
@@ -106,7 +105,7 @@ __device__ __forceinline__ void store4(const MatmulArgs& g, int64_t at, float (&
 //
 // B [N, K]: 16 columns a thread block, whose eight waves take the blocks of K in turn, U at a time.
 // B [K, N]: 16 NF columns, 128 (one cache line) where K is long; the LDS transpose read makes the operands.
-// 1x4096x7168: 8.4 us (3.5 TB/s of B) and 2.5 for the sum; a plain read of as many bytes takes 5.4.
+// 1x4096x7168: 8.4 us (3.5 TB/s of B) and 2.5 for the sum, 11.0 the call; a plain read of as many bytes takes 5.4.
 template <bool KN, bool ROWS, bool WHOLE, int MF, int NF, int U>
 __global__ __launch_bounds__(512) void fp8_matmul_few_kernel(const MatmulArgs g, float* __restrict__ part,
                                                                         int per) {
@@ -348,9 +347,10 @@ __device__ __forceinline__ const T* uniform_ptr(const T* p) {
 //
 // Waves that have their fragments run at a higher priority (s_setprio) until their matrix instructions are out, so
 // that those of a compute unit take turns between LDS and the matrix cores (1023x7168x4096 42.4 -> 41.0 us, with
-// fp32 C 66.9 -> 64.3, 7168x4096x21808 with fp32 C 1335 -> 1263).  Counters at 4096x4096x7168: matrix cores busy 50 %
-// of the time, vector ALU (promotion, addresses) 39 %, LDS without conflicts; the rest is the barrier each step and
-// the fragments that every wave reads behind it.  A second barrier inside the step, to send B's next block earlier,
+// fp32 C 66.9 -> 64.3, 7168x4096x21808 with fp32 C 1335 -> 1263, all on one card; on others the last now takes 1330 to
+// 1360).  Counters at 4096x4096x7168: matrix cores busy 50 % of the time (21804x4096x7168 47 %, fp32 C 45 %), vector ALU
+// (promotion, addresses) 39 %, LDS without conflicts; the rest is the barrier each step and the fragments that every
+// wave reads behind it.  A second barrier inside the step, to send B's next block earlier,
 // gave nothing.
 //
 // Each 32 x 32 block of C is held transposed (B is the MFMA's first operand): lane l has row l % 32 and 16

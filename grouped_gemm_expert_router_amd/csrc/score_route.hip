@@ -211,6 +211,10 @@ __global__ __launch_bounds__(256) void score_choose_kernel(const ScoreArgs p, co
 // as long as that is above 1e-3 (of x below -10 there is then no more than u / 500 in it), for a softmax above 2^-15.
 // What is smaller goes to 64 bits.
 //
+// A round in which several lanes hold the same value counts as undecided, and so does one in which nothing is left.  So a
+// choice of all the experts that stay, or of all but one (up to 16), is made in 64 bits for every token: 16384 tokens,
+// eight of 8 experts 44 us (six of them 17), eight of one group of eight among 64 in eight 51 (of two groups 23).
+//
 // Tokens that are done again wait until the block's others are through: what they need in registers is then no
 // longer kept through the choice (16384x128 22 -> 20 us, 21804x256 in groups 57 -> 52; with four waves a block 49,
 // and 39 since a tie is its own token's matter).  Kernels of 21804x256 in groups: choice 28 us, scan 5, places 5.
