@@ -191,9 +191,9 @@ __global__ __launch_bounds__(256) void plan_hist_kernel(const int32_t* __restric
   for (int e = lane; e < E; e += 64) cnt[e] = 0;
   __syncthreads();
   if (s < S) {
-    const int lo = s * seg, n = min(A - lo, seg);  // counted from lo: past it, numbers may leave 32 bits
-    for (int i = lane; i < n; i += 64) {
-      const int e = ids[lo + i];
+    const uint32_t lo = s * seg, hi = lo + min(A - (int)lo, seg);  // a step past the last pair may leave 31 bits
+    for (uint32_t p = lo + lane; p < hi; p += 64) {
+      const int e = ids[p];
       if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
     }
   }
@@ -284,11 +284,11 @@ __global__ __launch_bounds__(256) void plan_scatter_kernel(const int32_t* __rest
   if (s >= S) return;
   int nbits = 1;
   while ((1 << nbits) < E) ++nbits;
-  const int lo = s * seg, n = min(A - lo, seg);
+  const uint32_t lo = s * seg, hi = lo + min(A - (int)lo, seg);
   const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
-  for (int base = 0; base < n; base += 64) {
-    const bool in = base + lane < n;
-    const int p = in ? lo + base + lane : lo;
+  for (uint32_t base = lo; base < hi; base += 64) {
+    const uint32_t p = base + lane;
+    const bool in = p < hi;
     const int e = in ? ids[p] : -1;
     const bool valid = in && e >= 0 && e < E;
     uint64_t m = __ballot(valid);
