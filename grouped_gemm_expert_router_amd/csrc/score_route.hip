@@ -202,6 +202,8 @@ __global__ __launch_bounds__(256) void score_choose_kernel(const ScoreArgs p, co
 // more round shows the next value): their values again in 64 bits, one a lane, and their order by counting.
 // The last group that stays and the first that does not, a softmax with a bias (whose sum would have to be
 // taken again), or a value that is no ordinary number: the whole token in 64 bits, by the wave.
+// (Behind the last expert that can be chosen the rounds find empty places, kNone with a register's number.  They decide
+// nothing, however many lanes hold the same, and none of them is a candidate: 16384 tokens, eight of 8 experts 18 us.)
 // What a score is off, relative to itself, in u = 2^-24: a sigmoid |x| + 5 (the exponential's argument is rounded,
 // which counts |x| (1 - s); the exponential 2, the sum 1, the reciprocal 2), a softmax |x - max| + 5 and a sum of up
 // to 16 terms a lane; the addition of the bias 1, and the four bits 16 between two values.  As |s| <= |c| + max |bias|,
@@ -210,10 +212,6 @@ __global__ __launch_bounds__(256) void score_choose_kernel(const ScoreArgs p, co
 // two scores without the four bits, |c1| + |c2| <= |v| + 4 max |bias|: apart above 2^-19 (32 u) of |v| + 6 max |bias|
 // as long as that is above 1e-3 (of x below -10 there is then no more than u / 500 in it), for a softmax above 2^-15.
 // What is smaller goes to 64 bits.
-//
-// A round in which several lanes hold the same value counts as undecided, and so does one in which nothing is left.  So a
-// choice of all the experts that stay, or of all but one (up to 16), is made in 64 bits for every token: 16384 tokens,
-// eight of 8 experts 44 us (six of them 17), eight of one group of eight among 64 in eight 51 (of two groups 23).
 //
 // Tokens that are done again wait until the block's others are through: what they need in registers is then no
 // longer kept through the choice (16384x128 22 -> 20 us, 21804x256 in groups 57 -> 52; with four waves a block 49,
@@ -230,6 +228,7 @@ constexpr int kSegPairs = 2048;   // pairs of a block, at most
 constexpr int kSegments = 1024;   // blocks, at most, that the plan is made of
 constexpr int kOneBlock = 32;     // tokens that one block does by itself (64x256: 20 us, 17.7 in two blocks)
 constexpr float kNone = -3.0e38f; // below every value that counts: those are above -2 kFarBias
+constexpr float kEmpty = -1e38f;  // above a place without an expert (kNone with a register's number), below the others
 constexpr float kFarBias = 1e30f; // a finite bias from here on: every token in 64 bits
 constexpr int kRedo = -2;         // in the place of a token's ids: to be done again
 
@@ -437,8 +436,8 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
       if (lg >= 8) merge_best<4>(g1, g2);
       if (LPT == 64 && lg >= 16) merge_best<8>(g1, g2);
       if (LPT == 64 && lg >= 32) merge_best<16>(g1, g2);
-      const bool alive = g1 > -1e38f;
-      const float v = p.group_best == 2 && g2 > -1e38f ? g1 + g2 : g1;
+      const bool alive = g1 > kEmpty;
+      const float v = p.group_best == 2 && g2 > kEmpty ? g1 + g2 : g1;
       int rank = 0;
       if constexpr (LPT == 16) {
         if (lg == 1) rank_groups<1>(v, rank);
@@ -454,7 +453,7 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
       dropped = !alive || rank >= p.group_topk;
       const float least = -lanes_max<LPT>(dropped ? kNone : -v), next = lanes_max<LPT>(dropped && alive ? v : kNone);
       const float near = fabsf(next) + 6 * bm;
-      odd |= next > -1e38f && !(least - next > kGroupOff * near && (!SIG || near > 1e-3f));
+      odd |= next > kEmpty && !(least - next > kGroupOff * near && (!SIG || near > 1e-3f));
       if (dropped) b1 = b2 = b3 = b4 = kNone;
     }
     if (!active) b1 = kNone - 1e35f * l;  // one winner in every round, which takes nothing
@@ -467,7 +466,7 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
       const float m = lanes_max<LPT>(b1);
       const bool win = b1 == m;
       const uint64_t won = __ballot(win);
-      if (__popcll(won) != TPW) several |= LPT == 64 || __popcll(won >> (16 * sub) & 0xFFFF) != 1;
+      if (__popcll(won) != TPW) several |= m > kEmpty && (LPT == 64 || __popcll(won >> (16 * sub) & 0xFFFF) != 1);
       last = m;
       if (j == keep) break;
       if (l == j) mine_v = m;
@@ -499,23 +498,25 @@ __global__ __launch_bounds__(64 * kChooseWaves, LPT == 16 ? 3 : 2) void score_ch
     if (l == keep - 1) after = last;
     auto apart = [&](float hi, float lo) __attribute__((always_inline)) { return hi - lo > kOff * (fabsf(lo) + bm); };
     const bool unsure = active && l < p.k && !apart(mine_v, after);
-    odd |= several || (active && l < p.k && !(fabsf(mine_v) + (SIG ? bm : 0.0f) > (SIG ? 1e-6f : 1e-30f) && mine_v > -1e38f));
+    odd |= several || (active && l < p.k && !(fabsf(mine_v) + (SIG ? bm : 0.0f) > (SIG ? 1e-6f : 1e-30f) && mine_v > kEmpty));
     if (!SIG && bias) odd |= unsure;
     odd |= active && l == p.k - 1 && !apart(mine_v, last);
     // the lanes' candidates (an id past the experts: none was left, and the token is done again below)
     int mine = active && l < keep ? min(cand[l], p.E - 1) : 0;
     if ((SIG || !bias) && __ballot(unsure)) {
+      // (a round in which nothing was left has no candidate, whatever its winner was)
+      const bool real = active && l < keep && mine_v > kEmpty;
       double v = -INFINITY;
-      if (active && l < keep) {
+      if (real) {
         const double x1 = row[mine];
         v = SIG ? sigmoid_scaled(x1, 0.0) + (bias ? (double)bias[mine] : 0.0) : x1;
       }
       int rank = 0;
       bool near = false;
       rank_candidates<1>(v, mine, rank, near);
-      if constexpr (!SIG) odd |= near && active && l < keep;  // logits whose scores may be equal in 64 bits
-      if (active && l < keep) cand[rank] = mine;
-      if (active && l < keep) mine = min(cand[l], p.E - 1);
+      if constexpr (!SIG) odd |= near && real;  // logits whose scores may be equal in 64 bits
+      if (real) cand[rank] = mine;
+      if (real) mine = min(cand[l], p.E - 1);
     }
     // slot l of the lanes' token, and its weight
     const bool slot = l < p.k && local < ntok;

@@ -139,3 +139,35 @@ def test_softmax_gradient_beside_barred_experts():
         ref, size, s = softmax_gradient(x, ids, g)
         assert (got[:, 7:30:3] == 0).all()
         assert_close("d", torch.from_numpy(got), ref, size * units(x) + s * np.abs(g).sum(1, keepdims=True) * 2.0 ** -48)
+
+
+# ------------------------------------------------------------------ places without an expert
+@pytest.mark.parametrize("each", range(2, 17))
+@pytest.mark.parametrize("sigmoid", [True, False], ids=["sigmoid", "softmax"])
+def test_every_expert_of_one_group_in_sixteen(each, sigmoid):
+    """As many choices as the group that stays has experts, some of them too close for fp32: nothing else may come between."""
+    for T in (3, 400):
+        x = draw(T, 16 * each, each)
+        x[::2] = np.round(x[::2] * 4) / 4
+        for k in {each, max(1, each - 1)}:
+            got = check_route(x, k, sigmoid, True, groups=16, keep=1, best=2)
+            assert (got["ids"] // each == got["ids"][:, :1] // each).all()
+            check_route(x, k, sigmoid, False, bias=np.full(16 * each, 0.25, np.float32), groups=16, keep=1, best=1)
+
+
+@pytest.mark.parametrize("groups,more", [(16, 9), (8, 3), (8, 11), (4, 1), (4, 7), (2, 1)])
+@pytest.mark.parametrize("sigmoid", [True, False], ids=["sigmoid", "softmax"])
+def test_barred_experts_behind_the_last_choice(groups, more, sigmoid):
+    """256 experts, sixteen a lane.  Of one group the last two of each sixteen can be chosen, but of one sixteen `more` others;
+    its last two, barred by their logits, have the largest bias.  All that there are are chosen, and all but one."""
+    rng = np.random.default_rng(groups + more)
+    lanes = 16 // groups
+    for at in range(lanes):
+        x, bias = np.full((200, 256), -np.inf, np.float32), np.zeros(256, np.float32)
+        can = [16 * lane + r for lane in range(lanes) for r in ((14, 15) if lane != at else range(more))]
+        x[:, can] = (0.5 + rng.standard_normal((200, len(can))) / 512).astype(np.float32)   # too close for fp32, but unlike
+        bias[[16 * at + 14, 16 * at + 15]] = 2
+        for k in (len(can), len(can) - 1):
+            got = check_route(x, k, sigmoid, True, bias=bias, groups=groups, keep=1, best=2)
+            assert np.isin(got["ids"], can).all()
+            check_route(x, k, sigmoid, True, groups=groups, keep=1, best=2)
