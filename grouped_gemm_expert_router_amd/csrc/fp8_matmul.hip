@@ -347,8 +347,8 @@ __device__ __forceinline__ const T* uniform_ptr(const T* p) {
 //
 // Waves that have their fragments run at a higher priority (s_setprio) until their matrix instructions are out, so
 // that those of a compute unit take turns between LDS and the matrix cores (1023x7168x4096 42.4 -> 41.0 us, with
-// fp32 C 66.9 -> 64.3, 7168x4096x21808 with fp32 C 1335 -> 1263, all on one card; on others the last now takes 1330 to
-// 1360).  Counters at 4096x4096x7168: matrix cores busy 50 % of the time (21804x4096x7168 47 %, fp32 C 45 %), vector ALU
+// fp32 C 66.9 -> 64.3, 7168x4096x21808 with fp32 C 1335 -> 1263, all on one card; on others the last takes 1330 to
+// 1380).  Counters at 4096x4096x7168: matrix cores busy 50 % of the time (21804x4096x7168 47 %, fp32 C 45 %), vector ALU
 // (promotion, addresses) 39 %, LDS without conflicts; the rest is the barrier each step and the fragments that every
 // wave reads behind it.  A second barrier inside the step, to send B's next block earlier,
 // gave nothing.

@@ -451,8 +451,8 @@ int moe_fp8_quantize(const void* src, int32_t src_dtype, int64_t rows, int64_t c
  * adds them: 1.5e-5 of the result's norm on normal data, and at most 7 * 2^-13 of the sum of all terms'
  * magnitudes, which is more than C's own rounding where terms cancel (an fp32 C keeps them).  The product of two
  * scales that meet has to be a normal fp32 number, and A's scale times a block's sum finite.  Sums run in a fixed
- * order (bitwise reproducible), which M, N, K, b_form and c_dtype decide.  lda, ldb, ldc: codes or values from one row to the next; what lies between two rows is
- * not touched.
+ * order (bitwise reproducible), which M, N, K, b_form and c_dtype decide.  lda, ldb, ldc: codes or values
+ * from one row to the next; what lies between two rows is not touched.
  * M of any size, 0 .. 2^30; N and K positive multiples of 16 up to 2^24, M * N < 2^36; lda, ldb
  * multiples of 16, ldc of 8, at least the row's length; lda and ldb at most 2^28, ldc 2^31.  ws:
  * moe_fp8_matmul_workspace_bytes (256-byte aligned; may be NULL where that is 0).  A, B, C and C_in 16-byte aligned. */
